@@ -344,6 +344,85 @@ int kda_cp_correct(const float *u, const float *s_start, const int32_t *cu_seg, 
                    int32_t d, float *out, void *stream);
 
 /*
+ * kda_linear_prefill -- varlen prefill of linear attention with one decay per head.
+ *
+ *     S_t = exp(g_t) S_(t-1) + k_t v_t^T,     o_t = scale S_t^T q_t     (the read includes token t)
+ *
+ * A head without the delta rule and with a scalar retention in place of KDA's channel-wise one; the
+ * states have kda_prefill's layout, so that kda_state_copy moves them too.
+ *
+ *   q                 [total_tokens, H, d_k]; k [total_tokens, n_kv_heads, d_k]; v [total_tokens,
+ *                     n_kv_heads, d_v]; `dtype`.  Query head h reads key/value head
+ *                     h / (H / n_kv_heads); every query head has a state of its own.
+ *   g                 fp32 log decays: [total_tokens, H] if g_per_token, else [H].  g <= 0; -inf
+ *                     forgets everything before the token.  Products of decays are formed as
+ *                     products, never as quotients, so any such g is safe.
+ *   cu_seqlens, n_seqs, total_tokens, init_state, final_state   as for kda_prefill (init_state may
+ *                     be final_state).  An empty sequence's final state is its initial one.
+ *   out               [total_tokens, H, d_v] `out_dtype`; must not alias an input.
+ *   workspace         device scratch of workspace_bytes >= kda_linear_prefill_workspace(...) bytes,
+ *                     NULL if that is 0.  Calls in flight on different streams need one each.
+ * Head sizes: multiples of 8 from 8 to 256.
+ * States, sums and decays are fp32; outputs are rounded once.  A NaN or infinity in an input of a
+ * sequence leaves the other sequences as they are; within its own it may also reach outputs up to
+ * 127 tokens before it.
+ * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_MISALIGNED, KDA_ERR_CUDA.
+ */
+int kda_linear_prefill(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                       const int32_t *cu_seqlens, int32_t n_seqs, int64_t total_tokens, int32_t n_heads,
+                       int32_t n_kv_heads, int32_t d_k, int32_t d_v, float scale, int32_t dtype,
+                       int32_t out_dtype, const float *init_state, void *out, float *final_state,
+                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace kda_linear_prefill needs for these sizes (0: none), or -1 for invalid ones.
+ * Host-only. */
+int64_t kda_linear_prefill_workspace(int32_t n_seqs, int64_t total_tokens, int32_t n_heads, int32_t d_k,
+                                     int32_t d_v, int32_t dtype);
+
+/*
+ * kda_linear_decode -- kda_linear_prefill's recurrence for one new token per sequence, state
+ * updated in place.
+ *   q [n_seqs, H, d_k], k [n_seqs, n_kv_heads, d_k], v [n_seqs, n_kv_heads, d_v] (`dtype`);
+ *   g fp32 [n_seqs, H] if g_per_token, else [H];  state fp32 [n_seqs, H, d_k, d_v];
+ *   out [n_seqs, H, d_v] `out_dtype`.  Head sizes, errors: as for kda_linear_prefill.
+ */
+int kda_linear_decode(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                      float *state, void *out, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads,
+                      int32_t d_k, int32_t d_v, float scale, int32_t dtype, int32_t out_dtype, void *stream);
+
+/*
+ * kda_norm_gate -- the norm over a head's channels on the mixer's output, with its gate:
+ *     out = o rsqrt(mean(o^2) + eps) w sigmoid(z)          per (token, head), mean over d channels
+ *   o, z, out   [tokens, H, d], dtypes o_dtype, z_dtype, out_dtype.  out may be o or z of its own type.
+ *   w           fp32 [d] (w_heads = 1, shared by the heads) or [H, d] (w_heads = H).
+ *   d           a multiple of 8 up to 256.  eps > 0.
+ * The sum of squares is fp32 and the result is rounded once.
+ * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE (d), KDA_ERR_MISALIGNED, KDA_ERR_CUDA.
+ */
+int kda_norm_gate(const void *o, int32_t o_dtype, const void *z, int32_t z_dtype, const float *w,
+                  int32_t w_heads, void *out, int32_t out_dtype, int64_t tokens, int32_t n_heads, int32_t d,
+                  float eps, void *stream);
+
+/*
+ * kda_residual_norm -- the residual add between two blocks, with the norm after the first (on its
+ * output y), its gate and residual scale, and the norm before the second:
+ *     u = y                                        or, with w_post,  y rsqrt(mean(y^2) + eps) w_post
+ *     r = x + scale u                              or, with z,       x + scale u sigmoid(z)
+ *     out = r rsqrt(mean(r^2) + eps) w
+ *   x, res      [tokens, width] `res_dtype`: the residual stream before and after.  res may be x.
+ *   y, z, out   [tokens, width] `dtype`.  out may be y or z.
+ *   w_post, w   fp32 [width].
+ *   y           NULL: no add, out = x rsqrt(mean(x^2) + eps) w (then z, w_post and res are NULL too).
+ *   width       any; rows of whole 16-byte units (a multiple of 8 channels) up to 16384 channels
+ *               are read once, other widths three times, channel by channel.
+ * Sums of squares and r are fp32; the second norm takes r before it is rounded into res.
+ * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_MISALIGNED, KDA_ERR_CUDA.
+ */
+int kda_residual_norm(const void *x, int32_t res_dtype, const void *y, const void *z, int32_t dtype,
+                      const float *w_post, const float *w, float scale, float eps, void *res, void *out,
+                      int64_t tokens, int32_t width, void *stream);
+
+/*
  * kda_device_status -- synchronize `stream`, then read and clear the current device's sticky
  * error word (KDA_OK if no device-side error was recorded since the last read).  *status
  * receives the recorded kda_status.  Returns KDA_OK, or KDA_ERR_CUDA if the read failed.

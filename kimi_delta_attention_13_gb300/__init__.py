@@ -22,7 +22,7 @@ from ._lib import KDAError
 
 __all__ = ["prefill", "prefill_recurrent", "decode", "state_copy", "device_status", "prefill_path",
            "num_checkpoints", "KDAError", "load", "diag_device_timeout", "premix", "output_gate",
-           "prefill_staged"]
+           "prefill_staged", "linear_prefill", "linear_decode", "norm_gate", "residual_norm"]
 
 _DTYPES = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
 
@@ -40,6 +40,17 @@ def _stream(device: torch.device, stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_stream(device: torch.device, stream):
+    """A context in which torch allocates for `stream` (None: the current one)."""
+    import contextlib
+
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 def _require(t: torch.Tensor, name: str, device, dtype=None, shape=None):
@@ -227,6 +238,162 @@ def output_gate(o, z, *, out=None, out_dtype=None, stream=None):
                              _DTYPES[out.dtype], o.numel(), _stream(dev, stream))
     _lib.check(rc, "kda_output_gate")
     return out
+
+
+def _linear_inputs(q, k, v, g, name):
+    """Checks shared by linear_prefill and linear_decode; returns (rows, H, H_kv, d_k, d_v, per_token)."""
+    dev, dtype = q.device, q.dtype
+    if dtype not in _DTYPES:
+        raise ValueError("q/k/v must be bfloat16 or float32")
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q, k and v must be [{name}, heads, d]")
+    rows, H, dk = q.shape
+    Hkv, dv = k.shape[1], v.shape[2]
+    if Hkv < 1 or H % Hkv != 0:
+        raise ValueError(f"k has {Hkv} heads, which {H} query heads cannot share evenly")
+    _require(q, "q", dev, dtype)
+    _require(k, "k", dev, dtype, (rows, Hkv, dk))
+    _require(v, "v", dev, dtype, (rows, Hkv, dv))
+    per_token = g.dim() == 2
+    _require(g, "g", dev, torch.float32, (rows, H) if per_token else (H,))
+    return rows, H, Hkv, dk, dv, per_token
+
+
+def _out_like(out, out_dtype, dtype, dev, shape):
+    """`out` checked, or a new tensor of `out_dtype` (default: the inputs' type)."""
+    if out is None:
+        out = torch.empty(shape, device=dev, dtype=out_dtype or dtype)
+    else:
+        _require(out, "out", dev, out_dtype, shape)
+    if out.dtype not in _DTYPES:
+        raise ValueError("out must be bfloat16 or float32")
+    return out
+
+
+def linear_prefill(q, k, v, g, cu_seqlens=None, init_state=None, *, scale: float = 1.0, out=None,
+                   final_state=True, workspace=None, out_dtype=None, stream=None):
+    """Varlen prefill of linear attention with one decay per head (kda_linear_prefill):
+    S_t = exp(g_t) S_(t-1) + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q: [T, H, d_k]; k: [T, H_kv, d_k]; v: [T, H_kv, d_v] (bf16 or fp32, contiguous, CUDA; H a
+    multiple of H_kv); g: fp32 log decays <= 0 (-inf forgets), [T, H] per token or [H] constant;
+    cu_seqlens: int32 [N+1] on the device or None for one sequence; init_state: fp32
+    [N, H, d_k, d_v] or None (zeros).  final_state: True to allocate, a tensor to fill (init_state
+    itself for an in-place resume), or None/False.  out_dtype defaults to q's.  workspace: a uint8
+    tensor to reuse across calls of one stream, else one is allocated where the sizes need it.
+    Returns (out, final_state)."""
+    lib = _lib.load()
+    dev, dtype = q.device, q.dtype
+    T, H, Hkv, dk, dv, per_token = _linear_inputs(q, k, v, g, "T")
+    if cu_seqlens is None:
+        n = 1
+    else:
+        _require(cu_seqlens, "cu_seqlens", dev, torch.int32)
+        n = cu_seqlens.numel() - 1
+    shape = (n, H, dk, dv)
+    if init_state is not None:
+        _require(init_state, "init_state", dev, torch.float32, shape)
+    out = _out_like(out, out_dtype, dtype, dev, (T, H, dv))
+    if final_state is True:
+        final_state = torch.empty(shape, device=dev, dtype=torch.float32)
+    elif final_state is False or final_state is None:
+        final_state = None
+    else:
+        _require(final_state, "final_state", dev, torch.float32, shape)
+    need = lib.kda_linear_prefill_workspace(n, T, H, dk, dv, _DTYPES[dtype])
+    if workspace is not None:
+        _require(workspace, "workspace", dev, torch.uint8)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} needed")
+    elif need > 0:
+        # taken from the pool of the stream the kernels run on, so that its reuse waits for them
+        with _on_stream(dev, stream):
+            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    rc = lib.kda_linear_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(cu_seqlens), n, T, H,
+                                Hkv, dk, dv, float(scale), _DTYPES[dtype], _DTYPES[out.dtype],
+                                _ptr(init_state), _ptr(out), _ptr(final_state), _ptr(workspace),
+                                0 if workspace is None else workspace.numel(), _stream(dev, stream))
+    _lib.check(rc, "kda_linear_prefill")
+    return out, final_state
+
+
+def linear_decode(q, k, v, g, state, *, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """linear_prefill's recurrence for one token per sequence (kda_linear_decode): state
+    [N, H, d_k, d_v] fp32 is updated in place.  q: [N, H, d_k]; k: [N, H_kv, d_k]; v: [N, H_kv, d_v];
+    g: fp32 [N, H] or [H].  Returns out [N, H, d_v] (out_dtype, default q's)."""
+    lib = _lib.load()
+    dev, dtype = q.device, q.dtype
+    N, H, Hkv, dk, dv, per_token = _linear_inputs(q, k, v, g, "N")
+    _require(state, "state", dev, torch.float32, (N, H, dk, dv))
+    out = _out_like(out, out_dtype, dtype, dev, (N, H, dv))
+    rc = lib.kda_linear_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(state), _ptr(out), N, H,
+                               Hkv, dk, dv, float(scale), _DTYPES[dtype], _DTYPES[out.dtype],
+                               _stream(dev, stream))
+    _lib.check(rc, "kda_linear_decode")
+    return out
+
+
+def norm_gate(o, z, w, *, eps: float = 1e-6, out=None, out_dtype=None, stream=None):
+    """Norm over a head's channels with the output gate (kda_norm_gate):
+    out = o * rsqrt(mean(o^2) + eps) * w * sigmoid(z).
+
+    o, z: [T, H, d] (bf16 or fp32 each); w: fp32 [d] or [H, d].  out: a tensor to fill (o or z
+    itself for an in-place call), else a new one of out_dtype (default z's)."""
+    lib = _lib.load()
+    dev = o.device
+    _require(o, "o", dev)
+    if o.dim() != 3 or o.dtype not in _DTYPES or z.dtype not in _DTYPES:
+        raise ValueError("o and z must be [T, H, d] of bfloat16 or float32")
+    T, H, d = o.shape
+    _require(z, "z", dev, shape=o.shape)
+    _require(w, "w", dev, torch.float32, (H, d) if w.dim() == 2 else (d,))
+    out = _out_like(out, out_dtype, z.dtype, dev, o.shape)
+    rc = lib.kda_norm_gate(_ptr(o), _DTYPES[o.dtype], _ptr(z), _DTYPES[z.dtype], _ptr(w),
+                           H if w.dim() == 2 else 1, _ptr(out), _DTYPES[out.dtype], T, H, d, float(eps),
+                           _stream(dev, stream))
+    _lib.check(rc, "kda_norm_gate")
+    return out
+
+
+def residual_norm(x, y, w, *, w_post=None, z=None, scale: float = 1.0, eps: float = 1e-6, res=None,
+                  out=None, out_dtype=None, stream=None):
+    """The residual add between two blocks with the norms around it (kda_residual_norm):
+    u = y (or norm(y) * w_post), u *= sigmoid(z) if z is given, res = x + scale * u,
+    out = norm(res) * w.
+
+    x: [T, D] (bf16 or fp32), the residual stream; y, z: [T, D] of one type, the block's output and
+    its gate; w_post, w: fp32 [D].  res: a tensor to fill (x itself for an in-place add), else new;
+    out: of y's type, new unless passed.  y None: only out = norm(x) * w, of out_dtype (default
+    x's).  Returns (res, out); res is x where y is None."""
+    lib = _lib.load()
+    dev = x.device
+    _require(x, "x", dev)
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError("x must be [T, D] of bfloat16 or float32")
+    T, D = x.shape
+    _require(w, "w", dev, torch.float32, (D,))
+    if y is None:
+        if z is not None or w_post is not None or res is not None:
+            raise ValueError("z, w_post and res belong to an add: pass y")
+        out = _out_like(out, out_dtype, x.dtype, dev, (T, D))
+    else:
+        if y.dtype not in _DTYPES or (out_dtype is not None and out_dtype != y.dtype):
+            raise ValueError("y must be bfloat16 or float32, and out of its type")
+        _require(y, "y", dev, shape=(T, D))
+        if z is not None:
+            _require(z, "z", dev, y.dtype, (T, D))
+        if w_post is not None:
+            _require(w_post, "w_post", dev, torch.float32, (D,))
+        if res is None:
+            res = torch.empty_like(x)
+        else:
+            _require(res, "res", dev, x.dtype, (T, D))
+        out = _out_like(out, y.dtype, y.dtype, dev, (T, D))
+    rc = lib.kda_residual_norm(_ptr(x), _DTYPES[x.dtype], _ptr(y), _ptr(z), _DTYPES[out.dtype],
+                               _ptr(w_post), _ptr(w), float(scale), float(eps), _ptr(res), _ptr(out), T, D,
+                               _stream(dev, stream))
+    _lib.check(rc, "kda_residual_norm")
+    return (x if y is None else res), out
 
 
 def prefill_staged(h_q, h_k, h_v, h_g, h_beta, h_cu_seqlens=None, init_state=None, *,

@@ -40,6 +40,15 @@ SIGNATURES = {
     "kda_output_gate": (ctypes.c_int, [_vp, _i32, _vp, _i32, _vp, _i32, _i64, _vp]),
     "kda_cp_combine": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
     "kda_cp_correct": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _vp, _vp]),
+    "kda_linear_prefill": (ctypes.c_int, [_vp] * 4 + [_i32, _vp, _i32, _i64, _i32, _i32, _i32, _i32,
+                                           ctypes.c_float, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "kda_linear_prefill_workspace": (ctypes.c_int64, [_i32, _i64, _i32, _i32, _i32, _i32]),
+    "kda_linear_decode": (ctypes.c_int, [_vp] * 4 + [_i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                          ctypes.c_float, _i32, _i32, _vp]),
+    "kda_norm_gate": (ctypes.c_int, [_vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i64, _i32, _i32,
+                                      ctypes.c_float, _vp]),
+    "kda_residual_norm": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, ctypes.c_float,
+                                          ctypes.c_float, _vp, _vp, _i64, _i32, _vp]),
     "kda_prefill_staged": (ctypes.c_int, [_vp] * 6 + [_i32, _i64, _i32, _i32, _i32, _vp] + [_vp] * 9
                            + [_i64, _i64, _vp]),
     "kda_prefill_staged_scratch": (ctypes.c_int64, [_vp, _i32, _i64, _i64]),

@@ -1,5 +1,6 @@
 // kda_capi.cu -- the C ABI of libkda_gb300: host-side argument validation and kernel dispatch.
 // Declarations, argument meaning, layouts and error behaviour: include/kda.h.
+#include <cmath>
 #include <cstdio>
 
 #include <nvtx3/nvToolsExt.h>
@@ -87,6 +88,12 @@ int check_staged(const void *h_q, const void *h_k, const void *h_v, const void *
 bool tc_supported(int32_t d_k, int32_t d_v, int32_t dtype)
 {
     return dtype == KDA_BF16 && d_k == 128 && d_v == 128;
+}
+
+// Head sizes of the linear-attention calls: rows are whole 16-byte units in every type.
+bool bad_linear_dims(int32_t d_k, int32_t d_v)
+{
+    return d_k < 8 || d_k > 256 || d_k % 8 != 0 || d_v < 8 || d_v > 256 || d_v % 8 != 0;
 }
 
 }  // namespace
@@ -281,6 +288,100 @@ int kda_cp_correct(const float *u, const float *s_start, const int32_t *cu_seg, 
     if (out && (out == u || reinterpret_cast<const void *>(out) == s_start)) return KDA_ERR_INVALID_ARG;
     return launch_cp_correct(u, s_start, cu_seg, n_seg, skip_seg, n_skip, n_heads, (long long)total_tokens,
                              out, (cudaStream_t)stream);
+}
+
+int64_t kda_linear_prefill_workspace(int32_t n_seqs, int64_t total_tokens, int32_t n_heads, int32_t d_k,
+                                     int32_t d_v, int32_t dtype)
+{
+    if (n_seqs < 0 || total_tokens < 0 || total_tokens > 0x7fffffffLL || n_heads < 1 || bad_dtype(dtype) ||
+        bad_linear_dims(d_k, d_v))
+        return -1;
+    return linear_workspace_bytes(n_seqs, total_tokens, n_heads, d_k, d_v, dtype);
+}
+
+int kda_linear_prefill(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                       const int32_t *cu_seqlens, int32_t n_seqs, int64_t total_tokens, int32_t n_heads,
+                       int32_t n_kv_heads, int32_t d_k, int32_t d_v, float scale, int32_t dtype,
+                       int32_t out_dtype, const float *init_state, void *out, float *final_state,
+                       void *workspace, int64_t workspace_bytes, void *stream)
+{
+    const CallRange range("kda_linear_prefill");
+    if (n_seqs < 0 || total_tokens < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 ||
+        d_k < 1 || d_v < 1 || bad_dtype(dtype) || bad_dtype(out_dtype) || !std::isfinite(scale))
+        return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!q || !k || !v || !g || !out)) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && n_seqs == 0) return KDA_ERR_INVALID_ARG;
+    if (!cu_seqlens && n_seqs > 1) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;   // cu_seqlens are int32
+    if (bad_linear_dims(d_k, d_v)) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const void *ptrs[] = {q, k, v, g, init_state, out, final_state, workspace};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return KDA_ERR_MISALIGNED;
+    if (out && (out == q || out == k || out == v || out == g)) return KDA_ERR_INVALID_ARG;
+    const int64_t need = linear_workspace_bytes(n_seqs, total_tokens, n_heads, d_k, d_v, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
+    return launch_linear_prefill(q, k, v, g, g_per_token != 0, cu_seqlens, n_seqs, total_tokens, n_heads,
+                                 n_kv_heads, d_k, d_v, scale, dtype, out_dtype, init_state, out, final_state,
+                                 workspace, (cudaStream_t)stream);
+}
+
+int kda_linear_decode(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                      float *state, void *out, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads,
+                      int32_t d_k, int32_t d_v, float scale, int32_t dtype, int32_t out_dtype, void *stream)
+{
+    const CallRange range("kda_linear_decode");
+    if (n_seqs < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 || d_k < 1 || d_v < 1 ||
+        bad_dtype(dtype) || bad_dtype(out_dtype) || !std::isfinite(scale))
+        return KDA_ERR_INVALID_ARG;
+    if (n_seqs > 0 && (!q || !k || !v || !g || !state || !out)) return KDA_ERR_INVALID_ARG;
+    if (bad_linear_dims(d_k, d_v)) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const void *ptrs[] = {q, k, v, g, state, out};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    if (out && (out == q || out == k || out == v || out == g || out == state)) return KDA_ERR_INVALID_ARG;
+    return launch_linear_decode(q, k, v, g, g_per_token != 0, state, out, n_seqs, n_heads, n_kv_heads, d_k,
+                                d_v, scale, dtype, out_dtype, (cudaStream_t)stream);
+}
+
+int kda_norm_gate(const void *o, int32_t o_dtype, const void *z, int32_t z_dtype, const float *w,
+                  int32_t w_heads, void *out, int32_t out_dtype, int64_t tokens, int32_t n_heads, int32_t d,
+                  float eps, void *stream)
+{
+    const CallRange range("kda_norm_gate");
+    if (tokens < 0 || n_heads < 1 || d < 1 || (w_heads != 1 && w_heads != n_heads) || bad_dtype(o_dtype) ||
+        bad_dtype(z_dtype) || bad_dtype(out_dtype) || !(eps > 0.f) || !std::isfinite(eps))
+        return KDA_ERR_INVALID_ARG;
+    if (tokens > 0 && (!o || !z || !w || !out)) return KDA_ERR_INVALID_ARG;
+    if (d % 8 != 0 || d > 256) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const void *ptrs[] = {o, z, w, out};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    // in place over o or z is fine (same element type: each element is read before it is written)
+    if (out && ((out == o && out_dtype != o_dtype) || (out == z && out_dtype != z_dtype) || out == w))
+        return KDA_ERR_INVALID_ARG;
+    return launch_norm_gate(o, o_dtype, z, z_dtype, w, w_heads, out, out_dtype, tokens, n_heads, d, eps,
+                            (cudaStream_t)stream);
+}
+
+int kda_residual_norm(const void *x, int32_t res_dtype, const void *y, const void *z, int32_t dtype,
+                      const float *w_post, const float *w, float scale, float eps, void *res, void *out,
+                      int64_t tokens, int32_t width, void *stream)
+{
+    const CallRange range("kda_residual_norm");
+    if (tokens < 0 || width < 1 || bad_dtype(res_dtype) || bad_dtype(dtype) || !std::isfinite(scale) ||
+        !(eps > 0.f) || !std::isfinite(eps))
+        return KDA_ERR_INVALID_ARG;
+    if (tokens > 0 && (!x || !w || !out || (y && !res))) return KDA_ERR_INVALID_ARG;
+    if (!y && (z || w_post || res)) return KDA_ERR_INVALID_ARG;   // parts of an add that is not there
+    const void *ptrs[] = {x, y, z, w_post, w, res, out};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    // res may be x (in place), or y of the same element type; out may be y or z
+    if (out && (out == x || out == res || out == w || out == w_post)) return KDA_ERR_INVALID_ARG;
+    if (res && (res == z || (res == y && res_dtype != dtype))) return KDA_ERR_INVALID_ARG;
+    return launch_residual_norm(x, res_dtype, y, z, dtype, w_post, w, scale, eps, res, out, tokens, width,
+                                (cudaStream_t)stream);
 }
 
 int64_t kda_prefill_staged_scratch(const int32_t *h_cu_seqlens, int32_t n_seqs, int64_t total_tokens,

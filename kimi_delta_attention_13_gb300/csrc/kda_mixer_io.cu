@@ -29,38 +29,6 @@ constexpr int kMixTokens = 256;    // tokens per pre-mixer block (fewer block st
 template <typename T>
 constexpr int mix_depth() { return sizeof(T) == 2 ? 8 : 4; }
 
-// 8 consecutive elements <-> 8 floats (16-byte bf16 vector, or two 16-byte fp32 vectors)
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
-{
-    const uint4 r = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void load8(const float *p, float (&v)[8])
-{
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
-{
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float *p, const float (&v)[8])
-{
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-
 // 8 elements as loaded (packed bf16 stays packed until used): the prefetch ring's entries,
 // unpacked as 4 channel pairs
 template <typename T>
@@ -113,6 +81,7 @@ __device__ __forceinline__ float2 pair_mul(float2 a, float2 b)
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
     return v;
 }
+using kda::store8;   // the overloads for 8 floats, beside those for 4 pairs
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float2 (&v)[4])
 {
     uint32_t w[4];

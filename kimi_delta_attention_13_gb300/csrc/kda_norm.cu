@@ -1,0 +1,266 @@
+// kda_norm.cu -- the norms around a mixer: the gated head norm on its output, and the residual add
+// between two blocks with the norm after the first and the norm before the second.
+//
+//   norm_gate:      out = o rsqrt(mean(o^2) + eps) w sigmoid(z)            over a head's d channels
+//   residual_norm:  u = y, or y rsqrt(mean(y^2) + eps) w_post;  u = u sigmoid(z) if z is given
+//                   r = x + scale u;   out = r rsqrt(mean(r^2) + eps) w    over a row's D channels
+//
+// Both stream HBM once: a row stays in registers between its sum of squares and its use, in 32
+// bits, and each output is rounded once (the norm of r is taken before r is rounded).
+#include <type_traits>
+
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace {
+
+// Results rounded to bf16 take the fast exponential and division (relative error about 2^-21); fp32
+// results the full ones.
+template <typename TO>
+__device__ __forceinline__ float gate(float z)
+{
+    if constexpr (sizeof(TO) == 2) return __fdividef(1.f, 1.f + __expf(-z));
+    else return 1.f / (1.f + expf(-z));
+}
+
+__device__ __forceinline__ float warp_sum(float x)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// ---------------------------------------------------------------------------------------------
+// norm_gate: GROUP lanes of a warp hold one (token, head) row, 8 channels each
+
+template <typename TX, typename TZ, typename TO, int GROUP>
+__global__ void __launch_bounds__(256) norm_gate_kernel(const TX *o, const TZ *z,
+                                                        const float *__restrict__ w, TO *out, long long rows,
+                                                        int H, int w_heads, int d, float eps)
+{
+    constexpr int PER = 256 / GROUP;   // rows of a block at a time
+    const int lane = threadIdx.x % GROUP;
+    const bool ok = 8 * lane < d;
+    const float inv_d = 1.f / (float)d;
+    for (long long r = (long long)blockIdx.x * PER + threadIdx.x / GROUP; r - threadIdx.x / GROUP < rows;
+         r += (long long)gridDim.x * PER) {
+        const bool live = ok && r < rows;
+        const long long at = r * d + 8 * lane;
+        float x[8] = {}, g[8] = {};
+        if (live) {
+            load8(o + at, x);
+            load8(z + at, g);
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) ss = fmaf(x[c], x[c], ss);
+#pragma unroll
+        for (int m = GROUP / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        const float inv = rsqrtf(fmaf(ss, inv_d, eps));
+        if (live) {
+            float wv[8];
+            load8(w + (w_heads > 1 ? r % H * d : 0) + 8 * lane, wv);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] *= inv * wv[c] * gate<TO>(g[c]);
+            store8(out + at, x);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// residual_norm: one row per block of THREADS, VECS groups of 8 channels per thread
+
+struct ResidualArgs {
+    const void *x, *y, *z;       // [T, D]; y and z may be null
+    const float *w_post, *w;     // w_post may be null
+    void *res, *out;
+    long long rows;
+    int D;
+    float scale, eps;
+};
+
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float x, float *buf)
+{
+    x = warp_sum(x);
+    if constexpr (THREADS > 32) {
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) x += buf[i];
+    }
+    return x;
+}
+
+template <typename TR, typename TB, int THREADS, int VECS>
+__global__ void __launch_bounds__(THREADS) residual_norm_kernel(const ResidualArgs p)
+{
+    __shared__ float buf[2][32];
+    const long long row = blockIdx.x, base = row * p.D;
+    const TR *x = static_cast<const TR *>(p.x) + base;
+    const TB *y = p.y ? static_cast<const TB *>(p.y) + base : nullptr;
+    const TB *z = p.z ? static_cast<const TB *>(p.z) + base : nullptr;
+    float r[VECS][8], u[VECS][8], gz[VECS][8];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int c = (i * THREADS + threadIdx.x) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[i][e] = u[i][e] = gz[i][e] = 0.f;
+        if (c < p.D) {
+            if (y) load8(y + c, u[i]);
+            load8(x + c, r[i]);
+            if (z) load8(z + c, gz[i]);
+        }
+    }
+    if (y) {
+        float inv = p.scale;
+        if (p.w_post) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < VECS; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(u[i][e], u[i][e], ss);
+            inv = p.scale * rsqrtf(block_sum<THREADS>(ss, buf[0]) / (float)p.D + p.eps);
+        }
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            const int c = (i * THREADS + threadIdx.x) * 8;
+            if (c >= p.D) continue;
+            float wp[8];
+            if (p.w_post) load8(p.w_post + c, wp);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float t = u[i][e] * inv;
+                if (p.w_post) t *= wp[e];
+                if (z) t *= gate<TB>(gz[i][e]);
+                r[i][e] += t;
+            }
+            store8(static_cast<TR *>(p.res) + base + c, r[i]);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(r[i][e], r[i][e], ss);
+    const float inv = rsqrtf(block_sum<THREADS>(ss, buf[1]) / (float)p.D + p.eps);
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int c = (i * THREADS + threadIdx.x) * 8;
+        if (c >= p.D) continue;
+        float wv[8];
+        load8(p.w + c, wv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[i][e] *= inv * wv[e];
+        store8(static_cast<TB *>(p.out) + base + c, r[i]);
+    }
+}
+
+// Any width: scalar accesses, r computed once for its sum and once for its use.
+template <typename TR, typename TB>
+__global__ void __launch_bounds__(256) residual_norm_any_kernel(const ResidualArgs p)
+{
+    __shared__ float buf[2][32];
+    const long long base = (long long)blockIdx.x * p.D;
+    const TR *x = static_cast<const TR *>(p.x) + base;
+    const TB *y = p.y ? static_cast<const TB *>(p.y) + base : nullptr;
+    const TB *z = p.z ? static_cast<const TB *>(p.z) + base : nullptr;
+    float inv_post = p.scale;
+    if (y && p.w_post) {
+        float ss = 0.f;
+        for (int c = threadIdx.x; c < p.D; c += 256) {
+            const float t = to_f32(y[c]);
+            ss = fmaf(t, t, ss);
+        }
+        inv_post = p.scale * rsqrtf(block_sum<256>(ss, buf[0]) / (float)p.D + p.eps);
+    }
+    auto value = [&](int c) {
+        float r = to_f32(x[c]);
+        if (y) {
+            float t = to_f32(y[c]) * inv_post;
+            if (p.w_post) t *= p.w_post[c];
+            if (z) t *= gate<TB>(to_f32(z[c]));
+            r += t;
+        }
+        return r;
+    };
+    float ss = 0.f;
+    for (int c = threadIdx.x; c < p.D; c += 256) {
+        const float r = value(c);
+        ss = fmaf(r, r, ss);
+    }
+    const float inv = rsqrtf(block_sum<256>(ss, buf[1]) / (float)p.D + p.eps);
+    for (int c = threadIdx.x; c < p.D; c += 256) {   // res may be x: a channel is read before it is written
+        const float r = value(c);
+        if (y) store_as(static_cast<TR *>(p.res) + base + c, r);
+        store_as(static_cast<TB *>(p.out) + base + c, r * inv * p.w[c]);
+    }
+}
+
+template <typename TR, typename TB>
+void launch_residual(const ResidualArgs &p, cudaStream_t stream)
+{
+    const unsigned rows = (unsigned)p.rows;
+    if (p.D % 8 != 0 || p.D > 16384) {
+        residual_norm_any_kernel<TR, TB><<<rows, 256, 0, stream>>>(p);
+        return;
+    }
+    const int vecs = p.D / 8;
+    if (vecs <= 128) residual_norm_kernel<TR, TB, 128, 1><<<rows, 128, 0, stream>>>(p);
+    else if (vecs <= 256) residual_norm_kernel<TR, TB, 256, 1><<<rows, 256, 0, stream>>>(p);
+    else if (vecs <= 512) residual_norm_kernel<TR, TB, 512, 1><<<rows, 512, 0, stream>>>(p);
+    else if (vecs <= 1024) residual_norm_kernel<TR, TB, 512, 2><<<rows, 512, 0, stream>>>(p);
+    else if (vecs <= 1536) residual_norm_kernel<TR, TB, 512, 3><<<rows, 512, 0, stream>>>(p);
+    else residual_norm_kernel<TR, TB, 512, 4><<<rows, 512, 0, stream>>>(p);
+}
+
+}  // namespace
+
+int launch_norm_gate(const void *o, int o_dtype, const void *z, int z_dtype, const float *w, int w_heads,
+                     void *out, int out_dtype, int64_t T, int H, int d, float eps, cudaStream_t stream)
+{
+    const long long rows = T * H;
+    if (rows == 0) return KDA_OK;
+    auto go = [&](auto xt, auto zt, auto ot) {
+        using X = decltype(xt);
+        using Z = decltype(zt);
+        using O = decltype(ot);
+        auto launch = [&](auto group) {
+            constexpr int G = decltype(group)::value;
+            const long long want = (rows + 256 / G - 1) / (256 / G), cap = 152 * 8;
+            norm_gate_kernel<X, Z, O, G><<<(unsigned)(want < cap ? want : cap), 256, 0, stream>>>(
+                (const X *)o, (const Z *)z, w, (O *)out, rows, H, w_heads, d, eps);
+        };
+        if (d <= 64) launch(std::integral_constant<int, 8>{});
+        else if (d <= 128) launch(std::integral_constant<int, 16>{});
+        else launch(std::integral_constant<int, 32>{});
+    };
+    auto with_z = [&](auto xt, auto zt) {
+        if (out_dtype == KDA_BF16) go(xt, zt, __nv_bfloat16{}); else go(xt, zt, float{});
+    };
+    auto with_x = [&](auto xt) {
+        if (z_dtype == KDA_BF16) with_z(xt, __nv_bfloat16{}); else with_z(xt, float{});
+    };
+    if (o_dtype == KDA_BF16) with_x(__nv_bfloat16{}); else with_x(float{});
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int launch_residual_norm(const void *x, int res_dtype, const void *y, const void *z, int dtype,
+                         const float *w_post, const float *w, float scale, float eps, void *res, void *out,
+                         int64_t T, int D, cudaStream_t stream)
+{
+    if (T == 0) return KDA_OK;
+    if (T > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const ResidualArgs p = {x, y, z, w_post, w, res, out, T, D, scale, eps};
+    if (res_dtype == KDA_BF16) {
+        if (dtype == KDA_BF16) launch_residual<__nv_bfloat16, __nv_bfloat16>(p, stream);
+        else launch_residual<__nv_bfloat16, float>(p, stream);
+    } else {
+        if (dtype == KDA_BF16) launch_residual<float, __nv_bfloat16>(p, stream);
+        else launch_residual<float, float>(p, stream);
+    }
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace kda
