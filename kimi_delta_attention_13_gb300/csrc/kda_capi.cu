@@ -475,6 +475,10 @@ int kda_device_status(int32_t *status, void *stream)
     rc = read_and_clear_status_cp((cudaStream_t)stream, &cp);
     if (rc != KDA_OK) return rc;
     if (c == KDA_OK) c = cp;
+    int32_t lt = 0;
+    rc = read_and_clear_status_linear((cudaStream_t)stream, &lt);
+    if (rc != KDA_OK) return rc;
+    if (c == KDA_OK) c = lt;
     *status = b != KDA_OK ? b : (c != KDA_OK ? c : a);
     return KDA_OK;
 }

@@ -61,6 +61,7 @@ int read_and_clear_status_prefill_tc(cudaStream_t s, int32_t *status);
 int read_and_clear_status_prefill_tc_precise(cudaStream_t s, int32_t *status);
 int read_and_clear_status_decode(cudaStream_t s, int32_t *status);
 int read_and_clear_status_cp(cudaStream_t s, int32_t *status);
+int read_and_clear_status_linear(cudaStream_t s, int32_t *status);
 // Launch the one-CTA probe whose bounded device wait expires after `cycles` SM cycles.
 int launch_wait_timeout_probe(long long cycles, cudaStream_t stream);
 // Launch the one-thread run of the shared-memory bounds check on an out-of-window offset; read

@@ -193,8 +193,13 @@ int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream)
 // Segments are cut when the uncut sequences give the machine too few blocks.
 int plan_segments(int n_seqs, int64_t T, int H, int d_k, int d_v, int dtype)
 {
-    (void)d_k;
-    (void)dtype;
+    if (tc_path(d_k, d_v, dtype)) {
+        const int64_t ctas = (int64_t)n_seqs * H;
+        if (ctas >= 76) return 0;
+        int64_t len = (T * H / 152 + 127) / 128 * 128;
+        if (len < 512) len = 512;
+        return T <= len ? 0 : (int)len;
+    }
     const int64_t slices = ceil_div(d_v, kCols), blocks = (int64_t)n_seqs * H * slices;
     const int64_t want = 152 * 4;
     if (blocks >= want) return 0;
@@ -238,6 +243,7 @@ int launch_linear_prefill(const void *q, const void *k, const void *v, const flo
     p.items = (int)items;
     p.starts = static_cast<float *>(workspace);
     p.decays = p.starts ? p.starts + items * H * d_k * d_v : nullptr;
+    if (lin::tc_path(d_k, d_v, dtype) && T > 0) return lin::run_tc_path(p, out_dtype, stream);
     return lin::run_token_path(p, dtype, out_dtype, stream);
 }
 

@@ -107,7 +107,10 @@ __device__ __forceinline__ Item find_item(const int32_t *cu, int n_seqs, long lo
 
 // join of the segments, after a state pass
 void launch_join(const Args &p, cudaStream_t stream);
+int run_tc_path(const Args &p, int out_dtype, cudaStream_t stream);   // bf16 operands
 int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream);
+// whether the tensor-core kernel takes these operands
+inline bool tc_path(int d_k, int d_v, int dtype) { return dtype == KDA_BF16 && d_k <= 128 && d_v <= 128; }
 // tokens of a segment for these sizes, 0 where the sequences are not cut
 int plan_segments(int n_seqs, int64_t T, int H, int d_k, int d_v, int dtype);
 

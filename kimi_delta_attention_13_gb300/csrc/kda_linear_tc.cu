@@ -1,0 +1,632 @@
+// kda_linear_tc.cu -- linear attention with one decay per head for bf16 operands: chunks of 128
+// tokens on the tensor cores.
+//
+//     S_t = exp(g_t) S_(t-1) + k_t v_t^T,     o_t = scale S_t^T q_t
+//
+// With a_t = exp(g_t) and a chunk that starts from state S (rows i, j = tokens of the chunk):
+//     o_i = scale ( p_i S^T q_i  +  sum_(j <= i) w_ij (q_i . k_j) v_j )
+//     S  <- (prod a) S  +  sum_j c_j k_j v_j^T
+//     p_i = prod_(l <= i) a_l,   w_ij = prod_(j < l <= i) a_l,   c_j = prod_(l > j) a_l
+// Four products a chunk, M = 128 each, accumulated in fp32 in TMEM:
+//     scores = Q K^T         A, B = q, k tiles in shared memory
+//     D2 = P V               A = P = w . scores (bf16, TMEM), B = v tile
+//     D1 = Q S               B = the state as bf16 (shared memory)
+//     Dst = K^T V~           B = V~ = c . v, exactly split in two bf16 parts (two passes)
+// The state itself stays in fp32 registers: S <- (prod a) S + Dst.  Its update must be good to fp32,
+// so V~ carries 16 bits; P and the state's copy are rounded to bf16 once each (their products make
+// the outputs, to which a bf16 rounding of the result is added anyway).
+//
+// Every weight is a product of decays over the very tokens it spans, never a quotient or a
+// difference of sums, so any decay in [0, 1] is exact to a few ulps: w_ij = (suffix of j's 32-token
+// block after j) x (whole blocks between) x (prefix of i's block up to i), and inside one block a
+// running product from the diagonal down.
+//
+// One CTA works through the chunks of one (segment, head).  Roles, joined by mbarriers:
+//   warps 0-7    output of a chunk (scale (p D1 + D2) -> global), then the state update: 64 (dv = 128)
+//                state columns of one key channel per thread, and the state's bf16 copy
+//   warps 8-11   scores -> P, one token row per thread
+//   warps 12-15  the chunk's decays; V~ high part over v in place (after P V), low part beside it
+//   warp 16      TMA loads: q one tile, k and v two;  warp 17  Q K^T and P V;  warp 18  Q S, K^T V~
+// Two issuing warps, because the score side may run ahead of the state's chain.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "kda_linear.cuh"
+#include "sm100_ptx.cuh"
+
+namespace kda {
+namespace lin {
+namespace {
+
+using namespace ptx;
+
+constexpr int C = 128;                          // tokens of a chunk
+constexpr int kThreads = 19 * 32;
+constexpr long long kTimeout = 4000000000ll;    // bounded waits: 4e9 SM cycles (~2 s)
+constexpr uint32_t REGION = C * 128;            // 64 channels x 128 tokens
+
+__device__ int g_linear_tc_error;               // sticky device error word of this translation unit
+
+struct Decays {
+    float a[C];        // decay of a token (1 past the segment's end)
+    float suf[C];      // product of the decays after it in its block of 32
+    float blk[4];      // a block's product
+};
+
+enum Bar {
+    B_QFULL, B_KFULL, B_VFULL = B_KFULL + 2, B_SC_DONE = B_VFULL + 2, B_P_READY, B_PV_DONE, B_QS_DONE, B_VT_READY,
+    B_KV_DONE, B_ST_READY = B_KV_DONE + 2, B_D2_FREE, B_DEC_READY, B_DRAIN = B_DEC_READY + 2, B_COUNT = B_DRAIN + 2
+};
+
+struct Shared {
+    Decays dec[2];
+    uint64_t bars[B_COUNT];
+    uint32_t tmem;
+    int abort;
+    int zero;          // always 0: the abort flag of waits that must not give up early
+};
+
+template <int DK, int DV>
+struct Layout {
+    static constexpr uint32_t KT = DK / 64 * REGION, VT = DV / 64 * REGION;
+    static constexpr uint32_t Q = 0, K = KT, V = K + 2 * KT, LO = V + 2 * VT, S = LO + VT;
+    static constexpr uint32_t SREG = DK * 128;   // the state copy: 64 value channels x DK key channels
+    static constexpr uint32_t SHARED = S + DV / 64 * SREG;
+    static constexpr uint32_t BYTES = SHARED + sizeof(Shared);
+};
+static_assert(Layout<128, 128>::BYTES <= 232448, "shared memory per block");
+
+constexpr uint32_t TM_SC = 0, TM_D2 = 128, TM_D1 = 256, TM_DST = 384, TM_COLS = 512;
+
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+__device__ __forceinline__ bool wait(Shared *sh, int bar, int phase)
+{
+    if (mbar_wait(&sh->bars[bar], phase & 1, &sh->abort, kTimeout)) return true;
+    if (!*reinterpret_cast<volatile int *>(&sh->abort)) {
+        atomicExch(&g_linear_tc_error, KDA_ERR_DEVICE_TIMEOUT);
+        *reinterpret_cast<volatile int *>(&sh->abort) = 1;
+    }
+    return false;
+}
+
+// The same for a whole warp: its lanes leave a loop together.
+__device__ __forceinline__ bool wait_warp(Shared *sh, int bar, int phase)
+{
+    return __all_sync(0xffffffffu, wait(sh, bar, phase));
+}
+
+// inclusive product over lanes 0 .. lane
+__device__ __forceinline__ float scan_up(float x, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x *= y;
+    }
+    return x;
+}
+
+__device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
+
+// 2 bf16 values times c: the bf16 nearest to each product, and the bf16 nearest to what is left
+__device__ __forceinline__ void split2(uint32_t x, float c, uint32_t &hi, uint32_t &lo)
+{
+    const float x0 = __uint_as_float(x << 16), x1 = __uint_as_float(x & 0xffff0000u);
+    hi = pack_bf16x2(x0 * c, x1 * c);
+    lo = pack_bf16x2(fmaf(x0, c, -__uint_as_float(hi << 16)), fmaf(x1, c, -__uint_as_float(hi & 0xffff0000u)));
+}
+
+template <int DK, int DV, bool OUT>
+__device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv, uint8_t *smem,
+                          Shared *sh, int h, int hk, long long t0, int nch)
+{
+    using L = Layout<DK, DV>;
+    int nk = 0, nq = 0;   // k/v and q tiles issued
+    auto load = [&](const CUtensorMap *m, uint32_t off, int bar, int regions, int head, int c) {
+        mbar_arrive_expect_tx(&sh->bars[bar], regions * REGION);
+        for (int r = 0; r < regions; ++r)
+            tma_load_3d(smem + off + r * REGION, m, &sh->bars[bar], 64 * r, head, (int)(t0 + (long long)c * C));
+    };
+    auto kv = [&](int c) {
+        if (c >= 2 && !wait(sh, B_KV_DONE + (c & 1), (c >> 1) - 1)) return false;
+        load(mk, L::K + (c & 1) * L::KT, B_KFULL + (c & 1), DK / 64, hk, c);
+        load(mv, L::V + (c & 1) * L::VT, B_VFULL + (c & 1), DV / 64, hk, c);
+        nk = c + 1;
+        return true;
+    };
+    bool ok = kv(0);
+    for (int c = 0; ok && c < nch; ++c) {
+        if constexpr (OUT) {
+            if (c > 0) ok = wait(sh, B_SC_DONE, c - 1) && wait(sh, B_QS_DONE, c - 1);
+            if (!ok) break;
+            load(mq, L::Q, B_QFULL, DK / 64, h, c);
+            nq = c + 1;
+            if (c + 1 < nch)
+                for (int r = 0; r < DK / 64; ++r) tma_prefetch_l2_3d(mq, 64 * r, h, (int)(t0 + (long long)(c + 1) * C));
+        }
+        if (c + 1 < nch) ok = kv(c + 1);
+    }
+    if (!ok) {   // no copy in flight when the CTA leaves
+        for (int c = max(0, nk - 2); c < nk; ++c) {
+            mbar_wait(&sh->bars[B_KFULL + (c & 1)], (c >> 1) & 1, &sh->zero, kTimeout);
+            mbar_wait(&sh->bars[B_VFULL + (c & 1)], (c >> 1) & 1, &sh->zero, kTimeout);
+        }
+        if (nq > 0) mbar_wait(&sh->bars[B_QFULL], (nq - 1) & 1, &sh->zero, kTimeout);
+    }
+}
+
+template <int DK, int DV>
+__device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
+{
+    using L = Layout<DK, DV>;
+    constexpr uint32_t I_QK = idesc_bf16(128, 128, 0, 0), I_PV = idesc_bf16(128, DV, 0, 1);
+    const uint64_t q = smem_desc(sb + L::Q, 0, 1024);
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+        const int s = c & 1;
+        ok = wait(sh, B_QFULL, c) && wait(sh, B_KFULL + s, c >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t k = smem_desc(sb + L::K + s * L::KT, 0, 1024);
+#pragma unroll
+        for (int x = 0; x < DK / 16; ++x)
+            mma_ss(tm + TM_SC, desc_at(q, (x >> 2) * REGION + (x & 3) * 32),
+                   desc_at(k, (x >> 2) * REGION + (x & 3) * 32), I_QK, x > 0);
+        mma_commit(&sh->bars[B_SC_DONE]);
+        ok = wait(sh, B_P_READY, c) && wait(sh, B_VFULL + s, c >> 1) && (c == 0 || wait(sh, B_D2_FREE, c - 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t v = smem_desc(sb + L::V + s * L::VT, REGION, 1024);
+#pragma unroll
+        for (int x = 0; x < C / 16; ++x)
+            mma_ts(tm + TM_D2, tm + TM_SC + 8 * x, desc_at(v, x * 2048), I_PV, x > 0);
+        mma_commit(&sh->bars[B_PV_DONE]);
+    }
+    if (!ok) {
+        mma_commit(&sh->bars[B_DRAIN]);
+        mbar_wait(&sh->bars[B_DRAIN], 0, &sh->zero, kTimeout);
+    }
+}
+
+template <int DK, int DV, bool OUT>
+__device__ void state_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
+{
+    using L = Layout<DK, DV>;
+    constexpr uint32_t I_QS = idesc_bf16(128, DV, 0, 1), I_KV = idesc_bf16(128, DV, 1, 1);
+    const uint64_t q = smem_desc(sb + L::Q, 0, 1024), st = smem_desc(sb + L::S, L::SREG, 1024);
+    const uint64_t lo = smem_desc(sb + L::LO, REGION, 1024);
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+        const int s = c & 1;
+        if constexpr (OUT) {
+            ok = wait(sh, B_ST_READY, c) && wait(sh, B_QFULL, c);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < DK / 16; ++x)
+                mma_ss(tm + TM_D1, desc_at(q, (x >> 2) * REGION + (x & 3) * 32), desc_at(st, x * 2048), I_QS, x > 0);
+            mma_commit(&sh->bars[B_QS_DONE]);
+        } else {
+            ok = c == 0 || wait(sh, B_ST_READY, c - 1);
+        }
+        ok = ok && wait(sh, B_VT_READY, c) && wait(sh, B_KFULL + s, c >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t k = smem_desc(sb + L::K + s * L::KT, REGION, 1024);
+        const uint64_t v = smem_desc(sb + L::V + s * L::VT, REGION, 1024);
+#pragma unroll
+        for (int x = 0; x < C / 16; ++x) {
+            mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(lo, x * 2048), I_KV, x > 0);
+            mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(v, x * 2048), I_KV, 1);
+        }
+        mma_commit(&sh->bars[B_KV_DONE + s]);
+    }
+    if (!ok) {
+        mma_commit(&sh->bars[B_DRAIN + 1]);
+        mbar_wait(&sh->bars[B_DRAIN + 1], 0, &sh->zero, kTimeout);
+    }
+}
+
+// warps 8-11: thread = token row 32 blk + lane
+template <int DK, int DV>
+__device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len, int nch)
+{
+    using L = Layout<DK, DV>;
+    const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
+    const uint32_t tq = tm + TM_SC + ((uint32_t)(32 * blk) << 16);
+    for (int c = 0; c < nch; ++c) {
+        if (!wait_warp(sh, B_SC_DONE, c) || !wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) break;
+        const Decays &d = sh->dec[c & 1];
+        tc_fence_after();
+        const float pre = scan_up(d.a[row], lane);
+        for (int j = 0; j < blk; ++j) {   // whole blocks before the row's own
+            uint32_t r[32], o[16];
+            tmem_ld32(tq + 32 * j, r);
+            float f = pre;
+            for (int x = j + 1; x < blk; ++x) f *= d.blk[x];
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float4 w = reinterpret_cast<const float4 *>(d.suf + 32 * j)[x];
+                o[2 * x] = pack_bf16x2(__uint_as_float(r[4 * x]) * (f * w.x), __uint_as_float(r[4 * x + 1]) * (f * w.y));
+                o[2 * x + 1] = pack_bf16x2(__uint_as_float(r[4 * x + 2]) * (f * w.z), __uint_as_float(r[4 * x + 3]) * (f * w.w));
+            }
+            // P overwrites scores already read: columns 16 j .. 16 j + 15 of blocks <= j
+            tmem_st16(tq + 16 * j, o);
+        }
+        {
+            uint32_t r[32], o[16];
+            tmem_ld32(tq + 32 * blk, r);
+            tmem_wait_ld();
+            float w = 1.f, odd = 0.f;
+#pragma unroll
+            for (int x = 31; x >= 0; --x) {   // from the diagonal down: w = product of a over (x, lane]
+                const float p = x <= lane ? __uint_as_float(r[x]) * w : 0.f;
+                if (x & 1) odd = p;
+                else o[x / 2] = pack_bf16x2(p, odd);
+                if (x <= lane) w *= d.a[32 * blk + x];
+            }
+            tmem_st16(tq + 16 * blk, o);
+        }
+        if (blk < 3) {
+            uint32_t o[16] = {};
+            for (int j = blk + 1; j < 4; ++j) tmem_st16(tq + 16 * j, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        const long long n = len - (long long)c * C;
+        if (n < C) {   // rows of other sequences: their P is 0, and 0 x NaN must not get in
+            if (!wait_warp(sh, B_VFULL + (c & 1), c >> 1)) break;
+            if (row >= n) {
+                uint4 *v = reinterpret_cast<uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
+                for (int r = 0; r < DV / 64; ++r)
+                    for (int x = 0; x < 8; ++x) v[r * (REGION / 16) + x] = zero4();
+            }
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->bars[B_P_READY]);
+    }
+}
+
+// warps 12-15: the chunk's decays, and V~
+template <int DK, int DV, bool OUT>
+__device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long long t0, long long len, int nch)
+{
+    using L = Layout<DK, DV>;
+    const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
+    auto log_decay = [&](int c) {
+        const long long t = (long long)c * C + row;
+        return t < len ? (p.g_per_token ? p.g[(t0 + t) * p.H + h] : p.g[h]) : 0.f;
+    };
+    // returns the product of the decays after this thread's token within its block
+    auto put = [&](int c, float g) {
+        Decays &d = sh->dec[c & 1];
+        const float a = expf(g);
+        float suf = a;   // inclusive product from this lane up, then without the lane's own
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_down_sync(0xffffffffu, suf, o);
+            if (lane + o < 32) suf *= y;
+        }
+        if (lane == 0) d.blk[blk] = suf;
+        suf = __shfl_down_sync(0xffffffffu, suf, 1);
+        if (lane == 31) suf = 1.f;
+        d.a[row] = a;
+        d.suf[row] = suf;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->bars[B_DEC_READY + (c & 1)]);
+        return suf;
+    };
+    float g = log_decay(0), suf = 0.f, suf_next = 0.f;
+    if constexpr (OUT) {
+        suf = put(0, g);
+        g = nch > 1 ? log_decay(1) : 0.f;
+    }
+    for (int c = 0; c < nch; ++c) {
+        // A buffer of decays is free when the chunk two before is done with: its V~ by the product
+        // K^T V~ of that chunk, its outputs and state update by P V (OUT) or K^T V~ (state only) of
+        // the chunk in between.
+        if (c > 0 && !wait_warp(sh, B_KV_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
+        if constexpr (OUT) {
+            if (!wait_warp(sh, B_PV_DONE, c)) break;
+            if (c + 1 < nch) {
+                suf_next = put(c + 1, g);
+                if (c + 2 < nch) g = log_decay(c + 2);
+            }
+        } else {
+            suf = put(c, g);
+            if (c + 1 < nch) g = log_decay(c + 1);
+        }
+        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) break;
+        float w = suf;
+        for (int x = blk + 1; x < 4; ++x) w *= sh->dec[c & 1].blk[x];
+        const bool live = (long long)c * C + row < len;
+        uint4 *v = reinterpret_cast<uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
+        uint4 *lo = reinterpret_cast<uint4 *>(smem + L::LO + row * 128);
+#pragma unroll
+        for (int r = 0; r < DV / 64; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int x = r * (int)(REGION / 16) + (i ^ (lane & 7));
+                uint4 hi4 = zero4(), lo4 = zero4();
+                if (live) {
+                    const uint4 in = v[x];
+                    split2(in.x, w, hi4.x, lo4.x);
+                    split2(in.y, w, hi4.y, lo4.y);
+                    split2(in.z, w, hi4.z, lo4.z);
+                    split2(in.w, w, hi4.w, lo4.w);
+                }
+                v[x] = hi4;
+                lo[x] = lo4;
+            }
+        if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL + (c & 1), c >> 1)) break;
+        if (!live) {   // a row of another sequence: 0 x NaN must not get into the state
+            uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + (c & 1) * L::KT + row * 128);
+            for (int r = 0; r < DK / 64; ++r)
+                for (int i = 0; i < 8; ++i) k[r * (REGION / 16) + i] = zero4();
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->bars[B_VT_READY]);
+        suf = suf_next;
+    }
+}
+
+__device__ __forceinline__ void store_row8(__nv_bfloat16 *o, const float (&v)[8]) { store8(o, v); }
+__device__ __forceinline__ void store_row8(float *o, const float (&v)[8]) { store8(o, v); }
+
+// warps 0-7: thread = key channel / token row 32 (warp % 4) + lane, value channels [DV/2 half, +DV/2)
+template <int DK, int DV, typename TO, bool OUT>
+__device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm, const Item &it, int item, int h,
+                           int nch)
+{
+    using L = Layout<DK, DV>;
+    constexpr int N = DV / 2;
+    const int warp = threadIdx.x >> 5, blk = warp & 3, half = warp >> 2, lane = threadIdx.x & 31;
+    const int row = 32 * blk + lane, c0 = half * N;
+    const uint32_t tq = tm + ((uint32_t)(32 * blk) << 16) + c0;
+    const bool row_ok = row < p.dk;
+    const long long unit = (long long)p.dk * p.dv, at = (long long)row * p.dv + c0;
+    const long long own = ((long long)it.seq * p.H + h) * unit + at, slot = ((long long)item * p.H + h) * unit + at;
+    const float *from = it.seg == 0 && p.init ? p.init + own : nullptr;
+    if (OUT && it.nseg > 1 && (it.seg > 0 || p.init)) from = p.starts + slot;
+    float st[N];
+#pragma unroll
+    for (int x = 0; x < N; x += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (from && row_ok && c0 + x < p.dv) v = *reinterpret_cast<const float4 *>(from + x);
+        st[x] = v.x; st[x + 1] = v.y; st[x + 2] = v.z; st[x + 3] = v.w;
+        // a first segment's start is kept: the last segment may overwrite it (final_state = init)
+        if (!OUT && it.seg == 0 && p.init && row_ok && c0 + x < p.dv)
+            *reinterpret_cast<float4 *>(p.starts + slot + x) = v;
+    }
+    auto copy_state = [&] {   // bf16 copy, rows = key channels, 64 value channels per region
+        if (row < DK) {
+#pragma unroll
+            for (int x = 0; x < N; x += 8) {
+                uint4 u;
+                u.x = pack_bf16x2(st[x], st[x + 1]);
+                u.y = pack_bf16x2(st[x + 2], st[x + 3]);
+                u.z = pack_bf16x2(st[x + 4], st[x + 5]);
+                u.w = pack_bf16x2(st[x + 6], st[x + 7]);
+                const int col = c0 + x;
+                *reinterpret_cast<uint4 *>(smem + L::S + (col >> 6) * L::SREG + sw128(row, (col & 63) * 2)) = u;
+            }
+        }
+        fence_proxy_async_smem();
+    };
+    auto arrive = [&](int bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->bars[bar]);
+    };
+    if constexpr (OUT) {
+        copy_state();
+        arrive(B_ST_READY);
+    }
+    float whole = 1.f;
+    const long long len = it.t1 - it.t0;
+    for (int c = 0; c < nch; ++c) {
+        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return;
+        const Decays &d = sh->dec[c & 1];
+        const float tot = d.blk[0] * d.blk[1] * d.blk[2] * d.blk[3];
+        whole *= tot;
+        if constexpr (OUT) {
+            float pre = scan_up(d.a[row], lane) * p.scale;
+            for (int x = 0; x < blk; ++x) pre *= d.blk[x];
+            if (!wait_warp(sh, B_QS_DONE, c) || !wait_warp(sh, B_PV_DONE, c)) return;
+            tc_fence_after();
+            const long long t = (long long)c * C + row;
+            TO *o = static_cast<TO *>(p.out) + ((it.t0 + t) * p.H + h) * p.dv + c0;
+#pragma unroll
+            for (int x = 0; x < N; x += 16) {
+                uint32_t r1[16], r2[16];
+                tmem_ld16(tq + TM_D1 + x, r1);
+                tmem_ld16(tq + TM_D2 + x, r2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int y = 0; y < 16; y += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = fmaf(pre, __uint_as_float(r1[y + e]), p.scale * __uint_as_float(r2[y + e]));
+                    if (t < len && c0 + x + y < p.dv) store_row8(o + x + y, v);
+                }
+            }
+            tc_fence_before();
+            arrive(B_D2_FREE);
+        }
+        if (!wait_warp(sh, B_KV_DONE + (c & 1), c >> 1)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < N; x += 16) {
+            uint32_t r[16];
+            tmem_ld16(tq + TM_DST + x, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
+        }
+        tc_fence_before();
+        if constexpr (OUT) {
+            if (c + 1 < nch) {
+                copy_state();
+                arrive(B_ST_READY);
+            }
+        } else {
+            arrive(B_ST_READY);
+        }
+    }
+    float *to = nullptr;
+    if (OUT) to = it.seg == it.nseg - 1 && p.final_state ? p.final_state + own : nullptr;
+    else to = p.starts + slot + (long long)p.H * unit;
+    if (to && row_ok) {
+#pragma unroll
+        for (int x = 0; x < N; x += 4)
+            if (c0 + x < p.dv) *reinterpret_cast<float4 *>(to + x) = make_float4(st[x], st[x + 1], st[x + 2], st[x + 3]);
+    }
+    if (!OUT && threadIdx.x == 0) p.decays[(long long)item * p.H + h] = whole;
+}
+
+template <int DK, int DV, typename TO, bool OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, const Args p)
+{
+    using L = Layout<DK, DV>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Shared *sh = reinterpret_cast<Shared *>(smem + L::SHARED);
+    const int warp = threadIdx.x >> 5;
+    const int h = blockIdx.x % p.H, item = blockIdx.x / p.H;
+    const Item it = find_item(p.cu, p.n_seqs, p.T, p.seg_len, item);
+    if (it.seq < 0 || (!OUT && it.seg == it.nseg - 1)) return;
+    if ((smem_u32(smem) & 1023u) != 0) {   // the swizzle's atoms; the runtime honours the declaration
+        if (threadIdx.x == 0) atomicExch(&g_linear_tc_error, KDA_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < B_COUNT; ++b) {
+            int n = 1;
+            if (b == B_P_READY || b == B_VT_READY || b == B_DEC_READY || b == B_DEC_READY + 1) n = 4;
+            if (b == B_ST_READY || b == B_D2_FREE) n = 8;
+            mbar_init(&sh->bars[b], n);
+        }
+        sh->abort = 0;
+        sh->zero = 0;
+        fence_barrier_init();
+        if (OUT) tma_prefetch_desc(&mq);
+        tma_prefetch_desc(&mk);
+        tma_prefetch_desc(&mv);
+    }
+    if (warp == 17) {
+        tmem_alloc(&sh->tmem, TM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sh->tmem;
+    const long long len = it.t1 - it.t0;
+    const int nch = (int)((len + C - 1) / C);
+    if (warp < 8) {
+        state_role<DK, DV, TO, OUT>(p, smem, sh, tm, it, item, h, nch);
+    } else if (warp < 12) {
+        if (OUT) score_role<DK, DV>(smem, sh, tm, len, nch);
+    } else if (warp < 16) {
+        if (nch > 0) value_role<DK, DV, OUT>(p, smem, sh, h, it.t0, len, nch);
+    } else if ((threadIdx.x & 31) == 0 && nch > 0) {
+        if (warp == 16) load_role<DK, DV, OUT>(&mq, &mk, &mv, smem, sh, h, h / p.group, it.t0, nch);
+        if (warp == 17 && OUT) score_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
+        if (warp == 18) state_mma_role<DK, DV, OUT>(smem_u32(smem), sh, tm, nch);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 17) tmem_dealloc(tm, TM_COLS);
+}
+
+// ---------------------------------------------------------------------------------------------
+// host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// [T, heads, d] bf16: box = 64 channels x 1 head x 128 tokens, 128-byte swizzle; channels past d
+// and tokens past T read as zeros
+bool make_map(CUtensorMap *map, const void *base, int heads, int d, long long T)
+{
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)C}, es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV, typename TO, bool OUT>
+bool launch_one(const CUtensorMap *m, const Args &p, cudaStream_t stream)
+{
+    const int bytes = (int)Layout<DK, DV>::BYTES;
+    // a function attribute belongs to the current device: set it on every launch
+    if (cudaFuncSetAttribute(linear_tc_kernel<DK, DV, TO, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+        return false;
+    linear_tc_kernel<DK, DV, TO, OUT><<<(unsigned)(p.items * p.H), kThreads, bytes, stream>>>(m[0], m[1], m[2], p);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+template <int DK, int DV>
+int run_dims(const CUtensorMap *m, const Args &p, int out_dtype, cudaStream_t stream)
+{
+    if (p.seg_len > 0) {
+        if (!launch_one<DK, DV, float, false>(m, p, stream)) return KDA_ERR_CUDA;
+        launch_join(p, stream);
+    }
+    const bool ok = out_dtype == KDA_BF16 ? launch_one<DK, DV, __nv_bfloat16, true>(m, p, stream)
+                                          : launch_one<DK, DV, float, true>(m, p, stream);
+    return ok ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace
+
+int run_tc_path(const Args &p, int out_dtype, cudaStream_t stream)
+{
+    CUtensorMap m[3];
+    if (!make_map(&m[0], p.q, p.H, p.dk, p.T) || !make_map(&m[1], p.k, p.H / p.group, p.dk, p.T) ||
+        !make_map(&m[2], p.v, p.H / p.group, p.dv, p.T))
+        return KDA_ERR_CUDA;
+    if (p.dk <= 64) return p.dv <= 64 ? run_dims<64, 64>(m, p, out_dtype, stream) : run_dims<64, 128>(m, p, out_dtype, stream);
+    return p.dv <= 64 ? run_dims<128, 64>(m, p, out_dtype, stream) : run_dims<128, 128>(m, p, out_dtype, stream);
+}
+
+}  // namespace lin
+
+int read_and_clear_status_linear(cudaStream_t s, int32_t *status)
+{
+    int host = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&host, lin::g_linear_tc_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
+            cudaSuccess ||
+        cudaMemcpyToSymbolAsync(lin::g_linear_tc_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    *status = host;
+    return KDA_OK;
+}
+
+}  // namespace kda
