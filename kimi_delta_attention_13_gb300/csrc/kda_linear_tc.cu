@@ -42,7 +42,9 @@ namespace {
 using namespace ptx;
 
 constexpr int C = 128;                          // tokens of a chunk
-constexpr int kThreads = 19 * 32;
+constexpr int kThreads = 5 * 128;
+// Registers a thread of each warpgroup (96 at launch): 2 x 120 + 96 + 72 + 72 = 5 x 96
+constexpr int kRegsState = 120, kRegsValue = 72, kRegsIssue = 72;
 constexpr long long kTimeout = 4000000000ll;    // bounded waits: 4e9 SM cycles (~2 s)
 constexpr uint32_t REGION = C * 128;            // 64 channels x 128 tokens
 
@@ -110,13 +112,32 @@ __device__ __forceinline__ float scan_up(float x, int lane)
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
 
-// 2 bf16 values times c: the bf16 nearest to each product, and the bf16 nearest to what is left
-__device__ __forceinline__ void split2(uint32_t x, float c, uint32_t &hi, uint32_t &lo)
+// Two bf16 values times w = w1 + w2 as hi + lo: hi is v w1 rounded; what that leaves is exact in a
+// bf16 (an 8 by 8 bit product less its upper half), and v w2 is added to it with one rounding, of
+// 2^-9 of a 2^-8th.
+__device__ __forceinline__ void split2(uint32_t x, __nv_bfloat162 w1, __nv_bfloat162 w2, uint32_t &hi, uint32_t &lo)
 {
-    const float x0 = __uint_as_float(x << 16), x1 = __uint_as_float(x & 0xffff0000u);
-    hi = pack_bf16x2(x0 * c, x1 * c);
-    lo = pack_bf16x2(fmaf(x0, c, -__uint_as_float(hi << 16)), fmaf(x1, c, -__uint_as_float(hi & 0xffff0000u)));
+    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&x);
+    const __nv_bfloat162 h = __hmul2(v, w1);
+    const __nv_bfloat162 l = __hfma2(v, w2, __hfma2(v, w1, __hneg2(h)));
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
 }
+
+// products of two pairs (one instruction)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    unsigned long long r, x, y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <int DK, int DV, bool OUT>
 __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv, uint8_t *smem,
@@ -157,6 +178,8 @@ __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CU
     }
 }
 
+// The issuing roles run as whole warps, one elected lane issuing, so that the descriptors stay in
+// uniform registers: computed by a single lane they cost some 100 cycles a product.
 template <int DK, int DV>
 __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 {
@@ -166,26 +189,33 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
         const int s = c & 1;
-        ok = wait(sh, B_QFULL, c) && wait(sh, B_KFULL + s, c >> 1);
+        ok = wait_warp(sh, B_QFULL, c) && wait_warp(sh, B_KFULL + s, c >> 1);
         if (!ok) break;
         tc_fence_after();
         const uint64_t k = smem_desc(sb + L::K + s * L::KT, 0, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int x = 0; x < DK / 16; ++x)
-            mma_ss(tm + TM_SC, desc_at(q, (x >> 2) * REGION + (x & 3) * 32),
-                   desc_at(k, (x >> 2) * REGION + (x & 3) * 32), I_QK, x > 0);
-        mma_commit(&sh->bars[B_SC_DONE]);
-        ok = wait(sh, B_P_READY, c) && wait(sh, B_VFULL + s, c >> 1) && (c == 0 || wait(sh, B_D2_FREE, c - 1));
+            for (int x = 0; x < DK / 16; ++x)
+                mma_ss(tm + TM_SC, desc_at(q, (x >> 2) * REGION + (x & 3) * 32),
+                       desc_at(k, (x >> 2) * REGION + (x & 3) * 32), I_QK, x > 0);
+            mma_commit(&sh->bars[B_SC_DONE]);
+        }
+        __syncwarp();
+        ok = wait_warp(sh, B_P_READY, c) && wait_warp(sh, B_VFULL + s, c >> 1) &&
+             (c == 0 || wait_warp(sh, B_D2_FREE, c - 1));
         if (!ok) break;
         tc_fence_after();
         const uint64_t v = smem_desc(sb + L::V + s * L::VT, REGION, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int x = 0; x < C / 16; ++x)
-            mma_ts(tm + TM_D2, tm + TM_SC + 8 * x, desc_at(v, x * 2048), I_PV, x > 0);
-        mma_commit(&sh->bars[B_PV_DONE]);
+            for (int x = 0; x < C / 16; ++x)
+                mma_ts(tm + TM_D2, tm + TM_SC + 8 * x, desc_at(v, x * 2048), I_PV, x > 0);
+            mma_commit(&sh->bars[B_PV_DONE]);
+        }
+        __syncwarp();
     }
     if (!ok) {
-        mma_commit(&sh->bars[B_DRAIN]);
+        if (elect_one()) mma_commit(&sh->bars[B_DRAIN]);
         mbar_wait(&sh->bars[B_DRAIN], 0, &sh->zero, kTimeout);
     }
 }
@@ -201,30 +231,36 @@ __device__ void state_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     for (int c = 0; c < nch; ++c) {
         const int s = c & 1;
         if constexpr (OUT) {
-            ok = wait(sh, B_ST_READY, c) && wait(sh, B_QFULL, c);
+            ok = wait_warp(sh, B_ST_READY, c) && wait_warp(sh, B_QFULL, c);
             if (!ok) break;
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int x = 0; x < DK / 16; ++x)
-                mma_ss(tm + TM_D1, desc_at(q, (x >> 2) * REGION + (x & 3) * 32), desc_at(st, x * 2048), I_QS, x > 0);
-            mma_commit(&sh->bars[B_QS_DONE]);
+                for (int x = 0; x < DK / 16; ++x)
+                    mma_ss(tm + TM_D1, desc_at(q, (x >> 2) * REGION + (x & 3) * 32), desc_at(st, x * 2048), I_QS, x > 0);
+                mma_commit(&sh->bars[B_QS_DONE]);
+            }
+            __syncwarp();
         } else {
-            ok = c == 0 || wait(sh, B_ST_READY, c - 1);
+            ok = c == 0 || wait_warp(sh, B_ST_READY, c - 1);
         }
-        ok = ok && wait(sh, B_VT_READY, c) && wait(sh, B_KFULL + s, c >> 1);
+        ok = ok && wait_warp(sh, B_VT_READY, c) && wait_warp(sh, B_KFULL + s, c >> 1);
         if (!ok) break;
         tc_fence_after();
         const uint64_t k = smem_desc(sb + L::K + s * L::KT, REGION, 1024);
         const uint64_t v = smem_desc(sb + L::V + s * L::VT, REGION, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int x = 0; x < C / 16; ++x) {
-            mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(lo, x * 2048), I_KV, x > 0);
-            mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(v, x * 2048), I_KV, 1);
+            for (int x = 0; x < C / 16; ++x) {
+                mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(lo, x * 2048), I_KV, x > 0);
+                mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(v, x * 2048), I_KV, 1);
+            }
+            mma_commit(&sh->bars[B_KV_DONE + s]);
         }
-        mma_commit(&sh->bars[B_KV_DONE + s]);
+        __syncwarp();
     }
     if (!ok) {
-        mma_commit(&sh->bars[B_DRAIN + 1]);
+        if (elect_one()) mma_commit(&sh->bars[B_DRAIN + 1]);
         mbar_wait(&sh->bars[B_DRAIN + 1], 0, &sh->zero, kTimeout);
     }
 }
@@ -240,33 +276,45 @@ __device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len
         if (!wait_warp(sh, B_SC_DONE, c) || !wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) break;
         const Decays &d = sh->dec[c & 1];
         tc_fence_after();
-        const float pre = scan_up(d.a[row], lane);
+        uint32_t r[32], o[16];
+        tmem_ld32(tq, r);
+        const float pre = scan_up(d.a[row], lane);   // prefix of the row's own block
+        float f = pre;
+        for (int x = 1; x < blk; ++x) f *= d.blk[x];
+        tmem_wait_ld();
         for (int j = 0; j < blk; ++j) {   // whole blocks before the row's own
-            uint32_t r[32], o[16];
-            tmem_ld32(tq + 32 * j, r);
-            float f = pre;
-            for (int x = j + 1; x < blk; ++x) f *= d.blk[x];
-            tmem_wait_ld();
+            const float2 ff = make_float2(f, f);
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 const float4 w = reinterpret_cast<const float4 *>(d.suf + 32 * j)[x];
-                o[2 * x] = pack_bf16x2(__uint_as_float(r[4 * x]) * (f * w.x), __uint_as_float(r[4 * x + 1]) * (f * w.y));
-                o[2 * x + 1] = pack_bf16x2(__uint_as_float(r[4 * x + 2]) * (f * w.z), __uint_as_float(r[4 * x + 3]) * (f * w.w));
+                const float2 p = mul2(make_float2(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1])),
+                                      mul2(ff, make_float2(w.x, w.y)));
+                const float2 q = mul2(make_float2(__uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3])),
+                                      mul2(ff, make_float2(w.z, w.w)));
+                o[2 * x] = pack_bf16x2(p.x, p.y);
+                o[2 * x + 1] = pack_bf16x2(q.x, q.y);
             }
             // P overwrites scores already read: columns 16 j .. 16 j + 15 of blocks <= j
             tmem_st16(tq + 16 * j, o);
+            tmem_ld32(tq + 32 * (j + 1), r);
+            f = pre;   // the factor of the next block spans one block less
+            for (int x = j + 2; x < blk; ++x) f *= d.blk[x];
+            tmem_wait_ld();
         }
         {
-            uint32_t r[32], o[16];
-            tmem_ld32(tq + 32 * blk, r);
-            tmem_wait_ld();
             float w = 1.f, odd = 0.f;
 #pragma unroll
-            for (int x = 31; x >= 0; --x) {   // from the diagonal down: w = product of a over (x, lane]
-                const float p = x <= lane ? __uint_as_float(r[x]) * w : 0.f;
-                if (x & 1) odd = p;
-                else o[x / 2] = pack_bf16x2(p, odd);
-                if (x <= lane) w *= d.a[32 * blk + x];
+            for (int y = 7; y >= 0; --y) {   // from the diagonal down: w = product of a over (x, lane]
+                const float4 a = reinterpret_cast<const float4 *>(d.a + 32 * blk)[y];
+                const float ay[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int e = 3; e >= 0; --e) {
+                    const int x = 4 * y + e;
+                    const float p = x <= lane ? __uint_as_float(r[x]) * w : 0.f;
+                    if (x & 1) odd = p;
+                    else o[x / 2] = pack_bf16x2(p, odd);
+                    if (x <= lane) w *= ay[e];
+                }
             }
             tmem_st16(tq + 16 * blk, o);
         }
@@ -320,7 +368,7 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         if (lane == 0) mbar_arrive(&sh->bars[B_DEC_READY + (c & 1)]);
         return suf;
     };
-    float g = log_decay(0), suf = 0.f, suf_next = 0.f;
+    float g = log_decay(0), suf = 0.f;
     if constexpr (OUT) {
         suf = put(0, g);
         g = nch > 1 ? log_decay(1) : 0.f;
@@ -332,10 +380,6 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         if (c > 0 && !wait_warp(sh, B_KV_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
         if constexpr (OUT) {
             if (!wait_warp(sh, B_PV_DONE, c)) break;
-            if (c + 1 < nch) {
-                suf_next = put(c + 1, g);
-                if (c + 2 < nch) g = log_decay(c + 2);
-            }
         } else {
             suf = put(c, g);
             if (c + 1 < nch) g = log_decay(c + 1);
@@ -343,27 +387,36 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) break;
         float w = suf;
         for (int x = blk + 1; x < 4; ++x) w *= sh->dec[c & 1].blk[x];
+        const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
+        const __nv_bfloat162 ww1 = __halves2bfloat162(w1, w1), ww2 = __halves2bfloat162(w2, w2);
         const bool live = (long long)c * C + row < len;
         uint4 *v = reinterpret_cast<uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
         uint4 *lo = reinterpret_cast<uint4 *>(smem + L::LO + row * 128);
+        if (live) {
 #pragma unroll
-        for (int r = 0; r < DV / 64; ++r)
+            for (int r = 0; r < DV / 32; ++r) {
+                uint4 in[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int x = r * (int)(REGION / 16) + (i ^ (lane & 7));
-                uint4 hi4 = zero4(), lo4 = zero4();
-                if (live) {
-                    const uint4 in = v[x];
-                    split2(in.x, w, hi4.x, lo4.x);
-                    split2(in.y, w, hi4.y, lo4.y);
-                    split2(in.z, w, hi4.z, lo4.z);
-                    split2(in.w, w, hi4.w, lo4.w);
+                for (int i = 0; i < 4; ++i)
+                    in[i] = v[(r >> 1) * (int)(REGION / 16) + (((r & 1) * 4 + i) ^ (lane & 7))];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = (r >> 1) * (int)(REGION / 16) + (((r & 1) * 4 + i) ^ (lane & 7));
+                    uint4 hi4, lo4;
+                    split2(in[i].x, ww1, ww2, hi4.x, lo4.x);
+                    split2(in[i].y, ww1, ww2, hi4.y, lo4.y);
+                    split2(in[i].z, ww1, ww2, hi4.z, lo4.z);
+                    split2(in[i].w, ww1, ww2, hi4.w, lo4.w);
+                    v[x] = hi4;
+                    lo[x] = lo4;
                 }
-                v[x] = hi4;
-                lo[x] = lo4;
             }
+        } else {   // a row of another sequence: 0 x NaN must not get into the state
+            for (int r = 0; r < DV / 64; ++r)
+                for (int i = 0; i < 8; ++i) v[r * (REGION / 16) + i] = lo[r * (REGION / 16) + i] = zero4();
+        }
         if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL + (c & 1), c >> 1)) break;
-        if (!live) {   // a row of another sequence: 0 x NaN must not get into the state
+        if (!live) {
             uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + (c & 1) * L::KT + row * 128);
             for (int r = 0; r < DK / 64; ++r)
                 for (int i = 0; i < 8; ++i) k[r * (REGION / 16) + i] = zero4();
@@ -371,16 +424,18 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->bars[B_VT_READY]);
-        suf = suf_next;
+        if constexpr (OUT) {
+            if (c + 1 < nch) {
+                suf = put(c + 1, g);
+                if (c + 2 < nch) g = log_decay(c + 2);
+            }
+        }
     }
 }
 
-__device__ __forceinline__ void store_row8(__nv_bfloat16 *o, const float (&v)[8]) { store8(o, v); }
-__device__ __forceinline__ void store_row8(float *o, const float (&v)[8]) { store8(o, v); }
-
 // warps 0-7: thread = key channel / token row 32 (warp % 4) + lane, value channels [DV/2 half, +DV/2)
 template <int DK, int DV, typename TO, bool OUT>
-__device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm, const Item &it, int item, int h,
+__device__ void state_role(const Args &p, const CUtensorMap *mo, uint8_t *smem, Shared *sh, uint32_t tm, const Item &it, int item, int h,
                            int nch)
 {
     using L = Layout<DK, DV>;
@@ -429,52 +484,77 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
     float whole = 1.f;
     const long long len = it.t1 - it.t0;
     for (int c = 0; c < nch; ++c) {
-        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return;
+        bool ok = wait_warp(sh, B_DEC_READY + (c & 1), c >> 1);
         const Decays &d = sh->dec[c & 1];
         const float tot = d.blk[0] * d.blk[1] * d.blk[2] * d.blk[3];
         whole *= tot;
         if constexpr (OUT) {
             float pre = scan_up(d.a[row], lane) * p.scale;
             for (int x = 0; x < blk; ++x) pre *= d.blk[x];
-            if (!wait_warp(sh, B_QS_DONE, c) || !wait_warp(sh, B_PV_DONE, c)) return;
-            tc_fence_after();
-            const long long t = (long long)c * C + row;
-            TO *o = static_cast<TO *>(p.out) + ((it.t0 + t) * p.H + h) * p.dv + c0;
+            ok = ok && wait_warp(sh, B_QS_DONE, c) && wait_warp(sh, B_PV_DONE, c);
+            // A whole chunk's bf16 outputs leave by TMA from the state copy's place, which Q S has read
+            // and the next copy is not written to yet: row-per-thread stores of 16 bytes would touch
+            // 32 rows an instruction.  A partial chunk's (and fp32's) rows are stored from here.
+            const bool staged = sizeof(TO) == 2 && DK == 128 && (long long)(c + 1) * C <= len;
+            if (ok) {
+                tc_fence_after();
+                const long long t = (long long)c * C + row;
+                TO *o = static_cast<TO *>(p.out) + ((it.t0 + t) * p.H + h) * p.dv + c0;
 #pragma unroll
-            for (int x = 0; x < N; x += 16) {
-                uint32_t r1[16], r2[16];
-                tmem_ld16(tq + TM_D1 + x, r1);
-                tmem_ld16(tq + TM_D2 + x, r2);
+                for (int x = 0; x < N; x += 16) {
+                    uint32_t r1[16], r2[16];
+                    tmem_ld16(tq + TM_D1 + x, r1);
+                    tmem_ld16(tq + TM_D2 + x, r2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int y = 0; y < 16; y += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = fmaf(pre, __uint_as_float(r1[y + e]), p.scale * __uint_as_float(r2[y + e]));
+                        const int col = c0 + x + y;
+                        if (staged) {
+                            *reinterpret_cast<uint4 *>(smem + L::S + (col >> 6) * REGION + sw128(row, (col & 63) * 2)) =
+                                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                        } else if (t < len && col < p.dv) {
+                            store8(o + x + y, v);
+                        }
+                    }
+                }
+                tc_fence_before();
+                arrive(B_D2_FREE);
+                fence_proxy_async_smem();
+            }
+            if (!bar_and(1, 256, ok)) return;   // the group leaves together
+            if (staged && threadIdx.x == 0) {
+                for (int r = 0; r < DV / 64; ++r)
+                    tma_store_3d(mo, smem + L::S + r * REGION, 64 * r, h, (int)(it.t0 + (long long)c * C));
+                bulk_commit();
+            }
+        }
+        ok = ok && wait_warp(sh, B_KV_DONE + (c & 1), c >> 1);
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < N; x += 32) {
+                uint32_t r[32];
+                tmem_ld32(tq + TM_DST + x, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 16; y += 8) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = fmaf(pre, __uint_as_float(r1[y + e]), p.scale * __uint_as_float(r2[y + e]));
-                    if (t < len && c0 + x + y < p.dv) store_row8(o + x + y, v);
-                }
+                for (int e = 0; e < 32; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
             }
             tc_fence_before();
-            arrive(B_D2_FREE);
         }
-        if (!wait_warp(sh, B_KV_DONE + (c & 1), c >> 1)) return;
-        tc_fence_after();
-#pragma unroll
-        for (int x = 0; x < N; x += 16) {
-            uint32_t r[16];
-            tmem_ld16(tq + TM_DST + x, r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
-        }
-        tc_fence_before();
         if constexpr (OUT) {
+            if (threadIdx.x == 0) bulk_wait_read_all();   // the outputs' store has read the place
+            if (!bar_and(1, 256, ok)) return;
             if (c + 1 < nch) {
                 copy_state();
                 arrive(B_ST_READY);
             }
         } else {
+            if (!ok) return;
             arrive(B_ST_READY);
         }
     }
@@ -492,7 +572,7 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
 template <int DK, int DV, typename TO, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                 const __grid_constant__ CUtensorMap mv, const Args p)
+                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Args p)
 {
     using L = Layout<DK, DV>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -530,15 +610,19 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const long long len = it.t1 - it.t0;
     const int nch = (int)((len + C - 1) / C);
     if (warp < 8) {
-        state_role<DK, DV, TO, OUT>(p, smem, sh, tm, it, item, h, nch);
+        regs_up<kRegsState>();
+        state_role<DK, DV, TO, OUT>(p, &mo, smem, sh, tm, it, item, h, nch);
     } else if (warp < 12) {
         if (OUT) score_role<DK, DV>(smem, sh, tm, len, nch);
     } else if (warp < 16) {
+        regs_down<kRegsValue>();
         if (nch > 0) value_role<DK, DV, OUT>(p, smem, sh, h, it.t0, len, nch);
-    } else if ((threadIdx.x & 31) == 0 && nch > 0) {
-        if (warp == 16) load_role<DK, DV, OUT>(&mq, &mk, &mv, smem, sh, h, h / p.group, it.t0, nch);
-        if (warp == 17 && OUT) score_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
-        if (warp == 18) state_mma_role<DK, DV, OUT>(smem_u32(smem), sh, tm, nch);
+    } else {
+        regs_down<kRegsIssue>();
+        if (warp == 16 && (threadIdx.x & 31) == 0 && nch > 0)
+            load_role<DK, DV, OUT>(&mq, &mk, &mv, smem, sh, h, h / p.group, it.t0, nch);
+        if (warp == 17 && OUT && nch > 0) score_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
+        if (warp == 18 && nch > 0) state_mma_role<DK, DV, OUT>(smem_u32(smem), sh, tm, nch);
     }
     tc_fence_before();
     __syncthreads();
@@ -586,7 +670,7 @@ bool launch_one(const CUtensorMap *m, const Args &p, cudaStream_t stream)
     if (cudaFuncSetAttribute(linear_tc_kernel<DK, DV, TO, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess)
         return false;
-    linear_tc_kernel<DK, DV, TO, OUT><<<(unsigned)(p.items * p.H), kThreads, bytes, stream>>>(m[0], m[1], m[2], p);
+    linear_tc_kernel<DK, DV, TO, OUT><<<(unsigned)(p.items * p.H), kThreads, bytes, stream>>>(m[0], m[1], m[2], m[3], p);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -606,9 +690,10 @@ int run_dims(const CUtensorMap *m, const Args &p, int out_dtype, cudaStream_t st
 
 int run_tc_path(const Args &p, int out_dtype, cudaStream_t stream)
 {
-    CUtensorMap m[3];
+    CUtensorMap m[4];
     if (!make_map(&m[0], p.q, p.H, p.dk, p.T) || !make_map(&m[1], p.k, p.H / p.group, p.dk, p.T) ||
-        !make_map(&m[2], p.v, p.H / p.group, p.dv, p.T))
+        !make_map(&m[2], p.v, p.H / p.group, p.dv, p.T) ||
+        !make_map(&m[3], p.out, p.H, p.dv, p.T))   // used for bf16 outputs only
         return KDA_ERR_CUDA;
     if (p.dk <= 64) return p.dv <= 64 ? run_dims<64, 64>(m, p, out_dtype, stream) : run_dims<64, 128>(m, p, out_dtype, stream);
     return p.dv <= 64 ? run_dims<128, 64>(m, p, out_dtype, stream) : run_dims<128, 128>(m, p, out_dtype, stream);
