@@ -11,7 +11,7 @@
 //     scores = Q K^T         A, B = q, k tiles in shared memory
 //     D2 = P V               A = P = w . scores (bf16, TMEM), B = v tile
 //     D1 = Q S               B = the state as bf16 (shared memory)
-//     Dst = K^T V~           B = V~ = c . v, exactly split in two bf16 parts (two passes)
+//     Dst = K^T V~           B = V~ = c . v, split in two bf16 parts (two passes)
 // The state itself stays in fp32 registers: S <- (prod a) S + Dst.  Its update must be good to fp32,
 // so V~ carries 16 bits; P and the state's copy are rounded to bf16 once each (their products make
 // the outputs, to which a bf16 rounding of the result is added anyway).
@@ -22,12 +22,12 @@
 // running product from the diagonal down.
 //
 // One CTA works through the chunks of one (segment, head).  Roles, joined by mbarriers:
-//   warps 0-7    output of a chunk (scale (p D1 + D2) -> global), then the state update: 64 (dv = 128)
-//                state columns of one key channel per thread, and the state's bf16 copy
+//   warps 0-7    the state update: 64 (dv = 128) state columns of one key channel per thread, and the
+//                state's bf16 copy; then the chunk's outputs, scale (p D1 + D2) -> global
 //   warps 8-11   scores -> P, one token row per thread
-//   warps 12-15  the chunk's decays; V~ high part over v in place (after P V), low part beside it
-//   warp 16      TMA loads: q one tile, k and v two;  warp 17  Q K^T and P V;  warp 18  Q S, K^T V~
-// Two issuing warps, because the score side may run ahead of the state's chain.
+//   warps 12-15  the chunk's decays, and V~
+//   warp 16      TMA loads: q and k one tile, v two;  warps 17, 18, 19  issue Q K^T and P V;  K^T V~;  Q S
+// Three issuing warps, because scores, state and outputs of neighbouring chunks overlap.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -43,8 +43,10 @@ using namespace ptx;
 
 constexpr int C = 128;                          // tokens of a chunk
 constexpr int kThreads = 5 * 128;
-// Registers a thread of each warpgroup (96 at launch): 2 x 120 + 96 + 72 + 72 = 5 x 96
-constexpr int kRegsState = 120, kRegsValue = 72, kRegsIssue = 72;
+// Registers a thread of each warpgroup, 96 at launch: 2 x 120 + 96 + 64 + 80 = 5 x 96 with outputs,
+// 2 x 136 + 40 + 72 + 96 = 5 x 96 for states alone.  What does not fit spills to local memory, and with
+// this much shared memory nearly every reload of it comes from L2.
+constexpr int kRegsState[2] = {136, 120}, kRegsScore = 40, kRegsValue[2] = {72, 64}, kRegsIssue = 80;
 constexpr long long kTimeout = 4000000000ll;    // bounded waits: 4e9 SM cycles (~2 s)
 constexpr uint32_t REGION = C * 128;            // 64 channels x 128 tokens
 
@@ -57,8 +59,8 @@ struct Decays {
 };
 
 enum Bar {
-    B_QFULL, B_KFULL, B_VFULL = B_KFULL + 2, B_SC_DONE = B_VFULL + 2, B_P_READY, B_PV_DONE, B_QS_DONE, B_VT_READY,
-    B_KV_DONE, B_ST_READY = B_KV_DONE + 2, B_D2_FREE, B_DEC_READY, B_DRAIN = B_DEC_READY + 2, B_COUNT = B_DRAIN + 2
+    B_QFULL, B_KFULL, B_VFULL, B_SC_DONE = B_VFULL + 2, B_P_READY, B_PV_DONE, B_QS_DONE = B_PV_DONE + 2, B_VT_READY, B_KV_DONE,
+    B_ST_READY, B_DST_FREE, B_D2_FREE, B_DEC_READY = B_D2_FREE + 2, B_DRAIN = B_DEC_READY + 2, B_COUNT = B_DRAIN + 3
 };
 
 struct Shared {
@@ -72,7 +74,7 @@ struct Shared {
 template <int DK, int DV>
 struct Layout {
     static constexpr uint32_t KT = DK / 64 * REGION, VT = DV / 64 * REGION;
-    static constexpr uint32_t Q = 0, K = KT, V = K + 2 * KT, LO = V + 2 * VT, S = LO + VT;
+    static constexpr uint32_t Q = 0, K = KT, V = K + KT, HI = V + 2 * VT, LO = HI + VT, S = LO + VT;
     static constexpr uint32_t SREG = DK * 128;   // the state copy: 64 value channels x DK key channels
     static constexpr uint32_t SHARED = S + DV / 64 * SREG;
     static constexpr uint32_t BYTES = SHARED + sizeof(Shared);
@@ -85,7 +87,12 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return
 
 __device__ __forceinline__ bool wait(Shared *sh, int bar, int phase)
 {
-    if (mbar_wait(&sh->bars[bar], phase & 1, &sh->abort, kTimeout)) return true;
+    uint64_t *b = &sh->bars[bar];
+    if (mbar_try_wait(b, phase & 1)) return true;
+    const long long t0 = clock64();
+    do {
+        if (mbar_try_wait(b, phase & 1)) return true;
+    } while (!*reinterpret_cast<volatile int *>(&sh->abort) && clock64() - t0 <= kTimeout);
     if (!*reinterpret_cast<volatile int *>(&sh->abort)) {
         atomicExch(&g_linear_tc_error, KDA_ERR_DEVICE_TIMEOUT);
         *reinterpret_cast<volatile int *>(&sh->abort) = 1;
@@ -144,36 +151,44 @@ __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CU
                           Shared *sh, int h, int hk, long long t0, int nch)
 {
     using L = Layout<DK, DV>;
-    int nk = 0, nq = 0;   // k/v and q tiles issued
     auto load = [&](const CUtensorMap *m, uint32_t off, int bar, int regions, int head, int c) {
-        mbar_arrive_expect_tx(&sh->bars[bar], regions * REGION);
-        for (int r = 0; r < regions; ++r)
-            tma_load_3d(smem + off + r * REGION, m, &sh->bars[bar], 64 * r, head, (int)(t0 + (long long)c * C));
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&sh->bars[bar], regions * REGION);
+            for (int r = 0; r < regions; ++r)
+                tma_load_3d(smem + off + r * REGION, m, &sh->bars[bar], 64 * r, head, (int)(t0 + (long long)c * C));
+        }
+        __syncwarp();
     };
-    auto kv = [&](int c) {
-        if (c >= 2 && !wait(sh, B_KV_DONE + (c & 1), (c >> 1) - 1)) return false;
-        load(mk, L::K + (c & 1) * L::KT, B_KFULL + (c & 1), DK / 64, hk, c);
-        load(mv, L::V + (c & 1) * L::VT, B_VFULL + (c & 1), DV / 64, hk, c);
-        nk = c + 1;
-        return true;
+    auto ahead = [&](const CUtensorMap *m, int regions, int head, int c) {   // into L2
+        if (c < nch && elect_one())
+            for (int r = 0; r < regions; ++r) tma_prefetch_l2_3d(m, 64 * r, head, (int)(t0 + (long long)c * C));
+        __syncwarp();
     };
-    bool ok = kv(0);
-    for (int c = 0; ok && c < nch; ++c) {
+    auto value = [&](int c) { load(mv, L::V + (c & 1) * L::VT, B_VFULL + (c & 1), DV / 64, hk, c); };
+    int nk = 0, nq = 0, nv = 1;   // tiles issued
+    value(0);
+    for (int c = 0; c < nch; ++c) {
         if constexpr (OUT) {
-            if (c > 0) ok = wait(sh, B_SC_DONE, c - 1) && wait(sh, B_QS_DONE, c - 1);
-            if (!ok) break;
+            if (c > 0 && !(wait_warp(sh, B_SC_DONE, c - 1) && wait_warp(sh, B_QS_DONE, c - 1))) break;
             load(mq, L::Q, B_QFULL, DK / 64, h, c);
             nq = c + 1;
-            if (c + 1 < nch)
-                for (int r = 0; r < DK / 64; ++r) tma_prefetch_l2_3d(mq, 64 * r, h, (int)(t0 + (long long)(c + 1) * C));
+            ahead(mq, DK / 64, h, c + 1);
         }
-        if (c + 1 < nch) ok = kv(c + 1);
+        if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) break;
+        load(mk, L::K, B_KFULL, DK / 64, hk, c);
+        nk = c + 1;
+        ahead(mk, DK / 64, hk, c + 1);
+        if (c + 1 < nch) {
+            if (OUT && c > 0 && !wait_warp(sh, B_PV_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
+            value(c + 1);
+            nv = c + 2;
+            ahead(mv, DV / 64, hk, c + 2);
+        }
     }
-    if (!ok) {   // no copy in flight when the CTA leaves
-        for (int c = max(0, nk - 2); c < nk; ++c) {
-            mbar_wait(&sh->bars[B_KFULL + (c & 1)], (c >> 1) & 1, &sh->zero, kTimeout);
+    if (nk < nch || nv < nch) {   // no copy in flight when the CTA leaves
+        if (nk > 0) mbar_wait(&sh->bars[B_KFULL], (nk - 1) & 1, &sh->zero, kTimeout);
+        for (int c = max(0, nv - 2); c < nv; ++c)
             mbar_wait(&sh->bars[B_VFULL + (c & 1)], (c >> 1) & 1, &sh->zero, kTimeout);
-        }
         if (nq > 0) mbar_wait(&sh->bars[B_QFULL], (nq - 1) & 1, &sh->zero, kTimeout);
     }
 }
@@ -185,14 +200,13 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 {
     using L = Layout<DK, DV>;
     constexpr uint32_t I_QK = idesc_bf16(128, 128, 0, 0), I_PV = idesc_bf16(128, DV, 0, 1);
-    const uint64_t q = smem_desc(sb + L::Q, 0, 1024);
+    const uint64_t q = smem_desc(sb + L::Q, 0, 1024), k = smem_desc(sb + L::K, 0, 1024);
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
         const int s = c & 1;
-        ok = wait_warp(sh, B_QFULL, c) && wait_warp(sh, B_KFULL + s, c >> 1);
+        ok = wait_warp(sh, B_QFULL, c) && wait_warp(sh, B_KFULL, c);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t k = smem_desc(sb + L::K + s * L::KT, 0, 1024);
         if (elect_one()) {
 #pragma unroll
             for (int x = 0; x < DK / 16; ++x)
@@ -202,7 +216,7 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
         }
         __syncwarp();
         ok = wait_warp(sh, B_P_READY, c) && wait_warp(sh, B_VFULL + s, c >> 1) &&
-             (c == 0 || wait_warp(sh, B_D2_FREE, c - 1));
+             (c == 0 || wait_warp(sh, B_D2_FREE + (s ^ 1), (c - 1) >> 1));
         if (!ok) break;
         tc_fence_after();
         const uint64_t v = smem_desc(sb + L::V + s * L::VT, REGION, 1024);
@@ -210,7 +224,7 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 #pragma unroll
             for (int x = 0; x < C / 16; ++x)
                 mma_ts(tm + TM_D2, tm + TM_SC + 8 * x, desc_at(v, x * 2048), I_PV, x > 0);
-            mma_commit(&sh->bars[B_PV_DONE]);
+            mma_commit(&sh->bars[B_PV_DONE + s]);
         }
         __syncwarp();
     }
@@ -220,48 +234,57 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     }
 }
 
-template <int DK, int DV, bool OUT>
-__device__ void state_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
+template <int DK, int DV>
+__device__ void update_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 {
     using L = Layout<DK, DV>;
-    constexpr uint32_t I_QS = idesc_bf16(128, DV, 0, 1), I_KV = idesc_bf16(128, DV, 1, 1);
-    const uint64_t q = smem_desc(sb + L::Q, 0, 1024), st = smem_desc(sb + L::S, L::SREG, 1024);
-    const uint64_t lo = smem_desc(sb + L::LO, REGION, 1024);
+    constexpr uint32_t I_KV = idesc_bf16(128, DV, 1, 1);
+    const uint64_t k = smem_desc(sb + L::K, REGION, 1024);
+    const uint64_t hi = smem_desc(sb + L::HI, REGION, 1024), lo = smem_desc(sb + L::LO, REGION, 1024);
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
-        const int s = c & 1;
-        if constexpr (OUT) {
-            ok = wait_warp(sh, B_ST_READY, c) && wait_warp(sh, B_QFULL, c);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int x = 0; x < DK / 16; ++x)
-                    mma_ss(tm + TM_D1, desc_at(q, (x >> 2) * REGION + (x & 3) * 32), desc_at(st, x * 2048), I_QS, x > 0);
-                mma_commit(&sh->bars[B_QS_DONE]);
-            }
-            __syncwarp();
-        } else {
-            ok = c == 0 || wait_warp(sh, B_ST_READY, c - 1);
-        }
-        ok = ok && wait_warp(sh, B_VT_READY, c) && wait_warp(sh, B_KFULL + s, c >> 1);
+        ok = wait_warp(sh, B_VT_READY, c) && wait_warp(sh, B_KFULL, c) && (c == 0 || wait_warp(sh, B_DST_FREE, c - 1));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t k = smem_desc(sb + L::K + s * L::KT, REGION, 1024);
-        const uint64_t v = smem_desc(sb + L::V + s * L::VT, REGION, 1024);
         if (elect_one()) {
 #pragma unroll
             for (int x = 0; x < C / 16; ++x) {
                 mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(lo, x * 2048), I_KV, x > 0);
-                mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(v, x * 2048), I_KV, 1);
+                mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(hi, x * 2048), I_KV, 1);
             }
-            mma_commit(&sh->bars[B_KV_DONE + s]);
+            mma_commit(&sh->bars[B_KV_DONE]);
         }
         __syncwarp();
     }
     if (!ok) {
         if (elect_one()) mma_commit(&sh->bars[B_DRAIN + 1]);
         mbar_wait(&sh->bars[B_DRAIN + 1], 0, &sh->zero, kTimeout);
+    }
+}
+
+template <int DK, int DV>
+__device__ void read_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
+{
+    using L = Layout<DK, DV>;
+    constexpr uint32_t I_QS = idesc_bf16(128, DV, 0, 1);
+    const uint64_t q = smem_desc(sb + L::Q, 0, 1024), st = smem_desc(sb + L::S, L::SREG, 1024);
+    bool ok = true;
+    for (int c = 0; c < nch; ++c) {
+        ok = wait_warp(sh, B_ST_READY, c) && wait_warp(sh, B_QFULL, c) &&
+             (c == 0 || wait_warp(sh, B_D2_FREE + ((c - 1) & 1), (c - 1) >> 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+            for (int x = 0; x < DK / 16; ++x)
+                mma_ss(tm + TM_D1, desc_at(q, (x >> 2) * REGION + (x & 3) * 32), desc_at(st, x * 2048), I_QS, x > 0);
+            mma_commit(&sh->bars[B_QS_DONE]);
+        }
+        __syncwarp();
+    }
+    if (!ok) {
+        if (elect_one()) mma_commit(&sh->bars[B_DRAIN + 2]);
+        mbar_wait(&sh->bars[B_DRAIN + 2], 0, &sh->zero, kTimeout);
     }
 }
 
@@ -374,13 +397,9 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         g = nch > 1 ? log_decay(1) : 0.f;
     }
     for (int c = 0; c < nch; ++c) {
-        // A buffer of decays is free when the chunk two before is done with: its V~ by the product
-        // K^T V~ of that chunk, its outputs and state update by P V (OUT) or K^T V~ (state only) of
-        // the chunk in between.
-        if (c > 0 && !wait_warp(sh, B_KV_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
-        if constexpr (OUT) {
-            if (!wait_warp(sh, B_PV_DONE, c)) break;
-        } else {
+        // V~'s place is free when the last chunk's K^T V~ has read it.
+        if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) break;
+        if constexpr (!OUT) {   // (the state update of chunk c - 2, which read these decays' place, came before)
             suf = put(c, g);
             if (c + 1 < nch) g = log_decay(c + 1);
         }
@@ -390,7 +409,8 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
         const __nv_bfloat162 ww1 = __halves2bfloat162(w1, w1), ww2 = __halves2bfloat162(w2, w2);
         const bool live = (long long)c * C + row < len;
-        uint4 *v = reinterpret_cast<uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
+        const uint4 *v = reinterpret_cast<const uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
+        uint4 *hi = reinterpret_cast<uint4 *>(smem + L::HI + row * 128);
         uint4 *lo = reinterpret_cast<uint4 *>(smem + L::LO + row * 128);
         if (live) {
 #pragma unroll
@@ -407,17 +427,17 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
                     split2(in[i].y, ww1, ww2, hi4.y, lo4.y);
                     split2(in[i].z, ww1, ww2, hi4.z, lo4.z);
                     split2(in[i].w, ww1, ww2, hi4.w, lo4.w);
-                    v[x] = hi4;
+                    hi[x] = hi4;
                     lo[x] = lo4;
                 }
             }
         } else {   // a row of another sequence: 0 x NaN must not get into the state
             for (int r = 0; r < DV / 64; ++r)
-                for (int i = 0; i < 8; ++i) v[r * (REGION / 16) + i] = lo[r * (REGION / 16) + i] = zero4();
+                for (int i = 0; i < 8; ++i) hi[r * (REGION / 16) + i] = lo[r * (REGION / 16) + i] = zero4();
         }
-        if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL + (c & 1), c >> 1)) break;
+        if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL, c)) break;
         if (!live) {
-            uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + (c & 1) * L::KT + row * 128);
+            uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + row * 128);
             for (int r = 0; r < DK / 64; ++r)
                 for (int i = 0; i < 8; ++i) k[r * (REGION / 16) + i] = zero4();
         }
@@ -425,7 +445,8 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->bars[B_VT_READY]);
         if constexpr (OUT) {
-            if (c + 1 < nch) {
+            if (c + 1 < nch) {   // the place was chunk c - 1's, whose P and outputs are made
+                if (c > 0 && !wait_warp(sh, B_D2_FREE + ((c - 1) & 1), (c - 1) >> 1)) break;
                 suf = put(c + 1, g);
                 if (c + 2 < nch) g = log_decay(c + 2);
             }
@@ -433,9 +454,44 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
     }
 }
 
+// 16 bytes of an output row from consecutive fp32 values
+template <typename TO>
+__device__ __forceinline__ uint4 pack16(const float *v)
+{
+    if constexpr (sizeof(TO) == 2)
+        return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    else
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+__device__ __forceinline__ uint4 swap16(uint4 a, int mask)
+{
+    a.x = __shfl_xor_sync(0xffffffffu, a.x, mask);
+    a.y = __shfl_xor_sync(0xffffffffu, a.y, mask);
+    a.z = __shfl_xor_sync(0xffffffffu, a.z, mask);
+    a.w = __shfl_xor_sync(0xffffffffu, a.w, mask);
+    return a;
+}
+
+// u[x] of lane m holds unit x of row m (rows of a quad of lanes): afterwards unit m of row x.
+__device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane)
+{
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit <<= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (x & bit) continue;
+            const uint4 got = swap16(up ? u[x] : u[x | bit], bit);
+            if (up) u[x] = got;
+            else u[x | bit] = got;
+        }
+    }
+}
+
 // warps 0-7: thread = key channel / token row 32 (warp % 4) + lane, value channels [DV/2 half, +DV/2)
 template <int DK, int DV, typename TO, bool OUT>
-__device__ void state_role(const Args &p, const CUtensorMap *mo, uint8_t *smem, Shared *sh, uint32_t tm, const Item &it, int item, int h,
+__device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm, const Item &it, int item, int h,
                            int nch)
 {
     using L = Layout<DK, DV>;
@@ -484,78 +540,68 @@ __device__ void state_role(const Args &p, const CUtensorMap *mo, uint8_t *smem, 
     float whole = 1.f;
     const long long len = it.t1 - it.t0;
     for (int c = 0; c < nch; ++c) {
-        bool ok = wait_warp(sh, B_DEC_READY + (c & 1), c >> 1);
+        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return;
         const Decays &d = sh->dec[c & 1];
         const float tot = d.blk[0] * d.blk[1] * d.blk[2] * d.blk[3];
-        whole *= tot;
+        float pre = p.scale;
         if constexpr (OUT) {
-            float pre = scan_up(d.a[row], lane) * p.scale;
+            pre *= scan_up(d.a[row], lane);
             for (int x = 0; x < blk; ++x) pre *= d.blk[x];
-            ok = ok && wait_warp(sh, B_QS_DONE, c) && wait_warp(sh, B_PV_DONE, c);
-            // A whole chunk's bf16 outputs leave by TMA from the state copy's place, which Q S has read
-            // and the next copy is not written to yet: row-per-thread stores of 16 bytes would touch
-            // 32 rows an instruction.  A partial chunk's (and fp32's) rows are stored from here.
-            const bool staged = sizeof(TO) == 2 && DK == 128 && (long long)(c + 1) * C <= len;
-            if (ok) {
-                tc_fence_after();
-                const long long t = (long long)c * C + row;
-                TO *o = static_cast<TO *>(p.out) + ((it.t0 + t) * p.H + h) * p.dv + c0;
-#pragma unroll
-                for (int x = 0; x < N; x += 16) {
-                    uint32_t r1[16], r2[16];
-                    tmem_ld16(tq + TM_D1 + x, r1);
-                    tmem_ld16(tq + TM_D2 + x, r2);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int y = 0; y < 16; y += 8) {
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            v[e] = fmaf(pre, __uint_as_float(r1[y + e]), p.scale * __uint_as_float(r2[y + e]));
-                        const int col = c0 + x + y;
-                        if (staged) {
-                            *reinterpret_cast<uint4 *>(smem + L::S + (col >> 6) * REGION + sw128(row, (col & 63) * 2)) =
-                                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-                        } else if (t < len && col < p.dv) {
-                            store8(o + x + y, v);
-                        }
-                    }
-                }
-                tc_fence_before();
-                arrive(B_D2_FREE);
-                fence_proxy_async_smem();
-            }
-            if (!bar_and(1, 256, ok)) return;   // the group leaves together
-            if (staged && threadIdx.x == 0) {
-                for (int r = 0; r < DV / 64; ++r)
-                    tma_store_3d(mo, smem + L::S + r * REGION, 64 * r, h, (int)(it.t0 + (long long)c * C));
-                bulk_commit();
-            }
         }
-        ok = ok && wait_warp(sh, B_KV_DONE + (c & 1), c >> 1);
-        if (ok) {
-            tc_fence_after();
+        whole *= tot;
+        // the state first: the next chunk's Q S waits for it
+        if (!wait_warp(sh, B_KV_DONE, c)) return;
+        tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < N; x += 32) {
-                uint32_t r[32];
-                tmem_ld32(tq + TM_DST + x, r);
-                tmem_wait_ld();
+        for (int x = 0; x < N; x += 32) {
+            uint32_t r[32];
+            tmem_ld32(tq + TM_DST + x, r);
+            tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
-            }
-            tc_fence_before();
+            for (int e = 0; e < 32; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
         }
+        tc_fence_before();
+        arrive(B_DST_FREE);
         if constexpr (OUT) {
-            if (threadIdx.x == 0) bulk_wait_read_all();   // the outputs' store has read the place
-            if (!bar_and(1, 256, ok)) return;
+            if (!wait_warp(sh, B_QS_DONE, c)) return;
             if (c + 1 < nch) {
                 copy_state();
                 arrive(B_ST_READY);
             }
-        } else {
-            if (!ok) return;
-            arrive(B_ST_READY);
+            if (!wait_warp(sh, B_PV_DONE + (c & 1), c >> 1)) return;
+            tc_fence_after();
+            // Rows leave in pieces of four 16-byte units: a quad of lanes, which holds four rows, turns
+            // its units around so that it stores one row's four units side by side.  (A row per lane
+            // would touch 32 rows an instruction.)
+            const float scale = p.scale;
+            constexpr int UNIT = 16 / sizeof(TO), COLS = 4 * UNIT;
+            const long long t = (long long)c * C + (row & ~3);
+            TO *o = static_cast<TO *>(p.out) + ((it.t0 + t) * p.H + h) * p.dv;
+            const long long step = (long long)p.H * p.dv;
+            const int left = (int)min((long long)4, len - t);   // rows of the quad to store, may be <= 0
+#pragma unroll
+            for (int x = 0; x < N; x += COLS) {
+                uint4 u[4];
+#pragma unroll
+                for (int y = 0; y < COLS; y += 8) {
+                    uint32_t r1[8], r2[8];
+                    float v[8];
+                    tmem_ld8(tq + TM_D1 + x + y, r1);
+                    tmem_ld8(tq + TM_D2 + x + y, r2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = fmaf(pre, __uint_as_float(r1[e]), scale * __uint_as_float(r2[e]));
+#pragma unroll
+                    for (int e = 0; e < 8; e += UNIT) u[(y + e) / UNIT] = pack16<TO>(v + e);
+                }
+                transpose4(u, lane);
+                const int col = c0 + x + UNIT * (lane & 3);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (y < left && col < p.dv) *reinterpret_cast<uint4 *>(o + y * step + col) = u[y];
+            }
+            tc_fence_before();
+            arrive(B_D2_FREE + (c & 1));
         }
     }
     float *to = nullptr;
@@ -572,7 +618,7 @@ __device__ void state_role(const Args &p, const CUtensorMap *mo, uint8_t *smem, 
 template <int DK, int DV, typename TO, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, const Args p)
+                 const __grid_constant__ CUtensorMap mv, const Args p)
 {
     using L = Layout<DK, DV>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -589,7 +635,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         for (int b = 0; b < B_COUNT; ++b) {
             int n = 1;
             if (b == B_P_READY || b == B_VT_READY || b == B_DEC_READY || b == B_DEC_READY + 1) n = 4;
-            if (b == B_ST_READY || b == B_D2_FREE) n = 8;
+            if (b == B_ST_READY || b == B_DST_FREE || b == B_D2_FREE || b == B_D2_FREE + 1) n = 8;
             mbar_init(&sh->bars[b], n);
         }
         sh->abort = 0;
@@ -610,19 +656,21 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const long long len = it.t1 - it.t0;
     const int nch = (int)((len + C - 1) / C);
     if (warp < 8) {
-        regs_up<kRegsState>();
-        state_role<DK, DV, TO, OUT>(p, &mo, smem, sh, tm, it, item, h, nch);
+        regs_up<kRegsState[OUT]>();
+        state_role<DK, DV, TO, OUT>(p, smem, sh, tm, it, item, h, nch);
     } else if (warp < 12) {
-        if (OUT) score_role<DK, DV>(smem, sh, tm, len, nch);
+        if constexpr (!OUT) regs_down<kRegsScore>();
+        if constexpr (OUT) score_role<DK, DV>(smem, sh, tm, len, nch);
     } else if (warp < 16) {
-        regs_down<kRegsValue>();
+        regs_down<kRegsValue[OUT]>();
         if (nch > 0) value_role<DK, DV, OUT>(p, smem, sh, h, it.t0, len, nch);
     } else {
-        regs_down<kRegsIssue>();
-        if (warp == 16 && (threadIdx.x & 31) == 0 && nch > 0)
+        if constexpr (OUT) regs_down<kRegsIssue>();
+        if (warp == 16 && nch > 0)
             load_role<DK, DV, OUT>(&mq, &mk, &mv, smem, sh, h, h / p.group, it.t0, nch);
         if (warp == 17 && OUT && nch > 0) score_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
-        if (warp == 18 && nch > 0) state_mma_role<DK, DV, OUT>(smem_u32(smem), sh, tm, nch);
+        if (warp == 18 && nch > 0) update_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
+        if (warp == 19 && OUT && nch > 0) read_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
     }
     tc_fence_before();
     __syncthreads();
@@ -670,7 +718,7 @@ bool launch_one(const CUtensorMap *m, const Args &p, cudaStream_t stream)
     if (cudaFuncSetAttribute(linear_tc_kernel<DK, DV, TO, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess)
         return false;
-    linear_tc_kernel<DK, DV, TO, OUT><<<(unsigned)(p.items * p.H), kThreads, bytes, stream>>>(m[0], m[1], m[2], m[3], p);
+    linear_tc_kernel<DK, DV, TO, OUT><<<(unsigned)(p.items * p.H), kThreads, bytes, stream>>>(m[0], m[1], m[2], p);
     return cudaGetLastError() == cudaSuccess;
 }
 
@@ -690,10 +738,9 @@ int run_dims(const CUtensorMap *m, const Args &p, int out_dtype, cudaStream_t st
 
 int run_tc_path(const Args &p, int out_dtype, cudaStream_t stream)
 {
-    CUtensorMap m[4];
+    CUtensorMap m[3];
     if (!make_map(&m[0], p.q, p.H, p.dk, p.T) || !make_map(&m[1], p.k, p.H / p.group, p.dk, p.T) ||
-        !make_map(&m[2], p.v, p.H / p.group, p.dv, p.T) ||
-        !make_map(&m[3], p.out, p.H, p.dv, p.T))   // used for bf16 outputs only
+        !make_map(&m[2], p.v, p.H / p.group, p.dv, p.T))
         return KDA_ERR_CUDA;
     if (p.dk <= 64) return p.dv <= 64 ? run_dims<64, 64>(m, p, out_dtype, stream) : run_dims<64, 128>(m, p, out_dtype, stream);
     return p.dv <= 64 ? run_dims<128, 64>(m, p, out_dtype, stream) : run_dims<128, 128>(m, p, out_dtype, stream);
