@@ -23,10 +23,11 @@
 //
 // One CTA works through the chunks of one (segment, head).  Roles, joined by mbarriers:
 //   warps 0-7    the state update: 64 (dv = 128) state columns of one key channel per thread, and the
-//                state's bf16 copy; then the chunk's outputs, scale (p D1 + D2) -> global
-//   warps 8-11   scores -> P, one token row per thread
-//   warps 12-15  the chunk's decays, and V~
-//   warp 16      TMA loads: q and k one tile, v two;  warps 17, 18, 19  issue Q K^T and P V;  K^T V~;  Q S
+//                state's bf16 copy
+//   warps 8-15   the chunk's outputs, scale (p D1 + D2) -> global
+//   warps 16-19  scores -> P, one token row per thread
+//   warps 20-23  the chunk's decays, and V~
+//   warp 24      TMA loads: q and k one tile, v two;  warps 25, 26, 27  issue Q K^T and P V;  K^T V~;  Q S
 // Three issuing warps, because scores, state and outputs of neighbouring chunks overlap.
 #include <cudaTypedefs.h>
 
@@ -42,11 +43,19 @@ namespace {
 using namespace ptx;
 
 constexpr int C = 128;                          // tokens of a chunk
-constexpr int kThreads = 5 * 128;
-// Registers a thread of each warpgroup, 96 at launch: 2 x 120 + 96 + 64 + 80 = 5 x 96 with outputs,
-// 2 x 136 + 40 + 72 + 96 = 5 x 96 for states alone.  What does not fit spills to local memory, and with
-// this much shared memory nearly every reload of it comes from L2.
-constexpr int kRegsState[2] = {136, 120}, kRegsScore = 40, kRegsValue[2] = {72, 64}, kRegsIssue = 80;
+constexpr int kThreads = 7 * 128;
+// Registers a thread of each warpgroup, 72 at launch: 2 x 104 + 2 x 56 + 64 + 56 + 64 = 7 x 72 with
+// outputs, 2 x 120 + 2 x 24 + 24 + 80 + 64 for states alone.  What does not fit spills to local memory,
+// and with this much shared memory nearly every reload of it comes from L2.
+constexpr int kRegsState[2] = {120, 104}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {24, 64};
+constexpr int kRegsValue[2] = {80, 56}, kRegsIssue = 64;
+template <int N>
+__device__ __forceinline__ void set_regs()
+{
+    if constexpr (N > 72) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 constexpr long long kTimeout = 4000000000ll;    // bounded waits: 4e9 SM cycles (~2 s)
 constexpr uint32_t REGION = C * 128;            // 64 channels x 128 tokens
 
@@ -60,7 +69,7 @@ struct Decays {
 
 enum Bar {
     B_QFULL, B_KFULL, B_VFULL, B_SC_DONE = B_VFULL + 2, B_P_READY, B_PV_DONE, B_QS_DONE = B_PV_DONE + 2, B_VT_READY, B_KV_DONE,
-    B_ST_READY, B_DST_FREE, B_D2_FREE, B_DEC_READY = B_D2_FREE + 2, B_DRAIN = B_DEC_READY + 2, B_COUNT = B_DRAIN + 3
+    B_ST_READY, B_DST_FREE, B_D2_FREE = B_DST_FREE + 2, B_DEC_READY = B_D2_FREE + 2, B_DRAIN = B_DEC_READY + 2, B_COUNT = B_DRAIN + 3
 };
 
 struct Shared {
@@ -143,8 +152,18 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return v;
 }
 
-template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r, x, y, z;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+
 
 template <int DK, int DV, bool OUT>
 __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv, uint8_t *smem,
@@ -243,7 +262,7 @@ __device__ void update_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     const uint64_t hi = smem_desc(sb + L::HI, REGION, 1024), lo = smem_desc(sb + L::LO, REGION, 1024);
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
-        ok = wait_warp(sh, B_VT_READY, c) && wait_warp(sh, B_KFULL, c) && (c == 0 || wait_warp(sh, B_DST_FREE, c - 1));
+        ok = wait_warp(sh, B_VT_READY, c) && wait_warp(sh, B_KFULL, c) && (c == 0 || wait_warp(sh, B_DST_FREE + ((c - 1) & 1), (c - 1) >> 1));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -288,7 +307,7 @@ __device__ void read_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     }
 }
 
-// warps 8-11: thread = token row 32 blk + lane
+// warps 16-19: thread = token row 32 blk + lane
 template <int DK, int DV>
 __device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len, int nch)
 {
@@ -362,7 +381,7 @@ __device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len
     }
 }
 
-// warps 12-15: the chunk's decays, and V~
+// warps 20-23: the chunk's decays, and V~
 template <int DK, int DV, bool OUT>
 __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long long t0, long long len, int nch)
 {
@@ -413,23 +432,21 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         uint4 *hi = reinterpret_cast<uint4 *>(smem + L::HI + row * 128);
         uint4 *lo = reinterpret_cast<uint4 *>(smem + L::LO + row * 128);
         if (live) {
+            uint4 in[4];
+            auto at = [&](int x) { return (x >> 3) * (int)(REGION / 16) + ((x & 7) ^ (lane & 7)); };
 #pragma unroll
-            for (int r = 0; r < DV / 32; ++r) {
-                uint4 in[4];
+            for (int i = 0; i < 4; ++i) in[i] = v[at(i)];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    in[i] = v[(r >> 1) * (int)(REGION / 16) + (((r & 1) * 4 + i) ^ (lane & 7))];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int x = (r >> 1) * (int)(REGION / 16) + (((r & 1) * 4 + i) ^ (lane & 7));
-                    uint4 hi4, lo4;
-                    split2(in[i].x, ww1, ww2, hi4.x, lo4.x);
-                    split2(in[i].y, ww1, ww2, hi4.y, lo4.y);
-                    split2(in[i].z, ww1, ww2, hi4.z, lo4.z);
-                    split2(in[i].w, ww1, ww2, hi4.w, lo4.w);
-                    hi[x] = hi4;
-                    lo[x] = lo4;
-                }
+            for (int x = 0; x < DV / 8; ++x) {   // four loads stay in flight
+                const uint4 u = in[x & 3];
+                if (x + 4 < DV / 8) in[x & 3] = v[at(x + 4)];
+                uint4 hi4, lo4;
+                split2(u.x, ww1, ww2, hi4.x, lo4.x);
+                split2(u.y, ww1, ww2, hi4.y, lo4.y);
+                split2(u.z, ww1, ww2, hi4.z, lo4.z);
+                split2(u.w, ww1, ww2, hi4.w, lo4.w);
+                hi[at(x)] = hi4;
+                lo[at(x)] = lo4;
             }
         } else {   // a row of another sequence: 0 x NaN must not get into the state
             for (int r = 0; r < DV / 64; ++r)
@@ -446,7 +463,8 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         if (lane == 0) mbar_arrive(&sh->bars[B_VT_READY]);
         if constexpr (OUT) {
             if (c + 1 < nch) {   // the place was chunk c - 1's, whose P and outputs are made
-                if (c > 0 && !wait_warp(sh, B_D2_FREE + ((c - 1) & 1), (c - 1) >> 1)) break;
+                const int s = (c - 1) & 1, f = (c - 1) >> 1;
+                if (c > 0 && !(wait_warp(sh, B_D2_FREE + s, f) && wait_warp(sh, B_DST_FREE + s, f))) break;
                 suf = put(c + 1, g);
                 if (c + 2 < nch) g = log_decay(c + 2);
             }
@@ -489,8 +507,8 @@ __device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane)
     }
 }
 
-// warps 0-7: thread = key channel / token row 32 (warp % 4) + lane, value channels [DV/2 half, +DV/2)
-template <int DK, int DV, typename TO, bool OUT>
+// warps 0-7: thread = key channel 32 (warp % 4) + lane, value channels [DV/2 half, +DV/2)
+template <int DK, int DV, bool OUT>
 __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm, const Item &it, int item, int h,
                            int nch)
 {
@@ -543,13 +561,7 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
         if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return;
         const Decays &d = sh->dec[c & 1];
         const float tot = d.blk[0] * d.blk[1] * d.blk[2] * d.blk[3];
-        float pre = p.scale;
-        if constexpr (OUT) {
-            pre *= scan_up(d.a[row], lane);
-            for (int x = 0; x < blk; ++x) pre *= d.blk[x];
-        }
         whole *= tot;
-        // the state first: the next chunk's Q S waits for it
         if (!wait_warp(sh, B_KV_DONE, c)) return;
         tc_fence_after();
 #pragma unroll
@@ -561,47 +573,13 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
             for (int e = 0; e < 32; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
         }
         tc_fence_before();
-        arrive(B_DST_FREE);
+        arrive(B_DST_FREE + (c & 1));
         if constexpr (OUT) {
             if (!wait_warp(sh, B_QS_DONE, c)) return;
             if (c + 1 < nch) {
                 copy_state();
                 arrive(B_ST_READY);
             }
-            if (!wait_warp(sh, B_PV_DONE + (c & 1), c >> 1)) return;
-            tc_fence_after();
-            // Rows leave in pieces of four 16-byte units: a quad of lanes, which holds four rows, turns
-            // its units around so that it stores one row's four units side by side.  (A row per lane
-            // would touch 32 rows an instruction.)
-            const float scale = p.scale;
-            constexpr int UNIT = 16 / sizeof(TO), COLS = 4 * UNIT;
-            const long long t = (long long)c * C + (row & ~3);
-            TO *o = static_cast<TO *>(p.out) + ((it.t0 + t) * p.H + h) * p.dv;
-            const long long step = (long long)p.H * p.dv;
-            const int left = (int)min((long long)4, len - t);   // rows of the quad to store, may be <= 0
-#pragma unroll
-            for (int x = 0; x < N; x += COLS) {
-                uint4 u[4];
-#pragma unroll
-                for (int y = 0; y < COLS; y += 8) {
-                    uint32_t r1[8], r2[8];
-                    float v[8];
-                    tmem_ld8(tq + TM_D1 + x + y, r1);
-                    tmem_ld8(tq + TM_D2 + x + y, r2);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = fmaf(pre, __uint_as_float(r1[e]), scale * __uint_as_float(r2[e]));
-#pragma unroll
-                    for (int e = 0; e < 8; e += UNIT) u[(y + e) / UNIT] = pack16<TO>(v + e);
-                }
-                transpose4(u, lane);
-                const int col = c0 + x + UNIT * (lane & 3);
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    if (y < left && col < p.dv) *reinterpret_cast<uint4 *>(o + y * step + col) = u[y];
-            }
-            tc_fence_before();
-            arrive(B_D2_FREE + (c & 1));
         }
     }
     float *to = nullptr;
@@ -613,6 +591,64 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
             if (c0 + x < p.dv) *reinterpret_cast<float4 *>(to + x) = make_float4(st[x], st[x + 1], st[x + 2], st[x + 3]);
     }
     if (!OUT && threadIdx.x == 0) p.decays[(long long)item * p.H + h] = whole;
+}
+
+// warps 8-15: thread = token row 32 (warp % 4) + lane, value channels [DV/2 half, +DV/2)
+template <int DV, typename TO>
+__device__ void output_role(const Args &p, Shared *sh, uint32_t tm, const Item &it, int h, int nch)
+{
+    constexpr int N = DV / 2, UNIT = 16 / sizeof(TO), COLS = 4 * UNIT;
+    const int warp = threadIdx.x >> 5, blk = warp & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
+    const int c0 = ((warp >> 2) & 1) * N;
+    const uint32_t tq = tm + ((uint32_t)(32 * blk) << 16) + c0;
+    const long long len = it.t1 - it.t0, step = (long long)p.H * p.dv;
+    // Rows leave in pieces of four 16-byte units: a quad of lanes, which holds four rows, turns its
+    // units around so that it stores one row's four units side by side.  (A row per lane would touch
+    // 32 rows an instruction.)
+    long long t = row & ~3;
+    TO *o = static_cast<TO *>(p.out) + ((it.t0 + t) * p.H + h) * p.dv + c0 + UNIT * (lane & 3);
+    const int cols = p.dv - c0 - UNIT * (lane & 3);
+    const float2 scale = make_float2(p.scale, p.scale);
+    for (int c = 0; c < nch; ++c, t += C, o += C * step) {
+        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return;
+        const Decays &d = sh->dec[c & 1];
+        float f = p.scale * scan_up(d.a[row], lane);
+        for (int x = 0; x < blk; ++x) f *= d.blk[x];
+        const float2 pre = make_float2(f, f);
+        if (!wait_warp(sh, B_QS_DONE, c) || !wait_warp(sh, B_PV_DONE + (c & 1), c >> 1)) return;
+        tc_fence_after();
+        const long long left = len - t;   // rows of the quad to store, may be <= 0
+#pragma unroll
+        for (int x = 0; x < N; x += COLS) {
+            uint4 u[4];
+#pragma unroll
+            for (int y = 0; y < COLS; y += 8) {
+                uint32_t r1[8], r2[8];
+                float v[8];
+                tmem_ld8(tq + TM_D1 + x + y, r1);
+                tmem_ld8(tq + TM_D2 + x + y, r2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 s2 = mul2(scale, make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1])));
+                    const float2 w = fma2(pre, make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])), s2);
+                    v[e] = w.x;
+                    v[e + 1] = w.y;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e += UNIT) u[(y + e) / UNIT] = pack16<TO>(v + e);
+            }
+            if (x + COLS >= N) {   // everything is read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->bars[B_D2_FREE + (c & 1)]);
+            }
+            transpose4(u, lane);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (y < left && x < cols) *reinterpret_cast<uint4 *>(o + y * step + x) = u[y];
+        }
+    }
 }
 
 template <int DK, int DV, typename TO, bool OUT>
@@ -635,7 +671,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         for (int b = 0; b < B_COUNT; ++b) {
             int n = 1;
             if (b == B_P_READY || b == B_VT_READY || b == B_DEC_READY || b == B_DEC_READY + 1) n = 4;
-            if (b == B_ST_READY || b == B_DST_FREE || b == B_D2_FREE || b == B_D2_FREE + 1) n = 8;
+            if (b >= B_ST_READY && b < B_DEC_READY) n = 8;
             mbar_init(&sh->bars[b], n);
         }
         sh->abort = 0;
@@ -645,7 +681,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         tma_prefetch_desc(&mk);
         tma_prefetch_desc(&mv);
     }
-    if (warp == 17) {
+    if (warp == 25) {
         tmem_alloc(&sh->tmem, TM_COLS);
         tmem_relinquish();
     }
@@ -656,26 +692,29 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const long long len = it.t1 - it.t0;
     const int nch = (int)((len + C - 1) / C);
     if (warp < 8) {
-        regs_up<kRegsState[OUT]>();
-        state_role<DK, DV, TO, OUT>(p, smem, sh, tm, it, item, h, nch);
-    } else if (warp < 12) {
-        if constexpr (!OUT) regs_down<kRegsScore>();
-        if constexpr (OUT) score_role<DK, DV>(smem, sh, tm, len, nch);
+        set_regs<kRegsState[OUT]>();
+        state_role<DK, DV, OUT>(p, smem, sh, tm, it, item, h, nch);
     } else if (warp < 16) {
-        regs_down<kRegsValue[OUT]>();
+        set_regs<kRegsOut[OUT]>();
+        if constexpr (OUT) output_role<DV, TO>(p, sh, tm, it, h, nch);
+    } else if (warp < 20) {
+        set_regs<kRegsScore[OUT]>();
+        if constexpr (OUT) score_role<DK, DV>(smem, sh, tm, len, nch);
+    } else if (warp < 24) {
+        set_regs<kRegsValue[OUT]>();
         if (nch > 0) value_role<DK, DV, OUT>(p, smem, sh, h, it.t0, len, nch);
     } else {
-        if constexpr (OUT) regs_down<kRegsIssue>();
-        if (warp == 16 && nch > 0)
+        set_regs<kRegsIssue>();
+        if (warp == 24 && nch > 0)
             load_role<DK, DV, OUT>(&mq, &mk, &mv, smem, sh, h, h / p.group, it.t0, nch);
-        if (warp == 17 && OUT && nch > 0) score_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
-        if (warp == 18 && nch > 0) update_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
-        if (warp == 19 && OUT && nch > 0) read_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
+        if (warp == 25 && OUT && nch > 0) score_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
+        if (warp == 26 && nch > 0) update_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
+        if (warp == 27 && OUT && nch > 0) read_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 17) tmem_dealloc(tm, TM_COLS);
+    if (warp == 25) tmem_dealloc(tm, TM_COLS);
 }
 
 // ---------------------------------------------------------------------------------------------
