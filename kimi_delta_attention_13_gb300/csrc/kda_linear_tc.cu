@@ -45,10 +45,10 @@ using namespace ptx;
 constexpr int C = 128;                          // tokens of a chunk
 constexpr int kThreads = 7 * 128;
 // Registers a thread of each warpgroup, 72 at launch: 2 x 104 + 2 x 56 + 64 + 56 + 64 = 7 x 72 with
-// outputs, 2 x 120 + 2 x 24 + 24 + 80 + 64 for states alone.  What does not fit spills to local memory,
+// outputs, 2 x 120 + 2 x 24 + 72 + 72 + 64 for states alone.  What does not fit spills to local memory,
 // and with this much shared memory nearly every reload of it comes from L2.
-constexpr int kRegsState[2] = {120, 104}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {24, 64};
-constexpr int kRegsValue[2] = {80, 56}, kRegsIssue = 64;
+constexpr int kRegsState[2] = {120, 104}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {72, 64};
+constexpr int kRegsValue[2] = {72, 56}, kRegsIssue = 64;
 template <int N>
 __device__ __forceinline__ void set_regs()
 {
@@ -381,17 +381,20 @@ __device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len
     }
 }
 
-// warps 20-23: the chunk's decays, and V~
+// warps 20-23: the chunk's decays, and V~; for states alone warps 16-19 take the first half of a row's
+// channels off them
 template <int DK, int DV, bool OUT>
 __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long long t0, long long len, int nch)
 {
+    constexpr int UNITS = DV / 8 / (OUT ? 1 : 2);   // 16-byte units of a row for this thread
+    const bool main = OUT || threadIdx.x >= 20 * 32;
+    const int first = main && !OUT ? UNITS : 0;
     using L = Layout<DK, DV>;
     const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
     auto log_decay = [&](int c) {
         const long long t = (long long)c * C + row;
         return t < len ? (p.g_per_token ? p.g[(t0 + t) * p.H + h] : p.g[h]) : 0.f;
     };
-    // returns the product of the decays after this thread's token within its block
     auto put = [&](int c, float g) {
         Decays &d = sh->dec[c & 1];
         const float a = expf(g);
@@ -408,22 +411,21 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         d.suf[row] = suf;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->bars[B_DEC_READY + (c & 1)]);
-        return suf;
     };
-    float g = log_decay(0), suf = 0.f;
+    float g = log_decay(0);
     if constexpr (OUT) {
-        suf = put(0, g);
+        put(0, g);
         g = nch > 1 ? log_decay(1) : 0.f;
     }
     for (int c = 0; c < nch; ++c) {
         // V~'s place is free when the last chunk's K^T V~ has read it.
         if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) break;
-        if constexpr (!OUT) {   // (the state update of chunk c - 2, which read these decays' place, came before)
-            suf = put(c, g);
+        if (!OUT && main) {   // (the state update of chunk c - 2, which read these decays' place, came before)
+            put(c, g);
             if (c + 1 < nch) g = log_decay(c + 1);
         }
         if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) break;
-        float w = suf;
+        float w = sh->dec[c & 1].suf[row];
         for (int x = blk + 1; x < 4; ++x) w *= sh->dec[c & 1].blk[x];
         const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
         const __nv_bfloat162 ww1 = __halves2bfloat162(w1, w1), ww2 = __halves2bfloat162(w2, w2);
@@ -431,26 +433,26 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         const uint4 *v = reinterpret_cast<const uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
         uint4 *hi = reinterpret_cast<uint4 *>(smem + L::HI + row * 128);
         uint4 *lo = reinterpret_cast<uint4 *>(smem + L::LO + row * 128);
+        // unit x of the row, in an order that keeps eight rows' accesses in different banks
+        auto at = [&](int x) { return (x >> 3) * (int)(REGION / 16) + ((x & 7) ^ (lane & 7)); };
         if (live) {
             uint4 in[4];
-            auto at = [&](int x) { return (x >> 3) * (int)(REGION / 16) + ((x & 7) ^ (lane & 7)); };
 #pragma unroll
-            for (int i = 0; i < 4; ++i) in[i] = v[at(i)];
+            for (int i = 0; i < 4; ++i) in[i] = v[at(first + i)];
 #pragma unroll
-            for (int x = 0; x < DV / 8; ++x) {   // four loads stay in flight
+            for (int x = 0; x < UNITS; ++x) {   // four loads stay in flight
                 const uint4 u = in[x & 3];
-                if (x + 4 < DV / 8) in[x & 3] = v[at(x + 4)];
+                if (x + 4 < UNITS) in[x & 3] = v[at(first + x + 4)];
                 uint4 hi4, lo4;
                 split2(u.x, ww1, ww2, hi4.x, lo4.x);
                 split2(u.y, ww1, ww2, hi4.y, lo4.y);
                 split2(u.z, ww1, ww2, hi4.z, lo4.z);
                 split2(u.w, ww1, ww2, hi4.w, lo4.w);
-                hi[at(x)] = hi4;
-                lo[at(x)] = lo4;
+                hi[at(first + x)] = hi4;
+                lo[at(first + x)] = lo4;
             }
         } else {   // a row of another sequence: 0 x NaN must not get into the state
-            for (int r = 0; r < DV / 64; ++r)
-                for (int i = 0; i < 8; ++i) hi[r * (REGION / 16) + i] = lo[r * (REGION / 16) + i] = zero4();
+            for (int x = first; x < first + UNITS; ++x) hi[at(x)] = lo[at(x)] = zero4();
         }
         if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL, c)) break;
         if (!live) {
@@ -465,7 +467,7 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
             if (c + 1 < nch) {   // the place was chunk c - 1's, whose P and outputs are made
                 const int s = (c - 1) & 1, f = (c - 1) >> 1;
                 if (c > 0 && !(wait_warp(sh, B_D2_FREE + s, f) && wait_warp(sh, B_DST_FREE + s, f))) break;
-                suf = put(c + 1, g);
+                put(c + 1, g);
                 if (c + 2 < nch) g = log_decay(c + 2);
             }
         }
@@ -671,6 +673,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         for (int b = 0; b < B_COUNT; ++b) {
             int n = 1;
             if (b == B_P_READY || b == B_VT_READY || b == B_DEC_READY || b == B_DEC_READY + 1) n = 4;
+            if (b == B_VT_READY && !OUT) n = 8;
             if (b >= B_ST_READY && b < B_DEC_READY) n = 8;
             mbar_init(&sh->bars[b], n);
         }
@@ -700,6 +703,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     } else if (warp < 20) {
         set_regs<kRegsScore[OUT]>();
         if constexpr (OUT) score_role<DK, DV>(smem, sh, tm, len, nch);
+        else if (nch > 0) value_role<DK, DV, OUT>(p, smem, sh, h, it.t0, len, nch);
     } else if (warp < 24) {
         set_regs<kRegsValue[OUT]>();
         if (nch > 0) value_role<DK, DV, OUT>(p, smem, sh, h, it.t0, len, nch);

@@ -30,39 +30,85 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// ---------------------------------------------------------------------------------------------
-// norm_gate: GROUP lanes of a warp hold one (token, head) row, 8 channels each
+// 8 elements as loaded: packed until they are used, so that many loads stay in flight at few registers
+template <typename T>
+struct Raw8 {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p)   // read once: past the L1
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u[i].x), "=r"(u[i].y), "=r"(u[i].z), "=r"(u[i].w) : "l"(p + i * 4));
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void unpack(float (&v)[8]) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+            const uint4 a = u[0], b = u[1];
+            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z);
+            v[3] = __uint_as_float(a.w); v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
+            v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+        }
+    }
+};
 
-template <typename TX, typename TZ, typename TO, int GROUP>
-__global__ void __launch_bounds__(256) norm_gate_kernel(const TX *o, const TZ *z,
-                                                        const float *__restrict__ w, TO *out, long long rows,
-                                                        int H, int w_heads, int d, float eps)
+// ---------------------------------------------------------------------------------------------
+// norm_gate: GROUP lanes of a warp hold one (token, head) row, 8 channels each; a group takes DEPTH
+// rows at a time, all of whose loads go out first
+
+template <typename TX, typename TZ, typename TO, int GROUP, int DEPTH>
+__global__ void __launch_bounds__(256) norm_gate_kernel(const TX *o, const TZ *z, const float *__restrict__ w,
+                                                        TO *out, long long rows, int H, int w_heads, int d, float eps)
 {
-    constexpr int PER = 256 / GROUP;   // rows of a block at a time
+    constexpr int PER = 256 / GROUP;   // rows of a block side by side
     const int lane = threadIdx.x % GROUP;
     const bool ok = 8 * lane < d;
     const float inv_d = 1.f / (float)d;
-    for (long long r = (long long)blockIdx.x * PER + threadIdx.x / GROUP; r - threadIdx.x / GROUP < rows;
-         r += (long long)gridDim.x * PER) {
-        const bool live = ok && r < rows;
-        const long long at = r * d + 8 * lane;
-        float x[8] = {}, g[8] = {};
-        if (live) {
-            load8(o + at, x);
-            load8(z + at, g);
+    const long long r0 = (long long)blockIdx.x * PER * DEPTH + threadIdx.x / GROUP;
+    Raw8<TX> x[DEPTH];
+    Raw8<TZ> g[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+        const long long r = r0 + i * PER;
+        if (ok && r < rows) {
+            x[i].load(o + r * d + 8 * lane);
+            g[i].load(z + r * d + 8 * lane);
+        } else {
+            x[i].zero();
+            g[i].zero();
         }
+    }
+    float wv[8] = {};
+    if (ok && w_heads == 1) load8(w + 8 * lane, wv);
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+        const long long r = r0 + i * PER;
+        float v[8], gv[8];
+        x[i].unpack(v);
+        g[i].unpack(gv);
         float ss = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) ss = fmaf(x[c], x[c], ss);
+        for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
 #pragma unroll
         for (int m = GROUP / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         const float inv = rsqrtf(fmaf(ss, inv_d, eps));
-        if (live) {
-            float wv[8];
-            load8(w + (w_heads > 1 ? r % H * d : 0) + 8 * lane, wv);
+        if (ok && r < rows) {
+            if (w_heads > 1) load8(w + r % H * d + 8 * lane, wv);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] *= inv * wv[c] * gate<TO>(g[c]);
-            store8(out + at, x);
+            for (int c = 0; c < 8; ++c) v[c] *= inv * wv[c] * gate<TO>(gv[c]);
+            store8(out + r * d + 8 * lane, v);
         }
     }
 }
@@ -93,57 +139,74 @@ __device__ __forceinline__ float block_sum(float x, float *buf)
     return x;
 }
 
+// The row's inputs are loaded at once and stay packed; where that leaves 64 registers a thread
+// enough, 1024 threads of several blocks share an SM, one's loads beside another's sums.
+template <typename TR, typename TB, int VECS>
+constexpr bool fits64() { return 2 * VECS * (sizeof(TR) + 2 * sizeof(TB)) <= 36; }
+
 template <typename TR, typename TB, int THREADS, int VECS>
-__global__ void __launch_bounds__(THREADS) residual_norm_kernel(const ResidualArgs p)
+__global__ void __launch_bounds__(THREADS, fits64<TR, TB, VECS>() ? 1024 / THREADS : 1) residual_norm_kernel(const ResidualArgs p)
 {
     __shared__ float buf[2][32];
     const long long row = blockIdx.x, base = row * p.D;
     const TR *x = static_cast<const TR *>(p.x) + base;
     const TB *y = p.y ? static_cast<const TB *>(p.y) + base : nullptr;
     const TB *z = p.z ? static_cast<const TB *>(p.z) + base : nullptr;
-    float r[VECS][8], u[VECS][8], gz[VECS][8];
+    Raw8<TR> xr[VECS];
+    Raw8<TB> yr[VECS], zr[VECS];
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         const int c = (i * THREADS + threadIdx.x) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] = u[i][e] = gz[i][e] = 0.f;
+        yr[i].zero();
+        xr[i].zero();
+        zr[i].zero();
         if (c < p.D) {
-            if (y) load8(y + c, u[i]);
-            load8(x + c, r[i]);
-            if (z) load8(z + c, gz[i]);
+            if (y) yr[i].load(y + c);
+            xr[i].load(x + c);
+            if (z) zr[i].load(z + c);
         }
     }
-    if (y) {
-        float inv = p.scale;
-        if (p.w_post) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < VECS; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(u[i][e], u[i][e], ss);
-            inv = p.scale * rsqrtf(block_sum<THREADS>(ss, buf[0]) / (float)p.D + p.eps);
-        }
+    float inv_post = p.scale;
+    if (y && p.w_post) {
+        float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < VECS; ++i) {
-            const int c = (i * THREADS + threadIdx.x) * 8;
-            if (c >= p.D) continue;
-            float wp[8];
-            if (p.w_post) load8(p.w_post + c, wp);
+            float u[8];
+            yr[i].unpack(u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float t = u[i][e] * inv;
-                if (p.w_post) t *= wp[e];
-                if (z) t *= gate<TB>(gz[i][e]);
-                r[i][e] += t;
+            for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
+        }
+        inv_post = p.scale * rsqrtf(block_sum<THREADS>(ss, buf[0]) / (float)p.D + p.eps);
+    }
+    float r[VECS][8], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        const int c = (i * THREADS + threadIdx.x) * 8;
+        xr[i].unpack(r[i]);
+        if (y && c < p.D) {
+            float u[8];
+            yr[i].unpack(u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] *= inv_post;
+            if (p.w_post) {
+                float wp[8];
+                load8(p.w_post + c, wp);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] *= wp[e];
             }
+            if (z) {
+                float g[8];
+                zr[i].unpack(g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] *= gate<TB>(g[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[i][e] += u[e];
             store8(static_cast<TR *>(p.res) + base + c, r[i]);
         }
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < VECS; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(r[i][e], r[i][e], ss);
+    }
     const float inv = rsqrtf(block_sum<THREADS>(ss, buf[1]) / (float)p.D + p.eps);
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
@@ -227,10 +290,15 @@ int launch_norm_gate(const void *o, int o_dtype, const void *z, int z_dtype, con
         using Z = decltype(zt);
         using O = decltype(ot);
         auto launch = [&](auto group) {
-            constexpr int G = decltype(group)::value;
-            const long long want = (rows + 256 / G - 1) / (256 / G), cap = 152 * 8;
-            norm_gate_kernel<X, Z, O, G><<<(unsigned)(want < cap ? want : cap), 256, 0, stream>>>(
-                (const X *)o, (const Z *)z, w, (O *)out, rows, H, w_heads, d, eps);
+            constexpr int G = decltype(group)::value, PER = 256 / G, DEPTH = 4;
+            auto run = [&](auto depth) {
+                constexpr int N = decltype(depth)::value;
+                norm_gate_kernel<X, Z, O, G, N><<<(unsigned)((rows + PER * N - 1) / (PER * N)), 256, 0, stream>>>(
+                    (const X *)o, (const Z *)z, w, (O *)out, rows, H, w_heads, d, eps);
+            };
+            // few rows: one at a time, so that more blocks take part
+            if (rows >= 152ll * 8 * PER * DEPTH) run(std::integral_constant<int, DEPTH>{});
+            else run(std::integral_constant<int, 1>{});
         };
         if (d <= 64) launch(std::integral_constant<int, 8>{});
         else if (d <= 128) launch(std::integral_constant<int, 16>{});
