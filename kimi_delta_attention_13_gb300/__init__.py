@@ -37,8 +37,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device, stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    if stream is None:   # the current stream's handle, without a torch.cuda.Stream around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -54,6 +54,10 @@ def _on_stream(device: torch.device, stream):
 
 
 def _require(t: torch.Tensor, name: str, device, dtype=None, shape=None):
+    # one pass that accepts; what it does not accept is looked at again for the message
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype) \
+            and (shape is None or t.shape == shape) and (device is None or t.device == device):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -240,33 +244,33 @@ def output_gate(o, z, *, out=None, out_dtype=None, stream=None):
     return out
 
 
-def _linear_inputs(q, k, v, g, name):
-    """Checks shared by linear_prefill and linear_decode; returns (rows, H, H_kv, d_k, d_v, per_token)."""
+def _linear_inputs(q, k, v, g):
+    """Checks shared by linear_prefill and linear_decode; returns the arguments that both C calls
+    begin with and their sizes: ((q, k, v, g, per_token), rows, H, H_kv, d_k, d_v)."""
     dev, dtype = q.device, q.dtype
     if dtype not in _DTYPES:
         raise ValueError("q/k/v must be bfloat16 or float32")
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError(f"q, k and v must be [{name}, heads, d]")
+        raise ValueError("q, k and v must be [T, heads, d]")
     rows, H, dk = q.shape
-    Hkv, dv = k.shape[1], v.shape[2]
+    Hkv, dv = v.shape[1:]
     if Hkv < 1 or H % Hkv != 0:
-        raise ValueError(f"k has {Hkv} heads, which {H} query heads cannot share evenly")
+        raise ValueError(f"v has {Hkv} heads, which {H} query heads cannot share evenly")
+    per_token = g.dim() == 2
     _require(q, "q", dev, dtype)
     _require(k, "k", dev, dtype, (rows, Hkv, dk))
     _require(v, "v", dev, dtype, (rows, Hkv, dv))
-    per_token = g.dim() == 2
     _require(g, "g", dev, torch.float32, (rows, H) if per_token else (H,))
-    return rows, H, Hkv, dk, dv, per_token
+    return (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), per_token), rows, H, Hkv, dk, dv
 
 
-def _out_like(out, out_dtype, dtype, dev, shape):
-    """`out` checked, or a new tensor of `out_dtype` (default: the inputs' type)."""
+def _out(out, dtype, dev, shape, name="out"):
+    """`out` checked, or a new tensor."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16 or float32")
     if out is None:
-        out = torch.empty(shape, device=dev, dtype=out_dtype or dtype)
-    else:
-        _require(out, "out", dev, out_dtype, shape)
-    if out.dtype not in _DTYPES:
-        raise ValueError("out must be bfloat16 or float32")
+        return torch.empty(shape, device=dev, dtype=dtype)
+    _require(out, name, dev, dtype, shape)
     return out
 
 
@@ -279,21 +283,20 @@ def linear_prefill(q, k, v, g, cu_seqlens=None, init_state=None, *, scale: float
     multiple of H_kv); g: fp32 log decays <= 0 (-inf forgets), [T, H] per token or [H] constant;
     cu_seqlens: int32 [N+1] on the device or None for one sequence; init_state: fp32
     [N, H, d_k, d_v] or None (zeros).  final_state: True to allocate, a tensor to fill (init_state
-    itself for an in-place resume), or None/False.  out_dtype defaults to q's.  workspace: a uint8
-    tensor to reuse across calls of one stream, else one is allocated where the sizes need it.
-    Returns (out, final_state)."""
+    itself for an in-place resume), or None/False.  out_dtype defaults to out's, else q's.
+    workspace: a uint8 tensor to reuse across calls of one stream, else one is allocated where the
+    sizes need it.  Returns (out, final_state)."""
     lib = _lib.load()
     dev, dtype = q.device, q.dtype
-    T, H, Hkv, dk, dv, per_token = _linear_inputs(q, k, v, g, "T")
-    if cu_seqlens is None:
-        n = 1
-    else:
+    head, T, H, Hkv, dk, dv = _linear_inputs(q, k, v, g)
+    n, cu = 1, None
+    if cu_seqlens is not None:
         _require(cu_seqlens, "cu_seqlens", dev, torch.int32)
-        n = cu_seqlens.numel() - 1
+        n, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
     shape = (n, H, dk, dv)
     if init_state is not None:
         _require(init_state, "init_state", dev, torch.float32, shape)
-    out = _out_like(out, out_dtype, dtype, dev, (T, H, dv))
+    out = _out(out, out_dtype or (dtype if out is None else out.dtype), dev, (T, H, dv))
     if final_state is True:
         final_state = torch.empty(shape, device=dev, dtype=torch.float32)
     elif final_state is False or final_state is None:
@@ -309,27 +312,27 @@ def linear_prefill(q, k, v, g, cu_seqlens=None, init_state=None, *, scale: float
         # taken from the pool of the stream the kernels run on, so that its reuse waits for them
         with _on_stream(dev, stream):
             workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    rc = lib.kda_linear_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(cu_seqlens), n, T, H,
-                                Hkv, dk, dv, float(scale), _DTYPES[dtype], _DTYPES[out.dtype],
-                                _ptr(init_state), _ptr(out), _ptr(final_state), _ptr(workspace),
+    rc = lib.kda_linear_prefill(*head, cu, n, T, H, Hkv, dk, dv, scale, _DTYPES[dtype], _DTYPES[out.dtype],
+                                _ptr(init_state), out.data_ptr(), _ptr(final_state), _ptr(workspace),
                                 0 if workspace is None else workspace.numel(), _stream(dev, stream))
-    _lib.check(rc, "kda_linear_prefill")
+    if rc:
+        _lib.check(rc, "kda_linear_prefill")
     return out, final_state
 
 
 def linear_decode(q, k, v, g, state, *, scale: float = 1.0, out=None, out_dtype=None, stream=None):
     """linear_prefill's recurrence for one token per sequence (kda_linear_decode): state
     [N, H, d_k, d_v] fp32 is updated in place.  q: [N, H, d_k]; k: [N, H_kv, d_k]; v: [N, H_kv, d_v];
-    g: fp32 [N, H] or [H].  Returns out [N, H, d_v] (out_dtype, default q's)."""
+    g: fp32 [N, H] or [H].  Returns out [N, H, d_v] (out_dtype, default out's, else q's)."""
     lib = _lib.load()
     dev, dtype = q.device, q.dtype
-    N, H, Hkv, dk, dv, per_token = _linear_inputs(q, k, v, g, "N")
+    head, N, H, Hkv, dk, dv = _linear_inputs(q, k, v, g)
     _require(state, "state", dev, torch.float32, (N, H, dk, dv))
-    out = _out_like(out, out_dtype, dtype, dev, (N, H, dv))
-    rc = lib.kda_linear_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(state), _ptr(out), N, H,
-                               Hkv, dk, dv, float(scale), _DTYPES[dtype], _DTYPES[out.dtype],
-                               _stream(dev, stream))
-    _lib.check(rc, "kda_linear_decode")
+    out = _out(out, out_dtype or (dtype if out is None else out.dtype), dev, (N, H, dv))
+    rc = lib.kda_linear_decode(*head, state.data_ptr(), out.data_ptr(), N, H, Hkv, dk, dv, scale,
+                               _DTYPES[dtype], _DTYPES[out.dtype], _stream(dev, stream))
+    if rc:
+        _lib.check(rc, "kda_linear_decode")
     return out
 
 
@@ -340,18 +343,20 @@ def norm_gate(o, z, w, *, eps: float = 1e-6, out=None, out_dtype=None, stream=No
     o, z: [T, H, d] (bf16 or fp32 each); w: fp32 [d] or [H, d].  out: a tensor to fill (o or z
     itself for an in-place call), else a new one of out_dtype (default z's)."""
     lib = _lib.load()
-    dev = o.device
+    dev, shape = o.device, o.shape
     _require(o, "o", dev)
-    if o.dim() != 3 or o.dtype not in _DTYPES or z.dtype not in _DTYPES:
+    if len(shape) != 3 or o.dtype not in _DTYPES or z.dtype not in _DTYPES:
         raise ValueError("o and z must be [T, H, d] of bfloat16 or float32")
-    T, H, d = o.shape
-    _require(z, "z", dev, shape=o.shape)
-    _require(w, "w", dev, torch.float32, (H, d) if w.dim() == 2 else (d,))
-    out = _out_like(out, out_dtype, z.dtype, dev, o.shape)
-    rc = lib.kda_norm_gate(_ptr(o), _DTYPES[o.dtype], _ptr(z), _DTYPES[z.dtype], _ptr(w),
-                           H if w.dim() == 2 else 1, _ptr(out), _DTYPES[out.dtype], T, H, d, float(eps),
+    T, H, d = shape
+    per_head = w.dim() == 2
+    _require(z, "z", dev, None, shape)
+    _require(w, "w", dev, torch.float32, (H, d) if per_head else (d,))
+    out = _out(out, out_dtype or (z.dtype if out is None else out.dtype), dev, shape)
+    rc = lib.kda_norm_gate(o.data_ptr(), _DTYPES[o.dtype], z.data_ptr(), _DTYPES[z.dtype], w.data_ptr(),
+                           H if per_head else 1, out.data_ptr(), _DTYPES[out.dtype], T, H, d, eps,
                            _stream(dev, stream))
-    _lib.check(rc, "kda_norm_gate")
+    if rc:
+        _lib.check(rc, "kda_norm_gate")
     return out
 
 
@@ -366,33 +371,32 @@ def residual_norm(x, y, w, *, w_post=None, z=None, scale: float = 1.0, eps: floa
     out: of y's type, new unless passed.  y None: only out = norm(x) * w, of out_dtype (default
     x's).  Returns (res, out); res is x where y is None."""
     lib = _lib.load()
-    dev = x.device
+    dev, shape, rtype = x.device, x.shape, x.dtype
     _require(x, "x", dev)
-    if x.dim() != 2 or x.dtype not in _DTYPES:
+    if len(shape) != 2 or rtype not in _DTYPES:
         raise ValueError("x must be [T, D] of bfloat16 or float32")
-    T, D = x.shape
+    T, D = shape
     _require(w, "w", dev, torch.float32, (D,))
     if y is None:
         if z is not None or w_post is not None or res is not None:
             raise ValueError("z, w_post and res belong to an add: pass y")
-        out = _out_like(out, out_dtype, x.dtype, dev, (T, D))
+        dtype = out_dtype or (rtype if out is None else out.dtype)
     else:
-        if y.dtype not in _DTYPES or (out_dtype is not None and out_dtype != y.dtype):
+        dtype = y.dtype
+        if dtype not in _DTYPES or (out_dtype is not None and out_dtype != dtype):
             raise ValueError("y must be bfloat16 or float32, and out of its type")
-        _require(y, "y", dev, shape=(T, D))
+        _require(y, "y", dev, dtype, shape)
         if z is not None:
-            _require(z, "z", dev, y.dtype, (T, D))
+            _require(z, "z", dev, dtype, shape)
         if w_post is not None:
             _require(w_post, "w_post", dev, torch.float32, (D,))
-        if res is None:
-            res = torch.empty_like(x)
-        else:
-            _require(res, "res", dev, x.dtype, (T, D))
-        out = _out_like(out, y.dtype, y.dtype, dev, (T, D))
-    rc = lib.kda_residual_norm(_ptr(x), _DTYPES[x.dtype], _ptr(y), _ptr(z), _DTYPES[out.dtype],
-                               _ptr(w_post), _ptr(w), float(scale), float(eps), _ptr(res), _ptr(out), T, D,
+        res = _out(res, rtype, dev, shape, "res")
+    out = _out(out, dtype, dev, shape)
+    rc = lib.kda_residual_norm(x.data_ptr(), _DTYPES[rtype], _ptr(y), _ptr(z), _DTYPES[dtype], _ptr(w_post),
+                               w.data_ptr(), scale, eps, _ptr(res), out.data_ptr(), T, D,
                                _stream(dev, stream))
-    _lib.check(rc, "kda_residual_norm")
+    if rc:
+        _lib.check(rc, "kda_residual_norm")
     return (x if y is None else res), out
 
 

@@ -4,10 +4,12 @@
 //     S_t = exp(g_t) S_(t-1) + k_t v_t^T,     o_t = scale S_t^T q_t
 //
 // This is the path for fp32 inputs and for head sizes the tensor-core kernel does not take.  A
-// block owns 32 value columns of one (segment, head): lane = column, warp w = key channels
-// [w ROWS, (w + 1) ROWS), the state in registers.  Per token and thread that is a multiply, a
-// fused multiply-add into the state and one into the read for each of its rows; key and query rows
-// come from shared memory as broadcasts, a block of tokens at a time.
+// block owns 128 value columns of one (segment, head): a thread holds 16 key channels x 4 columns of
+// the state in registers, warp w the channels [16 w, 16 w + 16), lane l the columns 4 l .. 4 l + 3.
+// Per token that is a multiply, a fused multiply-add into the state and one into the read for each of
+// its 64 elements, two rows an instruction; key and query rows come from shared memory as
+// broadcasts, a block of tokens at a time, the next block's loads in flight beside them.  Bound by
+// the FMA pipe: 3 d_k d_v operations a token and head (2 in the pass for states alone).
 //
 // Long sequences are cut into segments worked on side by side: linear_token_kernel<.., false>
 // leaves the end state of every segment but a sequence's last (from zeros; a first segment from
@@ -19,23 +21,55 @@ namespace kda {
 namespace lin {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCols = 32;
+constexpr int kCols = 128;   // value columns of a block
+constexpr int kRows = 16;    // key channels of a warp
 
-template <typename T, typename TO, int ROWS, bool OUT>
-__global__ void __launch_bounds__(kThreads) linear_token_kernel(const Args p)
+__device__ __forceinline__ float2 pair_fma(float2 a, float2 b, float2 c)
 {
-    constexpr int DK = ROWS * kWarps;          // padded key channels
-    constexpr int TB = ROWS <= 16 ? 16 : 8;    // tokens staged at a time
+    unsigned long long r, x, y, z;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ float2 pair_mul(float2 a, float2 b)
+{
+    unsigned long long r, x, y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+
+// 4 consecutive elements as fp32
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p)
+{
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+
+template <typename T, typename TO, int WARPS, bool OUT>
+__global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
+{
+    constexpr int THREADS = 32 * WARPS, DK = kRows * WARPS;
+    constexpr int TB = WARPS <= 8 ? 8 : 4;   // tokens staged at a time
+    constexpr int KUNITS = TB * DK / 4, VUNITS = TB * kCols / 4;
+    constexpr int KU = (KUNITS + THREADS - 1) / THREADS, VU = (VUNITS + THREADS - 1) / THREADS;
     __shared__ __align__(16) float sk[TB][DK];
     __shared__ __align__(16) float sq[OUT ? TB : 1][DK];
-    __shared__ float sv[TB][kCols];
+    __shared__ __align__(16) float sv[TB][kCols];
     __shared__ float sa[TB];
-    __shared__ float part[OUT ? TB : 1][kWarps][kCols];
+    __shared__ __align__(16) float part[OUT ? TB : 1][WARPS][kCols];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % p.H, item = blockIdx.x / p.H, hk = h / p.group;
-    const int col = blockIdx.y * kCols + lane;
+    const int h = blockIdx.x % p.H, item = blockIdx.x / p.H, hk = h / p.group, Hkv = p.H / p.group;
+    const int cb = blockIdx.y * kCols, col = cb + 4 * lane;
     const bool col_ok = col < p.dv;
     const Item it = find_item(p.cu, p.n_seqs, p.T, p.seg_len, item);
     if (it.seq < 0 || (!OUT && it.seg == it.nseg - 1)) return;
@@ -45,62 +79,99 @@ __global__ void __launch_bounds__(kThreads) linear_token_kernel(const Args p)
     const float *from = nullptr;
     if (it.seg == 0) from = p.init ? p.init + own : nullptr;
     if (OUT && it.nseg > 1 && (it.seg > 0 || p.init)) from = p.starts + slot;
-    float st[ROWS];
+    float2 st[kRows / 2][4];   // rows 2 r, 2 r + 1 of the warp's; column 4 lane + c
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        const int i = warp * ROWS + r;
-        st[r] = from && col_ok && i < p.dk ? from[(long long)i * p.dv + col] : 0.f;
+    for (int r = 0; r < kRows; ++r) {
+        const int i = warp * kRows + r;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (from && col_ok && i < p.dk) s = *reinterpret_cast<const float4 *>(from + (long long)i * p.dv + col);
         // a first segment's start is kept: the last segment may overwrite it (final_state = init)
         if (!OUT && it.seg == 0 && p.init && col_ok && i < p.dk)
-            p.starts[slot + (long long)i * p.dv + col] = st[r];
+            *reinterpret_cast<float4 *>(p.starts + slot + (long long)i * p.dv + col) = s;
+        const float e[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (r & 1) st[r / 2][c].y = e[c];
+            else st[r / 2][c].x = e[c];
+        }
     }
-    float whole = 1.f;
     const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
-    const int Hkv = p.H / p.group;
+    float4 nk[KU], nq[OUT ? KU : 1], nv[VU];
+    float ng = 0.f;
+    auto fetch = [&](long long tb) {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+            const int e = tid + u * THREADS, t = e / (DK / 4), i = e % (DK / 4) * 4;
+            const bool ok = e < KUNITS && tb + t < it.t1 && i < p.dk;
+            nk[u] = ok ? load4(k + ((tb + t) * Hkv + hk) * p.dk + i) : zero;
+            if constexpr (OUT) nq[u] = ok ? load4(q + ((tb + t) * p.H + h) * p.dk + i) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < VU; ++u) {
+            const int e = tid + u * THREADS, t = e / (kCols / 4), c = cb + e % (kCols / 4) * 4;
+            nv[u] = e < VUNITS && tb + t < it.t1 && c < p.dv ? load4(v + ((tb + t) * Hkv + hk) * p.dv + c) : zero;
+        }
+        if (tid < TB) ng = tb + tid < it.t1 ? (p.g_per_token ? p.g[(tb + tid) * p.H + h] : p.g[h]) : 0.f;
+    };
+    float whole = 1.f;
+    if (it.t0 < it.t1) fetch(it.t0);
     for (long long tb = it.t0; tb < it.t1; tb += TB) {
         const int n = (int)min((long long)TB, it.t1 - tb);
-        __syncthreads();
-        for (int e = tid; e < TB * DK; e += kThreads) {
-            const int t = e / DK, i = e % DK;
-            const bool ok = t < n && i < p.dk;
-            sk[t][i] = ok ? to_f32(k[((tb + t) * Hkv + hk) * p.dk + i]) : 0.f;
-            if constexpr (OUT) sq[t][i] = ok ? to_f32(q[((tb + t) * p.H + h) * p.dk + i]) : 0.f;
-        }
-        for (int e = tid; e < TB * kCols; e += kThreads) {
-            const int t = e / kCols, c = blockIdx.y * kCols + e % kCols;
-            sv[t][e % kCols] = t < n && c < p.dv ? to_f32(v[((tb + t) * Hkv + hk) * p.dv + c]) : 0.f;
-        }
-        if (tid < TB) sa[tid] = tid < n ? expf(p.g_per_token ? p.g[(tb + tid) * p.H + h] : p.g[h]) : 1.f;
-        __syncthreads();
-        for (int t = 0; t < n; ++t) {
-            const float a = sa[t], x = sv[t][lane];
-            const float4 *k4 = reinterpret_cast<const float4 *>(&sk[t][warp * ROWS]);
-            float acc = 0.f;
 #pragma unroll
-            for (int r = 0; r < ROWS / 4; ++r) {
-                const float4 kr = k4[r];
-                st[4 * r] = fmaf(st[4 * r], a, kr.x * x);
-                st[4 * r + 1] = fmaf(st[4 * r + 1], a, kr.y * x);
-                st[4 * r + 2] = fmaf(st[4 * r + 2], a, kr.z * x);
-                st[4 * r + 3] = fmaf(st[4 * r + 3], a, kr.w * x);
-                if constexpr (OUT) {
-                    const float4 qr = reinterpret_cast<const float4 *>(&sq[t][warp * ROWS])[r];
-                    acc += st[4 * r] * qr.x + st[4 * r + 1] * qr.y + st[4 * r + 2] * qr.z + st[4 * r + 3] * qr.w;
-                }
+        for (int u = 0; u < KU; ++u) {
+            const int e = tid + u * THREADS;
+            if (e < KUNITS) {
+                *reinterpret_cast<float4 *>(&sk[0][0] + 4 * e) = nk[u];
+                if constexpr (OUT) *reinterpret_cast<float4 *>(&sq[0][0] + 4 * e) = nq[u];
             }
-            if constexpr (OUT) part[t][warp][lane] = acc;
+        }
+#pragma unroll
+        for (int u = 0; u < VU; ++u)
+            if (tid + u * THREADS < VUNITS) *reinterpret_cast<float4 *>(&sv[0][0] + 4 * (tid + u * THREADS)) = nv[u];
+        if (tid < TB) sa[tid] = expf(ng);
+        __syncthreads();
+        if (tb + TB < it.t1) fetch(tb + TB);
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+            const float a = sa[t];
+            const float2 aa = make_float2(a, a);
+            const float4 x = *reinterpret_cast<const float4 *>(&sv[t][4 * lane]);
+            const float2 xx[4] = {make_float2(x.x, x.x), make_float2(x.y, x.y), make_float2(x.z, x.z), make_float2(x.w, x.w)};
+            float2 acc[4] = {};
+#pragma unroll
+            for (int r = 0; r < kRows / 4; ++r) {
+                const float4 kr = *reinterpret_cast<const float4 *>(&sk[t][warp * kRows + 4 * r]);
+                const float2 k2[2] = {make_float2(kr.x, kr.y), make_float2(kr.z, kr.w)};
+                float2 q2[2];
+                if constexpr (OUT) {
+                    const float4 qr = *reinterpret_cast<const float4 *>(&sq[t][warp * kRows + 4 * r]);
+                    q2[0] = make_float2(qr.x, qr.y);
+                    q2[1] = make_float2(qr.z, qr.w);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float2 &s = st[2 * r + e][c];
+                        s = pair_fma(s, aa, pair_mul(k2[e], xx[c]));
+                        if constexpr (OUT) acc[c] = pair_fma(s, q2[e], acc[c]);
+                    }
+            }
+            if constexpr (OUT)
+                *reinterpret_cast<float4 *>(&part[t][warp][4 * lane]) =
+                    make_float4(acc[0].x + acc[0].y, acc[1].x + acc[1].y, acc[2].x + acc[2].y, acc[3].x + acc[3].y);
             if constexpr (!OUT) whole *= a;
         }
+        __syncthreads();
         if constexpr (OUT) {
-            __syncthreads();
-            for (int e = tid; e < n * kCols; e += kThreads) {
+            for (int e = tid; e < n * kCols; e += THREADS) {
                 const int t = e / kCols, c = e % kCols;
                 float acc = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) acc += part[t][w][c];
-                if (blockIdx.y * kCols + c < p.dv)
-                    store_as(static_cast<TO *>(p.out) + ((tb + t) * p.H + h) * p.dv + blockIdx.y * kCols + c,
-                             acc * p.scale);
+                for (int w = 0; w < WARPS; ++w) acc += part[t][w][c];
+                if (cb + c < p.dv)
+                    store_as(static_cast<TO *>(p.out) + ((tb + t) * p.H + h) * p.dv + cb + c, acc * p.scale);
             }
         }
     }
@@ -111,9 +182,12 @@ __global__ void __launch_bounds__(kThreads) linear_token_kernel(const Args p)
     else to = p.starts + slot + (long long)p.H * unit;
     if (to && col_ok) {
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const int i = warp * ROWS + r;
-            if (i < p.dk) to[(long long)i * p.dv + col] = st[r];
+        for (int r = 0; r < kRows; ++r) {
+            const int i = warp * kRows + r;
+            const float2 *s = st[r / 2];
+            if (i < p.dk)
+                *reinterpret_cast<float4 *>(to + (long long)i * p.dv + col) =
+                    r & 1 ? make_float4(s[0].y, s[1].y, s[2].y, s[3].y) : make_float4(s[0].x, s[1].x, s[2].x, s[3].x);
         }
     }
     if (!OUT && tid == 0 && blockIdx.y == 0) p.decays[(long long)item * p.H + h] = whole;
@@ -144,12 +218,23 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const Args p)
     const float *a = p.decays + (long long)first * p.H + h;
     const long long step = (long long)p.H * unit4;
     float4 cur = s[step];
-#pragma unroll 4
-    for (int j = 1; j < nseg - 1; ++j) {
-        const float f = a[(long long)j * p.H];
-        const float4 d = s[(j + 1) * step];
-        cur = make_float4(fmaf(f, cur.x, d.x), fmaf(f, cur.y, d.y), fmaf(f, cur.z, d.z), fmaf(f, cur.w, d.w));
-        s[(j + 1) * step] = cur;
+    constexpr int AHEAD = 8;   // segments whose loads are in flight
+    for (int j0 = 1; j0 < nseg - 1; j0 += AHEAD) {
+        float f[AHEAD];
+        float4 d[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int j = min(j0 + i, nseg - 2);
+            f[i] = a[(long long)j * p.H];
+            d[i] = s[(j + 1) * step];
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (j0 + i >= nseg - 1) break;
+            cur = make_float4(fmaf(f[i], cur.x, d[i].x), fmaf(f[i], cur.y, d[i].y), fmaf(f[i], cur.z, d[i].z),
+                              fmaf(f[i], cur.w, d[i].w));
+            s[(j0 + i + 1) * step] = cur;
+        }
     }
 }
 
@@ -157,9 +242,9 @@ template <typename T, typename TO, bool OUT>
 void launch_tokens(const Args &p, cudaStream_t stream)
 {
     const dim3 grid((unsigned)(p.items * p.H), (unsigned)ceil_div(p.dv, kCols));
-    if (p.dk <= 64) linear_token_kernel<T, TO, 8, OUT><<<grid, kThreads, 0, stream>>>(p);
-    else if (p.dk <= 128) linear_token_kernel<T, TO, 16, OUT><<<grid, kThreads, 0, stream>>>(p);
-    else linear_token_kernel<T, TO, 32, OUT><<<grid, kThreads, 0, stream>>>(p);
+    if (p.dk <= 64) linear_token_kernel<T, TO, 4, OUT><<<grid, 128, 0, stream>>>(p);
+    else if (p.dk <= 128) linear_token_kernel<T, TO, 8, OUT><<<grid, 256, 0, stream>>>(p);
+    else linear_token_kernel<T, TO, 16, OUT><<<grid, 512, 0, stream>>>(p);
 }
 
 template <typename T, typename TO>
@@ -201,9 +286,9 @@ int plan_segments(int n_seqs, int64_t T, int H, int d_k, int d_v, int dtype)
         return T <= len ? 0 : (int)len;
     }
     const int64_t slices = ceil_div(d_v, kCols), blocks = (int64_t)n_seqs * H * slices;
-    const int64_t want = 152 * 4;
+    const int64_t want = 152 * 2;
     if (blocks >= want) return 0;
-    int64_t len = (T * H * slices / want + 15) / 16 * 16;
+    int64_t len = (T * H * slices / want + 7) / 8 * 8;
     if (len < 64) len = 64;
     return T <= len ? 0 : (int)len;
 }
