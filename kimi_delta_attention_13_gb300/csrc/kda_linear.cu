@@ -6,10 +6,13 @@
 // This is the path for fp32 inputs and for head sizes the tensor-core kernel does not take.  A
 // block owns 128 value columns of one (segment, head): a thread holds 16 key channels x 4 columns of
 // the state in registers, warp w the channels [16 w, 16 w + 16), lane l the columns 4 l .. 4 l + 3.
-// Per token that is a multiply, a fused multiply-add into the state and one into the read for each of
-// its 64 elements, two rows an instruction; key and query rows come from shared memory as
-// broadcasts, a block of tokens at a time, the next block's loads in flight beside them.  Bound by
-// the FMA pipe: 3 d_k d_v operations a token and head (2 in the pass for states alone).
+// Eight tokens (i, j) are taken at a time.  With a_t = exp(g_t) and S the state before them,
+//     o_i = scale ( (prod_(l <= i) a_l) S^T q_i + sum_(j <= i) (prod_(j < l <= i) a_l) (q_i . k_j) v_j )
+//     S  <- (prod a) S + sum_j k_j (prod_(l > j) a_l v_j)^T
+// so that an element of the state costs one fused multiply-add a token for the read and one for the
+// update, two rows an instruction (decaying it token by token would cost a multiply more).  Key and
+// query rows come from shared memory as broadcasts; the next tokens' loads are in flight meanwhile.
+// Bound by the FMA pipe: 2 d_k d_v operations a token and head, 1 in the pass for states alone.
 //
 // Long sequences are cut into segments worked on side by side: linear_token_kernel<.., false>
 // leaves the end state of every segment but a sequence's last (from zeros; a first segment from
@@ -55,6 +58,16 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p)
                        __uint_as_float(u.y & 0xffff0000u));
 }
 
+__device__ __forceinline__ void store4(float *p, const float (&f)[4])
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&f)[4])
+{
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
 template <typename T, typename TO, int WARPS, bool OUT>
 __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
 {
@@ -62,10 +75,13 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
     constexpr int TB = WARPS <= 8 ? 8 : 4;   // tokens staged at a time
     constexpr int KUNITS = TB * DK / 4, VUNITS = TB * kCols / 4;
     constexpr int KU = (KUNITS + THREADS - 1) / THREADS, VU = (VUNITS + THREADS - 1) / THREADS;
-    __shared__ __align__(16) float sk[TB][DK];
-    __shared__ __align__(16) float sq[OUT ? TB : 1][DK];
+    constexpr int DP = DK + 4;               // padded rows: the score threads walk several at once
+    constexpr int SUB = THREADS / (TB * TB); // threads of a score
+    __shared__ __align__(16) float sk[TB][DP];
+    __shared__ __align__(16) float sq[OUT ? TB : 1][DP];
     __shared__ __align__(16) float sv[TB][kCols];
     __shared__ float sa[TB];
+    __shared__ float sw[TB][TB + 1];         // a score's weight times the score; then the prefix of i
     __shared__ __align__(16) float part[OUT ? TB : 1][WARPS][kCols];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % p.H, item = blockIdx.x / p.H, hk = h / p.group, Hkv = p.H / p.group;
@@ -122,8 +138,8 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
         for (int u = 0; u < KU; ++u) {
             const int e = tid + u * THREADS;
             if (e < KUNITS) {
-                *reinterpret_cast<float4 *>(&sk[0][0] + 4 * e) = nk[u];
-                if constexpr (OUT) *reinterpret_cast<float4 *>(&sq[0][0] + 4 * e) = nq[u];
+                *reinterpret_cast<float4 *>(&sk[e / (DK / 4)][e % (DK / 4) * 4]) = nk[u];
+                if constexpr (OUT) *reinterpret_cast<float4 *>(&sq[e / (DK / 4)][e % (DK / 4) * 4]) = nq[u];
             }
         }
 #pragma unroll
@@ -132,47 +148,93 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
         if (tid < TB) sa[tid] = expf(ng);
         __syncthreads();
         if (tb + TB < it.t1) fetch(tb + TB);
+        if constexpr (OUT) {
+            {   // scores within the block
+                const int pair = tid / SUB, i = pair / TB, j = pair % TB;
+                float sum = 0.f;
+#pragma unroll 4
+                for (int x = tid % SUB * 4; x < DK; x += 4 * SUB) {
+                    const float4 kr = *reinterpret_cast<const float4 *>(&sk[j][x]);
+                    const float4 qr = *reinterpret_cast<const float4 *>(&sq[i][x]);
+                    sum += kr.x * qr.x + kr.y * qr.y + kr.z * qr.z + kr.w * qr.w;
+                }
+#pragma unroll
+                for (int o = SUB / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                float w = 1.f;
+                for (int l = i; l > j; --l) w *= sa[l];
+                if (tid % SUB == 0 && j <= i) {
+                    sw[i][j] = sum * w;
+                    if (j == 0) sw[i][TB] = w * sa[0];
+                }
+            }
 #pragma unroll 1
-        for (int t = 0; t < n; ++t) {
-            const float a = sa[t];
-            const float2 aa = make_float2(a, a);
+            for (int t = 0; t < n; ++t) {
+                float2 acc[4] = {};
+#pragma unroll
+                for (int r = 0; r < kRows / 4; ++r) {
+                    const float4 qr = *reinterpret_cast<const float4 *>(&sq[t][warp * kRows + 4 * r]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        acc[c] = pair_fma(st[2 * r][c], make_float2(qr.x, qr.y), acc[c]);
+                        acc[c] = pair_fma(st[2 * r + 1][c], make_float2(qr.z, qr.w), acc[c]);
+                    }
+                }
+                *reinterpret_cast<float4 *>(&part[t][warp][4 * lane]) =
+                    make_float4(acc[0].x + acc[0].y, acc[1].x + acc[1].y, acc[2].x + acc[2].y, acc[3].x + acc[3].y);
+            }
+        }
+        float all = 1.f;
+#pragma unroll
+        for (int t = 0; t < TB; ++t) all *= sa[t];   // (1 past the segment's end)
+        if constexpr (!OUT) whole *= all;
+#pragma unroll
+        for (int r = 0; r < kRows / 2; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) st[r][c] = pair_mul(st[r][c], make_float2(all, all));
+        float suf = 1.f;   // product of the decays after token t
+#pragma unroll 1
+        for (int t = n - 1; t >= 0; --t) {
             const float4 x = *reinterpret_cast<const float4 *>(&sv[t][4 * lane]);
-            const float2 xx[4] = {make_float2(x.x, x.x), make_float2(x.y, x.y), make_float2(x.z, x.z), make_float2(x.w, x.w)};
-            float2 acc[4] = {};
+            const float xs[4] = {x.x * suf, x.y * suf, x.z * suf, x.w * suf};
+            suf *= sa[t];
 #pragma unroll
             for (int r = 0; r < kRows / 4; ++r) {
                 const float4 kr = *reinterpret_cast<const float4 *>(&sk[t][warp * kRows + 4 * r]);
-                const float2 k2[2] = {make_float2(kr.x, kr.y), make_float2(kr.z, kr.w)};
-                float2 q2[2];
-                if constexpr (OUT) {
-                    const float4 qr = *reinterpret_cast<const float4 *>(&sq[t][warp * kRows + 4 * r]);
-                    q2[0] = make_float2(qr.x, qr.y);
-                    q2[1] = make_float2(qr.z, qr.w);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 xx = make_float2(xs[c], xs[c]);
+                    st[2 * r][c] = pair_fma(make_float2(kr.x, kr.y), xx, st[2 * r][c]);
+                    st[2 * r + 1][c] = pair_fma(make_float2(kr.z, kr.w), xx, st[2 * r + 1][c]);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float2 &s = st[2 * r + e][c];
-                        s = pair_fma(s, aa, pair_mul(k2[e], xx[c]));
-                        if constexpr (OUT) acc[c] = pair_fma(s, q2[e], acc[c]);
-                    }
             }
-            if constexpr (OUT)
-                *reinterpret_cast<float4 *>(&part[t][warp][4 * lane]) =
-                    make_float4(acc[0].x + acc[0].y, acc[1].x + acc[1].y, acc[2].x + acc[2].y, acc[3].x + acc[3].y);
-            if constexpr (!OUT) whole *= a;
         }
         __syncthreads();
         if constexpr (OUT) {
-            for (int e = tid; e < n * kCols; e += THREADS) {
-                const int t = e / kCols, c = e % kCols;
-                float acc = 0.f;
+            for (int e = tid; e < n * (kCols / 4); e += THREADS) {
+                const int t = e / (kCols / 4), c = e % (kCols / 4) * 4;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) acc += part[t][w][c];
-                if (cb + c < p.dv)
-                    store_as(static_cast<TO *>(p.out) + ((tb + t) * p.H + h) * p.dv + cb + c, acc * p.scale);
+                for (int w = 0; w < WARPS; ++w) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&part[t][w][c]);
+                    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+                }
+                const float pre = sw[t][TB];
+                acc.x *= pre; acc.y *= pre; acc.z *= pre; acc.w *= pre;
+#pragma unroll
+                for (int j = 0; j < TB; ++j) {
+                    if (j > t) break;
+                    const float4 x = *reinterpret_cast<const float4 *>(&sv[j][c]);
+                    const float f = sw[t][j];
+                    acc.x = fmaf(f, x.x, acc.x); acc.y = fmaf(f, x.y, acc.y);
+                    acc.z = fmaf(f, x.z, acc.z); acc.w = fmaf(f, x.w, acc.w);
+                }
+                if (cb + c < p.dv) {
+                    TO *o = static_cast<TO *>(p.out) + ((tb + t) * p.H + h) * p.dv + cb + c;
+                    const float f[4] = {acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale};
+                    store4(o, f);
+                }
             }
+            __syncthreads();
         }
     }
     // OUT: the last segment leaves the sequence's final state.  Otherwise the end state from zeros
@@ -286,7 +348,7 @@ int plan_segments(int n_seqs, int64_t T, int H, int d_k, int d_v, int dtype)
         return T <= len ? 0 : (int)len;
     }
     const int64_t slices = ceil_div(d_v, kCols), blocks = (int64_t)n_seqs * H * slices;
-    const int64_t want = 152 * 2;
+    const int64_t want = 152 * 4;
     if (blocks >= want) return 0;
     int64_t len = (T * H * slices / want + 7) / 8 * 8;
     if (len < 64) len = 64;
