@@ -25,7 +25,8 @@
 //   warps 0-7    the state update: 64 (dv = 128) state columns of one key channel per thread, and the
 //                state's bf16 copy
 //   warps 8-15   the chunk's outputs, scale (p D1 + D2) -> global
-//   warps 16-23  V~, then scores -> P, one token row per thread and two threads a row; the decays
+//   warps 16-19  scores -> P, one token row per thread
+//   warps 20-23  the chunk's decays, and V~
 //   warp 24      TMA loads: q and k one tile, v two;  warps 25, 26, 27  issue Q K^T and P V;  K^T V~;  Q S
 // Three issuing warps, because scores, state and outputs of neighbouring chunks overlap.
 #include <cudaTypedefs.h>
@@ -43,10 +44,11 @@ using namespace ptx;
 
 constexpr int C = 128;                          // tokens of a chunk
 constexpr int kThreads = 7 * 128;
-// Registers a thread of each warpgroup, 72 at launch: 2 x 80 + 2 x 56 + 2 x 80 + 72 = 7 x 72 with
-// outputs, 2 x 112 + 2 x 24 + 2 x 72 + 72 for states alone.  What does not fit spills to local memory,
+// Registers a thread of each warpgroup, 72 at launch: 2 x 104 + 2 x 56 + 64 + 56 + 64 = 7 x 72 with
+// outputs, 2 x 120 + 2 x 24 + 72 + 72 + 64 for states alone.  What does not fit spills to local memory,
 // and with this much shared memory nearly every reload of it comes from L2.
-constexpr int kRegsState[2] = {112, 80}, kRegsOut[2] = {24, 56}, kRegsRows[2] = {72, 80}, kRegsIssue[2] = {72, 72};
+constexpr int kRegsState[2] = {120, 104}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {72, 64};
+constexpr int kRegsValue[2] = {72, 56}, kRegsIssue = 64;
 template <int N>
 __device__ __forceinline__ void set_regs()
 {
@@ -89,7 +91,6 @@ struct Layout {
 static_assert(Layout<128, 128>::BYTES <= 232448, "shared memory per block");
 
 constexpr uint32_t TM_SC = 0, TM_D2 = 128, TM_D1 = 256, TM_DST = 384, TM_COLS = 512;
-constexpr uint32_t TM_P = 64;   // P, from the scores' first column
 
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
@@ -241,7 +242,7 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
         if (elect_one()) {
 #pragma unroll
             for (int x = 0; x < C / 16; ++x)
-                mma_ts(tm + TM_D2, tm + TM_SC + TM_P + 8 * x, desc_at(v, x * 2048), I_PV, x > 0);
+                mma_ts(tm + TM_D2, tm + TM_SC + 8 * x, desc_at(v, x * 2048), I_PV, x > 0);
             mma_commit(&sh->bars[B_PV_DONE + s]);
         }
         __syncwarp();
@@ -306,21 +307,92 @@ __device__ void read_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     }
 }
 
-// warps 16-23: thread = token row 32 blk + lane.  V~ of a chunk, its P, and the next chunk's decays; two
-// warps share a row block, one half of V~'s channels and some of P's column blocks each.
-template <int DK, int DV, bool OUT>
-__device__ void row_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm, int h, long long t0, int len, int nch)
+// warps 16-19: thread = token row 32 blk + lane
+template <int DK, int DV>
+__device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len, int nch)
 {
     using L = Layout<DK, DV>;
-    constexpr int UNITS = DV / 16;   // 16-byte units of a row of v for this thread
-    const int warp = threadIdx.x >> 5, blk = warp & 3, half = (warp >> 2) & 1, lane = threadIdx.x & 31;
-    const int row = 32 * blk + lane, first = half * UNITS;
+    const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
     const uint32_t tq = tm + TM_SC + ((uint32_t)(32 * blk) << 16);
-    // unit x of a row, in an order that keeps eight rows' accesses in different banks
-    int turn = lane & 7;
-    auto at = [&](int x) { return (x >> 3) * (int)(REGION / 16) + ((x & 7) ^ turn); };
+    for (int c = 0; c < nch; ++c) {
+        if (!wait_warp(sh, B_SC_DONE, c) || !wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) break;
+        const Decays &d = sh->dec[c & 1];
+        tc_fence_after();
+        uint32_t r[32], o[16];
+        tmem_ld32(tq, r);
+        const float pre = scan_up(d.a[row], lane);   // prefix of the row's own block
+        float f = pre;
+        for (int x = 1; x < blk; ++x) f *= d.blk[x];
+        tmem_wait_ld();
+        for (int j = 0; j < blk; ++j) {   // whole blocks before the row's own
+            const float2 ff = make_float2(f, f);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float4 w = reinterpret_cast<const float4 *>(d.suf + 32 * j)[x];
+                const float2 p = mul2(make_float2(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1])),
+                                      mul2(ff, make_float2(w.x, w.y)));
+                const float2 q = mul2(make_float2(__uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3])),
+                                      mul2(ff, make_float2(w.z, w.w)));
+                o[2 * x] = pack_bf16x2(p.x, p.y);
+                o[2 * x + 1] = pack_bf16x2(q.x, q.y);
+            }
+            // P overwrites scores already read: columns 16 j .. 16 j + 15 of blocks <= j
+            tmem_st16(tq + 16 * j, o);
+            tmem_ld32(tq + 32 * (j + 1), r);
+            f = pre;   // the factor of the next block spans one block less
+            for (int x = j + 2; x < blk; ++x) f *= d.blk[x];
+            tmem_wait_ld();
+        }
+        {
+            float w = 1.f, odd = 0.f;
+#pragma unroll
+            for (int y = 7; y >= 0; --y) {   // from the diagonal down: w = product of a over (x, lane]
+                const float4 a = reinterpret_cast<const float4 *>(d.a + 32 * blk)[y];
+                const float ay[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int e = 3; e >= 0; --e) {
+                    const int x = 4 * y + e;
+                    const float p = x <= lane ? __uint_as_float(r[x]) * w : 0.f;
+                    if (x & 1) odd = p;
+                    else o[x / 2] = pack_bf16x2(p, odd);
+                    if (x <= lane) w *= ay[e];
+                }
+            }
+            tmem_st16(tq + 16 * blk, o);
+        }
+        if (blk < 3) {
+            uint32_t o[16] = {};
+            for (int j = blk + 1; j < 4; ++j) tmem_st16(tq + 16 * j, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        const long long n = len - (long long)c * C;
+        if (n < C) {   // rows of other sequences: their P is 0, and 0 x NaN must not get in
+            if (!wait_warp(sh, B_VFULL + (c & 1), c >> 1)) break;
+            if (row >= n) {
+                uint4 *v = reinterpret_cast<uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
+                for (int r = 0; r < DV / 64; ++r)
+                    for (int x = 0; x < 8; ++x) v[r * (REGION / 16) + x] = zero4();
+            }
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->bars[B_P_READY]);
+    }
+}
+
+// warps 20-23: the chunk's decays, and V~; for states alone warps 16-19 take the first half of a row's
+// channels off them
+template <int DK, int DV, bool OUT>
+__device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long long t0, long long len, int nch)
+{
+    constexpr int UNITS = DV / 8 / (OUT ? 1 : 2);   // 16-byte units of a row for this thread
+    const bool main = OUT || threadIdx.x >= 20 * 32;
+    const int first = main && !OUT ? UNITS : 0;
+    using L = Layout<DK, DV>;
+    const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
     auto log_decay = [&](int c) {
-        const int t = c * C + row;
+        const long long t = (long long)c * C + row;
         return t < len ? (p.g_per_token ? p.g[(t0 + t) * p.H + h] : p.g[h]) : 0.f;
     };
     auto put = [&](int c, float g) {
@@ -340,139 +412,64 @@ __device__ void row_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm, 
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->bars[B_DEC_READY + (c & 1)]);
     };
-    // P of the column block j before the row's own, from its scores
-    auto before = [&](const Decays &d, float pre, int j, const uint32_t (&r)[32]) {
-        uint32_t o[8];
-        float f = pre;
-        for (int x = j + 1; x < blk; ++x) f *= d.blk[x];
-        const float2 ff = make_float2(f, f);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const float4 w = reinterpret_cast<const float4 *>(d.suf + 32 * j)[x];
-            const float2 u = mul2(make_float2(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1])),
-                                  mul2(ff, make_float2(w.x, w.y)));
-            const float2 v = mul2(make_float2(__uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3])),
-                                  mul2(ff, make_float2(w.z, w.w)));
-            o[2 * (x & 3)] = pack_bf16x2(u.x, u.y);
-            o[2 * (x & 3) + 1] = pack_bf16x2(v.x, v.y);
-            if ((x & 3) == 3) tmem_st8(tq + TM_P + 16 * j + 8 * (x >> 2), o);
-            else asm volatile("" ::: "memory");   // no weights ahead of their turn: registers are short
-        }
-    };
-    float g = half == 0 ? log_decay(0) : 0.f;
-    if (half == 0) {
+    float g = log_decay(0);
+    if constexpr (OUT) {
         put(0, g);
         g = nch > 1 ? log_decay(1) : 0.f;
     }
     for (int c = 0; c < nch; ++c) {
-        const int n = min(C, len - c * C);   // rows of this segment
-        const Decays &d = sh->dec[c & 1];
-        asm volatile("" : "+r"(turn));   // the units' offsets are cheaper to form anew than to keep
         // V~'s place is free when the last chunk's K^T V~ has read it.
-        if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) return;
-        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) return;
-        {
-            float w = d.suf[row];
-            for (int x = blk + 1; x < 4; ++x) w *= d.blk[x];
-            const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
-            const __nv_bfloat162 ww1 = __halves2bfloat162(w1, w1), ww2 = __halves2bfloat162(w2, w2);
-            const uint4 *v = reinterpret_cast<const uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
-            uint4 *hi = reinterpret_cast<uint4 *>(smem + L::HI + row * 128);
-            uint4 *lo = reinterpret_cast<uint4 *>(smem + L::LO + row * 128);
-            if (row < n) {
-#pragma unroll 1
-                for (int b = first; b < first + UNITS; b += 4) {
-                    uint4 in[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) in[i] = v[at(b + i)];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 hi4, lo4;
-                        split2(in[i].x, ww1, ww2, hi4.x, lo4.x);
-                        split2(in[i].y, ww1, ww2, hi4.y, lo4.y);
-                        split2(in[i].z, ww1, ww2, hi4.z, lo4.z);
-                        split2(in[i].w, ww1, ww2, hi4.w, lo4.w);
-                        hi[at(b + i)] = hi4;
-                        lo[at(b + i)] = lo4;
-                    }
-                }
-            } else {   // a row of another sequence: 0 x NaN must not get into the state
-                for (int x = first; x < first + UNITS; ++x) hi[at(x)] = lo[at(x)] = zero4();
-            }
-            if (n < C && !wait_warp(sh, B_KFULL, c)) return;
-            if (row >= n) {   // (its column of the scores is not used)
-                uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + row * 128);
-                for (int r = half; r < DK / 64; r += 2)
-                    for (int i = 0; i < 8; ++i) k[r * (REGION / 16) + i] = zero4();
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->bars[B_VT_READY]);
+        if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) break;
+        if (!OUT && main) {   // (the state update of chunk c - 2, which read these decays' place, came before)
+            put(c, g);
+            if (c + 1 < nch) g = log_decay(c + 1);
         }
+        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) break;
+        float w = sh->dec[c & 1].suf[row];
+        for (int x = blk + 1; x < 4; ++x) w *= sh->dec[c & 1].blk[x];
+        const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
+        const __nv_bfloat162 ww1 = __halves2bfloat162(w1, w1), ww2 = __halves2bfloat162(w2, w2);
+        const bool live = (long long)c * C + row < len;
+        const uint4 *v = reinterpret_cast<const uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
+        uint4 *hi = reinterpret_cast<uint4 *>(smem + L::HI + row * 128);
+        uint4 *lo = reinterpret_cast<uint4 *>(smem + L::LO + row * 128);
+        // unit x of the row, in an order that keeps eight rows' accesses in different banks
+        auto at = [&](int x) { return (x >> 3) * (int)(REGION / 16) + ((x & 7) ^ (lane & 7)); };
+        if (live) {
+            uint4 in[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) in[i] = v[at(first + i)];
+#pragma unroll
+            for (int x = 0; x < UNITS; ++x) {   // four loads stay in flight
+                const uint4 u = in[x & 3];
+                if (x + 4 < UNITS) in[x & 3] = v[at(first + x + 4)];
+                uint4 hi4, lo4;
+                split2(u.x, ww1, ww2, hi4.x, lo4.x);
+                split2(u.y, ww1, ww2, hi4.y, lo4.y);
+                split2(u.z, ww1, ww2, hi4.z, lo4.z);
+                split2(u.w, ww1, ww2, hi4.w, lo4.w);
+                hi[at(first + x)] = hi4;
+                lo[at(first + x)] = lo4;
+            }
+        } else {   // a row of another sequence: 0 x NaN must not get into the state
+            for (int x = first; x < first + UNITS; ++x) hi[at(x)] = lo[at(x)] = zero4();
+        }
+        if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL, c)) break;
+        if (!live) {
+            uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + row * 128);
+            for (int r = 0; r < DK / 64; ++r)
+                for (int i = 0; i < 8; ++i) k[r * (REGION / 16) + i] = zero4();
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->bars[B_VT_READY]);
         if constexpr (OUT) {
-            // The column blocks of this warp: the diagonal one, and block 0 of the last rows, for the
-            // first warp; the others for the second.  P takes the upper half of the scores' columns:
-            // P of blocks 0, 1 lies over scores of block 2, P of 2, 3 over block 3.  So both warps
-            // first read a block that the other may write over (2 or 3, where there is one), and
-            // write after a barrier.
-            const int j0 = half == 0 ? blk : blk == 3 ? 2 : 0, j1 = half == 0 ? (blk == 3 ? 0 : -1) : blk - 1 - (j0 > 0);
-            const bool any = half == 0 || blk > 0;
-            bool ok = wait_warp(sh, B_SC_DONE, c);
-            uint32_t r[32];
-            if (ok && any) {
-                tc_fence_after();
-                tmem_ld32(tq + 32 * j0, r);
-                tmem_wait_ld();
-                tc_fence_before();
+            if (c + 1 < nch) {   // the place was chunk c - 1's, whose P and outputs are made
+                const int s = (c - 1) & 1, f = (c - 1) >> 1;
+                if (c > 0 && !(wait_warp(sh, B_D2_FREE + s, f) && wait_warp(sh, B_DST_FREE + s, f))) break;
+                put(c + 1, g);
+                if (c + 2 < nch) g = log_decay(c + 2);
             }
-            if (!bar_and(1 + blk, 64, ok)) return;
-            tc_fence_after();
-            const float pre = scan_up(d.a[row], lane);   // prefix of the row's own block
-            if (half == 0) {
-                uint32_t o[8];
-                float w = 1.f, odd = 0.f;
-#pragma unroll
-                for (int y = 7; y >= 0; --y) {   // from the diagonal down: w = product of a over (x, lane]
-                    const float4 a = reinterpret_cast<const float4 *>(d.a + 32 * blk)[y];
-                    const float ay[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                    for (int e = 3; e >= 0; --e) {
-                        const int x = 4 * y + e;
-                        const float u = x <= lane ? __uint_as_float(r[x]) * w : 0.f;
-                        if (x & 1) odd = u;
-                        else o[x / 2 & 7] = pack_bf16x2(u, odd);
-                        if (x <= lane) w *= ay[e];
-                    }
-                    if ((y & 3) == 0) tmem_st8(tq + TM_P + 16 * blk + 2 * y, o);
-                    else asm volatile("" ::: "memory");
-                }
-            } else {
-                if (any) before(d, pre, j0, r);
-                if (blk < 3) {   // columns after the row's block
-                    const uint32_t o[8] = {};
-                    for (int j = 2 * blk + 2; j < 8; ++j) tmem_st8(tq + TM_P + 8 * j, o);
-                }
-            }
-            if (any && j1 >= 0 && j1 != j0) {
-                tmem_ld32(tq + 32 * j1, r);
-                tmem_wait_ld();
-                before(d, pre, j1, r);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            if (n < C && row >= n) {   // rows of other sequences: their P is 0, and 0 x NaN must not get in
-                uint4 *v = reinterpret_cast<uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
-                for (int x = first; x < first + UNITS; ++x) v[at(x)] = zero4();
-            }
-            if (n < C) fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->bars[B_P_READY]);
-        }
-        if (half == 0 && c + 1 < nch) {   // the place was chunk c - 1's, whose state update and outputs are made
-            const int s = (c - 1) & 1, f = (c - 1) >> 1;
-            if (c > 0 && !(wait_warp(sh, B_DST_FREE + s, f) && (!OUT || wait_warp(sh, B_D2_FREE + s, f)))) return;
-            put(c + 1, g);
-            if (c + 2 < nch) g = log_decay(c + 2);
         }
     }
 }
@@ -570,12 +567,12 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
         if (!wait_warp(sh, B_KV_DONE, c)) return;
         tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < N; x += 8) {
-            uint32_t r[8];
-            tmem_ld8(tq + TM_DST + x, r);
+        for (int x = 0; x < N; x += 32) {
+            uint32_t r[32];
+            tmem_ld32(tq + TM_DST + x, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
+            for (int e = 0; e < 32; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
         }
         tc_fence_before();
         arrive(B_DST_FREE + (c & 1));
@@ -675,8 +672,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int b = 0; b < B_COUNT; ++b) {
             int n = 1;
-            if (b == B_DEC_READY || b == B_DEC_READY + 1) n = 4;
-            if (b == B_P_READY || b == B_VT_READY) n = 8;
+            if (b == B_P_READY || b == B_VT_READY || b == B_DEC_READY || b == B_DEC_READY + 1) n = 4;
+            if (b == B_VT_READY && !OUT) n = 8;
             if (b >= B_ST_READY && b < B_DEC_READY) n = 8;
             mbar_init(&sh->bars[b], n);
         }
@@ -703,11 +700,15 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     } else if (warp < 16) {
         set_regs<kRegsOut[OUT]>();
         if constexpr (OUT) output_role<DV, TO>(p, sh, tm, it, h, nch);
+    } else if (warp < 20) {
+        set_regs<kRegsScore[OUT]>();
+        if constexpr (OUT) score_role<DK, DV>(smem, sh, tm, len, nch);
+        else if (nch > 0) value_role<DK, DV, OUT>(p, smem, sh, h, it.t0, len, nch);
     } else if (warp < 24) {
-        set_regs<kRegsRows[OUT]>();
-        if (nch > 0) row_role<DK, DV, OUT>(p, smem, sh, tm, h, it.t0, (int)len, nch);
+        set_regs<kRegsValue[OUT]>();
+        if (nch > 0) value_role<DK, DV, OUT>(p, smem, sh, h, it.t0, len, nch);
     } else {
-        set_regs<kRegsIssue[OUT]>();
+        set_regs<kRegsIssue>();
         if (warp == 24 && nch > 0)
             load_role<DK, DV, OUT>(&mq, &mk, &mv, smem, sh, h, h / p.group, it.t0, nch);
         if (warp == 25 && OUT && nch > 0) score_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
