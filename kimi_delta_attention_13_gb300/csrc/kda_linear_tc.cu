@@ -57,6 +57,7 @@ __device__ __forceinline__ void set_regs()
 }
 
 constexpr long long kTimeout = 4000000000ll;    // bounded waits: 4e9 SM cycles (~2 s)
+constexpr int kPolls = 1 << 22;
 constexpr uint32_t REGION = C * 128;            // 64 channels x 128 tokens
 
 __device__ int g_linear_tc_error;               // sticky device error word of this translation unit
@@ -94,18 +95,16 @@ constexpr uint32_t TM_SC = 0, TM_D2 = 128, TM_D1 = 256, TM_DST = 384, TM_COLS = 
 
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
+// Waits for phase `phase` of a barrier, giving up after kPolls polls (each of which the hardware may
+// hold for a while) or when another thread has; the kernel's end records that.  As short as it can
+// be, since it stands in some thirty places: the roles' loops have to fit the instruction cache.
 __device__ __forceinline__ bool wait(Shared *sh, int bar, int phase)
 {
-    uint64_t *b = &sh->bars[bar];
-    if (mbar_try_wait(b, phase & 1)) return true;
-    const long long t0 = clock64();
-    do {
-        if (mbar_try_wait(b, phase & 1)) return true;
-    } while (!*reinterpret_cast<volatile int *>(&sh->abort) && clock64() - t0 <= kTimeout);
-    if (!*reinterpret_cast<volatile int *>(&sh->abort)) {
-        atomicExch(&g_linear_tc_error, KDA_ERR_DEVICE_TIMEOUT);
-        *reinterpret_cast<volatile int *>(&sh->abort) = 1;
+    for (int i = 0; i < kPolls; ++i) {
+        if (mbar_try_wait(&sh->bars[bar], phase & 1)) return true;
+        if (*reinterpret_cast<volatile int *>(&sh->abort)) break;
     }
+    *reinterpret_cast<volatile int *>(&sh->abort) = 1;
     return false;
 }
 
@@ -436,20 +435,21 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         // unit x of the row, in an order that keeps eight rows' accesses in different banks
         auto at = [&](int x) { return (x >> 3) * (int)(REGION / 16) + ((x & 7) ^ (lane & 7)); };
         if (live) {
-            uint4 in[4];
+#pragma unroll 1
+            for (int b = first; b < first + UNITS; b += 4) {
+                uint4 in[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) in[i] = v[at(first + i)];
+                for (int i = 0; i < 4; ++i) in[i] = v[at(b + i)];
 #pragma unroll
-            for (int x = 0; x < UNITS; ++x) {   // four loads stay in flight
-                const uint4 u = in[x & 3];
-                if (x + 4 < UNITS) in[x & 3] = v[at(first + x + 4)];
-                uint4 hi4, lo4;
-                split2(u.x, ww1, ww2, hi4.x, lo4.x);
-                split2(u.y, ww1, ww2, hi4.y, lo4.y);
-                split2(u.z, ww1, ww2, hi4.z, lo4.z);
-                split2(u.w, ww1, ww2, hi4.w, lo4.w);
-                hi[at(first + x)] = hi4;
-                lo[at(first + x)] = lo4;
+                for (int i = 0; i < 4; ++i) {
+                    uint4 hi4, lo4;
+                    split2(in[i].x, ww1, ww2, hi4.x, lo4.x);
+                    split2(in[i].y, ww1, ww2, hi4.y, lo4.y);
+                    split2(in[i].z, ww1, ww2, hi4.z, lo4.z);
+                    split2(in[i].w, ww1, ww2, hi4.w, lo4.w);
+                    hi[at(b + i)] = hi4;
+                    lo[at(b + i)] = lo4;
+                }
             }
         } else {   // a row of another sequence: 0 x NaN must not get into the state
             for (int x = first; x < first + UNITS; ++x) hi[at(x)] = lo[at(x)] = zero4();
@@ -558,7 +558,6 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
         arrive(B_ST_READY);
     }
     float whole = 1.f;
-    const long long len = it.t1 - it.t0;
     for (int c = 0; c < nch; ++c) {
         if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return;
         const Decays &d = sh->dec[c & 1];
@@ -620,7 +619,7 @@ __device__ void output_role(const Args &p, Shared *sh, uint32_t tm, const Item &
         if (!wait_warp(sh, B_QS_DONE, c) || !wait_warp(sh, B_PV_DONE + (c & 1), c >> 1)) return;
         tc_fence_after();
         const long long left = len - t;   // rows of the quad to store, may be <= 0
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < N; x += COLS) {
             uint4 u[4];
 #pragma unroll
@@ -719,6 +718,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     if (warp == 25) tmem_dealloc(tm, TM_COLS);
+    if (threadIdx.x == 0 && sh->abort) atomicExch(&g_linear_tc_error, KDA_ERR_DEVICE_TIMEOUT);
 }
 
 // ---------------------------------------------------------------------------------------------
