@@ -44,11 +44,11 @@ using namespace ptx;
 
 constexpr int C = 128;                          // tokens of a chunk
 constexpr int kThreads = 7 * 128;
-// Registers a thread of each warpgroup, 72 at launch: 2 x 104 + 2 x 56 + 64 + 56 + 64 = 7 x 72 with
-// outputs, 2 x 120 + 2 x 24 + 72 + 72 + 64 for states alone.  What does not fit spills to local memory,
-// and with this much shared memory nearly every reload of it comes from L2.
-constexpr int kRegsState[2] = {120, 104}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {72, 64};
-constexpr int kRegsValue[2] = {72, 56}, kRegsIssue = 64;
+// Registers a thread of each warpgroup, 72 at launch: 2 x 88 + 2 x 56 + 64 + 88 + 64 = 7 x 72 with
+// outputs, 2 x 112 + 2 x 24 + 80 + 80 + 64 < 7 x 72 for states alone.  What does not fit spills to local
+// memory, and with this much shared memory nearly every reload of it comes from L2.
+constexpr int kRegsState[2] = {112, 88}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {80, 64};
+constexpr int kRegsValue[2] = {80, 88}, kRegsIssue = 64;
 template <int N>
 __device__ __forceinline__ void set_regs()
 {
@@ -226,7 +226,7 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < DK / 16; ++x)
                 mma_ss(tm + TM_SC, desc_at(q, (x >> 2) * REGION + (x & 3) * 32),
                        desc_at(k, (x >> 2) * REGION + (x & 3) * 32), I_QK, x > 0);
@@ -239,7 +239,7 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
         tc_fence_after();
         const uint64_t v = smem_desc(sb + L::V + s * L::VT, REGION, 1024);
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < C / 16; ++x)
                 mma_ts(tm + TM_D2, tm + TM_SC + 8 * x, desc_at(v, x * 2048), I_PV, x > 0);
             mma_commit(&sh->bars[B_PV_DONE + s]);
@@ -265,7 +265,7 @@ __device__ void update_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < C / 16; ++x) {
                 mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(lo, x * 2048), I_KV, x > 0);
                 mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(hi, x * 2048), I_KV, 1);
@@ -293,7 +293,7 @@ __device__ void read_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < DK / 16; ++x)
                 mma_ss(tm + TM_D1, desc_at(q, (x >> 2) * REGION + (x & 3) * 32), desc_at(st, x * 2048), I_QS, x > 0);
             mma_commit(&sh->bars[B_QS_DONE]);
@@ -436,12 +436,13 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         auto at = [&](int x) { return (x >> 3) * (int)(REGION / 16) + ((x & 7) ^ (lane & 7)); };
         if (live) {
 #pragma unroll 1
-            for (int b = first; b < first + UNITS; b += 4) {
-                uint4 in[4];
+            for (int b = first; b < first + UNITS; b += UNITS < 8 ? UNITS : 8) {
+                constexpr int VB = UNITS < 8 ? UNITS : 8;
+                uint4 in[VB];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) in[i] = v[at(b + i)];
+                for (int i = 0; i < VB; ++i) in[i] = v[at(b + i)];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < VB; ++i) {
                     uint4 hi4, lo4;
                     split2(in[i].x, ww1, ww2, hi4.x, lo4.x);
                     split2(in[i].y, ww1, ww2, hi4.y, lo4.y);
@@ -566,12 +567,12 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
         if (!wait_warp(sh, B_KV_DONE, c)) return;
         tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < N; x += 32) {
-            uint32_t r[32];
-            tmem_ld32(tq + TM_DST + x, r);
+        for (int x = 0; x < N; x += 16) {
+            uint32_t r[16];
+            tmem_ld16(tq + TM_DST + x, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
+            for (int e = 0; e < 16; ++e) st[x + e] = fmaf(st[x + e], tot, __uint_as_float(r[e]));
         }
         tc_fence_before();
         arrive(B_DST_FREE + (c & 1));
