@@ -45,10 +45,10 @@ using namespace ptx;
 constexpr int C = 128;                          // tokens of a chunk
 constexpr int kThreads = 7 * 128;
 // Registers a thread of each warpgroup, 72 at launch: 2 x 88 + 2 x 56 + 64 + 88 + 64 = 7 x 72 with
-// outputs, 2 x 112 + 2 x 24 + 80 + 80 + 64 < 7 x 72 for states alone.  What does not fit spills to local
+// outputs, 2 x 104 + 2 x 24 + 88 + 88 + 64 < 7 x 72 for states alone.  What does not fit spills to local
 // memory, and with this much shared memory nearly every reload of it comes from L2.
-constexpr int kRegsState[2] = {112, 88}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {80, 64};
-constexpr int kRegsValue[2] = {80, 88}, kRegsIssue = 64;
+constexpr int kRegsState[2] = {104, 88}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {88, 64};
+constexpr int kRegsValue[2] = {88, 88}, kRegsIssue = 64;
 template <int N>
 __device__ __forceinline__ void set_regs()
 {
@@ -96,19 +96,21 @@ constexpr uint32_t TM_SC = 0, TM_D2 = 128, TM_D1 = 256, TM_DST = 384, TM_COLS = 
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
 // Waits for phase `phase` of a barrier, giving up after kPolls polls (each of which the hardware may
-// hold for a while) or when another thread has; the kernel's end records that.  As short as it can
-// be, since it stands in some thirty places: the roles' loops have to fit the instruction cache.
+// hold for a while): a role that gave up ends, the others run into their own limits, and the
+// kernel's end records it.  As short as it can be, since it stands in some thirty places: the
+// roles' loops together have to fit the instruction cache.
 __device__ __forceinline__ bool wait(Shared *sh, int bar, int phase)
 {
-    for (int i = 0; i < kPolls; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < kPolls; ++i)
         if (mbar_try_wait(&sh->bars[bar], phase & 1)) return true;
-        if (*reinterpret_cast<volatile int *>(&sh->abort)) break;
-    }
-    *reinterpret_cast<volatile int *>(&sh->abort) = 1;
     return false;
 }
 
-// The same for a whole warp: its lanes leave a loop together.
+// How a role ends that a wait gave up in.
+__device__ __forceinline__ void give_up(Shared *sh) { *reinterpret_cast<volatile int *>(&sh->abort) = 1; }
+
+// wait for a whole warp: its lanes leave a loop together.
 __device__ __forceinline__ bool wait_warp(Shared *sh, int bar, int phase)
 {
     return __all_sync(0xffffffffu, wait(sh, bar, phase));
@@ -208,6 +210,7 @@ __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CU
         for (int c = max(0, nv - 2); c < nv; ++c)
             mbar_wait(&sh->bars[B_VFULL + (c & 1)], (c >> 1) & 1, &sh->zero, kTimeout);
         if (nq > 0) mbar_wait(&sh->bars[B_QFULL], (nq - 1) & 1, &sh->zero, kTimeout);
+        return give_up(sh);
     }
 }
 
@@ -249,6 +252,7 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     if (!ok) {
         if (elect_one()) mma_commit(&sh->bars[B_DRAIN]);
         mbar_wait(&sh->bars[B_DRAIN], 0, &sh->zero, kTimeout);
+        give_up(sh);
     }
 }
 
@@ -277,6 +281,7 @@ __device__ void update_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     if (!ok) {
         if (elect_one()) mma_commit(&sh->bars[B_DRAIN + 1]);
         mbar_wait(&sh->bars[B_DRAIN + 1], 0, &sh->zero, kTimeout);
+        give_up(sh);
     }
 }
 
@@ -303,6 +308,7 @@ __device__ void read_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     if (!ok) {
         if (elect_one()) mma_commit(&sh->bars[B_DRAIN + 2]);
         mbar_wait(&sh->bars[B_DRAIN + 2], 0, &sh->zero, kTimeout);
+        give_up(sh);
     }
 }
 
@@ -314,7 +320,7 @@ __device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len
     const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
     const uint32_t tq = tm + TM_SC + ((uint32_t)(32 * blk) << 16);
     for (int c = 0; c < nch; ++c) {
-        if (!wait_warp(sh, B_SC_DONE, c) || !wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) break;
+        if (!wait_warp(sh, B_SC_DONE, c) || !wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return give_up(sh);
         const Decays &d = sh->dec[c & 1];
         tc_fence_after();
         uint32_t r[32], o[16];
@@ -367,11 +373,11 @@ __device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len
         tc_fence_before();
         const long long n = len - (long long)c * C;
         if (n < C) {   // rows of other sequences: their P is 0, and 0 x NaN must not get in
-            if (!wait_warp(sh, B_VFULL + (c & 1), c >> 1)) break;
+            if (!wait_warp(sh, B_VFULL + (c & 1), c >> 1)) return give_up(sh);
             if (row >= n) {
                 uint4 *v = reinterpret_cast<uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
-                for (int r = 0; r < DV / 64; ++r)
-                    for (int x = 0; x < 8; ++x) v[r * (REGION / 16) + x] = zero4();
+#pragma unroll 1
+                for (int x = 0; x < DV / 8; ++x) v[(x >> 3) * (REGION / 16) + (x & 7)] = zero4();
             }
             fence_proxy_async_smem();
         }
@@ -418,12 +424,12 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
     }
     for (int c = 0; c < nch; ++c) {
         // V~'s place is free when the last chunk's K^T V~ has read it.
-        if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) break;
+        if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) return give_up(sh);
         if (!OUT && main) {   // (the state update of chunk c - 2, which read these decays' place, came before)
             put(c, g);
             if (c + 1 < nch) g = log_decay(c + 1);
         }
-        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) break;
+        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) return give_up(sh);
         float w = sh->dec[c & 1].suf[row];
         for (int x = blk + 1; x < 4; ++x) w *= sh->dec[c & 1].blk[x];
         const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
@@ -453,13 +459,14 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
                 }
             }
         } else {   // a row of another sequence: 0 x NaN must not get into the state
+#pragma unroll 1
             for (int x = first; x < first + UNITS; ++x) hi[at(x)] = lo[at(x)] = zero4();
         }
-        if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL, c)) break;
+        if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL, c)) return give_up(sh);
         if (!live) {
             uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + row * 128);
-            for (int r = 0; r < DK / 64; ++r)
-                for (int i = 0; i < 8; ++i) k[r * (REGION / 16) + i] = zero4();
+#pragma unroll 1
+            for (int x = 0; x < DK / 8; ++x) k[(x >> 3) * (REGION / 16) + (x & 7)] = zero4();
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -467,7 +474,7 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         if constexpr (OUT) {
             if (c + 1 < nch) {   // the place was chunk c - 1's, whose P and outputs are made
                 const int s = (c - 1) & 1, f = (c - 1) >> 1;
-                if (c > 0 && !(wait_warp(sh, B_D2_FREE + s, f) && wait_warp(sh, B_DST_FREE + s, f))) break;
+                if (c > 0 && !(wait_warp(sh, B_D2_FREE + s, f) && wait_warp(sh, B_DST_FREE + s, f))) return give_up(sh);
                 put(c + 1, g);
                 if (c + 2 < nch) g = log_decay(c + 2);
             }
@@ -560,11 +567,11 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
     }
     float whole = 1.f;
     for (int c = 0; c < nch; ++c) {
-        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return;
+        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return give_up(sh);
         const Decays &d = sh->dec[c & 1];
         const float tot = d.blk[0] * d.blk[1] * d.blk[2] * d.blk[3];
         whole *= tot;
-        if (!wait_warp(sh, B_KV_DONE, c)) return;
+        if (!wait_warp(sh, B_KV_DONE, c)) return give_up(sh);
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < N; x += 16) {
@@ -577,7 +584,7 @@ __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm
         tc_fence_before();
         arrive(B_DST_FREE + (c & 1));
         if constexpr (OUT) {
-            if (!wait_warp(sh, B_QS_DONE, c)) return;
+            if (!wait_warp(sh, B_QS_DONE, c)) return give_up(sh);
             if (c + 1 < nch) {
                 copy_state();
                 arrive(B_ST_READY);
@@ -612,12 +619,12 @@ __device__ void output_role(const Args &p, Shared *sh, uint32_t tm, const Item &
     const int cols = p.dv - c0 - UNIT * (lane & 3);
     const float2 scale = make_float2(p.scale, p.scale);
     for (int c = 0; c < nch; ++c, t += C, o += C * step) {
-        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return;
+        if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1)) return give_up(sh);
         const Decays &d = sh->dec[c & 1];
         float f = p.scale * scan_up(d.a[row], lane);
         for (int x = 0; x < blk; ++x) f *= d.blk[x];
         const float2 pre = make_float2(f, f);
-        if (!wait_warp(sh, B_QS_DONE, c) || !wait_warp(sh, B_PV_DONE + (c & 1), c >> 1)) return;
+        if (!wait_warp(sh, B_QS_DONE, c) || !wait_warp(sh, B_PV_DONE + (c & 1), c >> 1)) return give_up(sh);
         tc_fence_after();
         const long long left = len - t;   // rows of the quad to store, may be <= 0
 #pragma unroll 1
