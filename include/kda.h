@@ -363,7 +363,12 @@ int kda_cp_correct(const float *u, const float *s_start, const int32_t *cu_seg, 
  *   workspace         device scratch of workspace_bytes >= kda_linear_prefill_workspace(...) bytes,
  *                     NULL if that is 0.  Calls in flight on different streams need one each.
  * Head sizes: multiples of 8 from 8 to 256.
- * States, sums and decays are fp32; outputs are rounded once.  A NaN or infinity in an input of a
+ * States, sums and decays are fp32.  bf16 inputs with head sizes up to 128 take the tensor-core kernel:
+ * there the scores, weighted, and the state that queries read are bf16 operands (each output is within
+ * 2^-8 of the sum of its terms' magnitudes, fp32 outputs too), and the update's operand is split in two
+ * bf16 parts (states within 2^-16 of theirs).  All else is fp32 throughout, rounded once at the end.
+ * The tensor-core kernel's waits are bounded: one that gave up shows as KDA_ERR_DEVICE_TIMEOUT in
+ * kda_device_status.  A NaN or infinity in an input of a
  * sequence leaves the other sequences as they are; within its own it may also reach outputs up to
  * 127 tokens before it.
  * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_MISALIGNED, KDA_ERR_CUDA.

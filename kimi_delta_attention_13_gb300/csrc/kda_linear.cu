@@ -12,7 +12,9 @@
 // so that an element of the state costs one fused multiply-add a token for the read and one for the
 // update, two rows an instruction (decaying it token by token would cost a multiply more).  Key and
 // query rows come from shared memory as broadcasts; the next tokens' loads are in flight meanwhile.
-// Bound by the FMA pipe: 2 d_k d_v operations a token and head, 1 in the pass for states alone.
+// Bound by the FMA pipe: 2 d_k d_v operations a token and head, 1 in the pass for states alone; the
+// pipe is busy for half of the time (2560 tokens in two sequences, 16 heads of 64 x 128: 55 us the
+// outputs, 26 us the states, 10 us the join; token by token with the decay 131 us in all).
 //
 // Long sequences are cut into segments worked on side by side: linear_token_kernel<.., false>
 // leaves the end state of every segment but a sequence's last (from zeros; a first segment from
@@ -337,18 +339,25 @@ int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream)
                                  : run_tokens<float, float>(p, stream);
 }
 
-// Segments are cut when the uncut sequences give the machine too few blocks.
+// Tokens of a segment, 0 where the sequences are not cut.
+//
+// Tensor-core kernel: the cut sequences give at most one block an SM, and are taken where they are the
+// faster by a fit to measured times (us): 8 + 3 a chunk of an uncut sequence, 17 + 5.5 a chunk of a
+// segment (two passes and the join).  T x H cut, uncut: 512 x 8 22.8, 19.8; 768 x 8 23.1, 26.0; 65536 x 8
+// 155, 1437; 1400 x 32 33, 42; 8192 x 32 109, 188; 2048 x 64 70, 54; 8192 x 96 248, 190.
+// Token kernel: cut to 16 warps an SM where there are less (2560 tokens, 16 heads: 64 x 128 in blocks of
+// four warps 85, 78, 91 us at 8, 16, 32 warps; 128 x 128 in blocks of eight 135 us at 16, 149 at 32).
 int plan_segments(int n_seqs, int64_t T, int H, int d_k, int d_v, int dtype)
 {
     if (tc_path(d_k, d_v, dtype)) {
-        const int64_t ctas = (int64_t)n_seqs * H;
-        if (ctas >= 76) return 0;
-        int64_t len = (T * H / 152 + 127) / 128 * 128;
-        if (len < 512) len = 512;
-        return T <= len ? 0 : (int)len;
+        const int64_t ctas = (int64_t)n_seqs * H, sms = 152;
+        if (ctas == 0 || ctas > sms / 2 || T == 0) return 0;
+        const int64_t per = sms / H;   // segments of one sequence
+        const int64_t len = ((n_seqs == 1 ? (T + per - 1) / per : T * H / (sms - ctas)) + 127) / 128 * 128;
+        return 34 + 11 * (len / 128) < 16 + 6 * (T / n_seqs / 128) ? (int)len : 0;
     }
     const int64_t slices = ceil_div(d_v, kCols), blocks = (int64_t)n_seqs * H * slices;
-    const int64_t want = 152 * 4;
+    const int64_t want = d_k <= 64 ? 152 * 4 : d_k <= 128 ? 152 * 2 : 152;   // 16 warps an SM
     if (blocks >= want) return 0;
     int64_t len = (T * H * slices / want + 7) / 8 * 8;
     if (len < 64) len = 64;

@@ -29,6 +29,19 @@
 //   warps 20-23  the chunk's decays, and V~
 //   warp 24      TMA loads: q and k one tile, v two;  warps 25, 26, 27  issue Q K^T and P V;  K^T V~;  Q S
 // Three issuing warps, because scores, state and outputs of neighbouring chunks overlap.
+//
+// What bounds it.  Bytes: 1 KB a token and head at d = 128 (T = 8192, H = 96: 815 MB, 120 us at the
+// measured copy rate).  Measured: 0.188 ms there (0.64 of that rate) on 96 of the 152 SMs, 5800 cycles
+// a chunk; with the row work (V~, P, outputs) taken out the same launches and products take 0.13 ms.
+// TMEM is full (scores and P 128 columns, D1, D2, Dst 128 each) and so is shared memory (7 tiles of
+// 32 KB), so scores and V~ have one buffer each and two cycles of about a chunk's time run side by
+// side: Q K^T -> P -> P V -> Q K^T, and V~ -> K^T V~ -> V~.  The tensor pipe is 42 % busy, shared
+// memory's data path about 75 %.  What was tried: one more set of warps on P and on V~ (32 warps):
+// 0.192 ms; outputs staged for TMA stores: no gain; polling or sleeping waits: no gain; the roles'
+// loops unrolled: 0.228 ms, with 2 M instruction-cache misses a call against 0.3 M, so loops here are
+// rolled where registers allow and waits are a few instructions.
+// Few heads: the sequences are cut so that up to 152 CTAs work side by side, which costs a second read
+// of k and v (T = 65536, H = 8: 0.155 ms against 1.44 ms uncut).
 #include <cudaTypedefs.h>
 
 #include <mutex>
