@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
     const int cb = blockIdx.y * kCols, col = cb + 4 * lane;
     const bool col_ok = col < p.dv;
     const Item it = find_item(p.cu, p.n_seqs, p.T, p.seg_len, item);
-    if (it.seq < 0 || (!OUT && it.seg == it.nseg - 1)) return;
+    if (it.seq < 0 || (!OUT && (it.seg == it.nseg - 1 || item + 1 >= p.items))) return;   // (a bad table
+    // could name more segments than there are places for)
 
     const long long unit = (long long)p.dk * p.dv;
     const long long own = ((long long)it.seq * p.H + h) * unit, slot = ((long long)item * p.H + h) * unit;

@@ -684,7 +684,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const int warp = threadIdx.x >> 5;
     const int h = blockIdx.x % p.H, item = blockIdx.x / p.H;
     const Item it = find_item(p.cu, p.n_seqs, p.T, p.seg_len, item);
-    if (it.seq < 0 || (!OUT && it.seg == it.nseg - 1)) return;
+    if (it.seq < 0 || (!OUT && (it.seg == it.nseg - 1 || item + 1 >= p.items))) return;   // (a bad table
+    // could name more segments than there are places for)
     if ((smem_u32(smem) & 1023u) != 0) {   // the swizzle's atoms; the runtime honours the declaration
         if (threadIdx.x == 0) atomicExch(&g_linear_tc_error, KDA_ERR_DEVICE_BOUNDS);
         return;
