@@ -238,7 +238,10 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     bool ok = true;
     for (int c = 0; c < nch; ++c) {
         const int s = c & 1;
-        ok = wait_warp(sh, B_QFULL, c) && wait_warp(sh, B_KFULL, c);
+        // The scores take the columns of the last chunk's P, which its product with V reads as an operand.
+        // Products that accumulate into different places are ordered by completion alone.
+        ok = wait_warp(sh, B_QFULL, c) && wait_warp(sh, B_KFULL, c) &&
+             (c == 0 || wait_warp(sh, B_PV_DONE + (s ^ 1), (c - 1) >> 1));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
