@@ -367,8 +367,8 @@ int kda_cp_correct(const float *u, const float *s_start, const int32_t *cu_seg, 
  * there the scores, weighted, and the state that queries read are bf16 operands (each output is within
  * 2^-8 of the sum of its terms' magnitudes, fp32 outputs too), and the update's operand is split in two
  * bf16 parts (states within 2^-16 of theirs).  All else is fp32 throughout, rounded once at the end.
- * The tensor-core kernel's waits are bounded: one that gave up shows as KDA_ERR_DEVICE_TIMEOUT in
- * kda_device_status.  A NaN or infinity in an input of a
+ * The tensor-core kernel's waits are bounded (2e9 SM cycles, about 1 s): one that gave up shows as
+ * KDA_ERR_DEVICE_TIMEOUT in kda_device_status.  A NaN or infinity in an input of a
  * sequence leaves the other sequences as they are; within its own it may also reach outputs up to
  * 127 tokens before it.
  * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_MISALIGNED, KDA_ERR_CUDA.
@@ -438,13 +438,21 @@ int kda_device_status(int32_t *status, void *stream);
  * kda_diag_device_timeout -- failure-detection check.  Launches one CTA on `stream` whose bounded
  * device wait is on a barrier that nothing completes; after `timeout_cycles` SM clock cycles
  * (1 .. 4e9; 2e6 is about 1 ms) the wait gives up and records KDA_ERR_DEVICE_TIMEOUT in the device
- * error word, through the same wait routine every kernel of the library uses.  A following
+ * error word, through the wait routine of the library's kernels (kda_linear_prefill's has one of its
+ * own, see kda_diag_linear_timeout).  A following
  * kda_device_status() returns that code and clears it; the CUDA context stays usable.  The pages
  * have no counterpart: it exists so that a caller (or a test) can see an expired device wait
  * surface as an error status instead of a hang.
  * Errors: KDA_ERR_INVALID_ARG (cycles out of range), KDA_ERR_CUDA.
  */
 int kda_diag_device_timeout(int64_t timeout_cycles, void *stream);
+
+/*
+ * kda_diag_linear_timeout -- kda_diag_device_timeout's check of the wait of kda_linear_prefill's
+ * tensor-core kernel, a shorter routine on the clock's lower 32 bits.  In the kernel it gives up after
+ * 2e9 SM cycles (about 1 s).  Arguments and errors as there.
+ */
+int kda_diag_linear_timeout(int64_t timeout_cycles, void *stream);
 
 /*
  * kda_diag_bounds_check -- the device-side bounds check of a debug build, shown to work.  A library

@@ -21,7 +21,7 @@ from . import _lib
 from ._lib import KDAError
 
 __all__ = ["prefill", "prefill_recurrent", "decode", "state_copy", "device_status", "prefill_path",
-           "num_checkpoints", "KDAError", "load", "diag_device_timeout", "premix", "output_gate",
+           "num_checkpoints", "KDAError", "load", "diag_device_timeout", "diag_linear_timeout", "premix", "output_gate",
            "prefill_staged", "linear_prefill", "linear_decode", "norm_gate", "residual_norm"]
 
 _DTYPES = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
@@ -516,3 +516,11 @@ def diag_device_timeout(timeout_cycles: int = 2_000_000, stream=None, device=Non
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     _lib.check(lib.kda_diag_device_timeout(int(timeout_cycles), _stream(dev, stream)),
                "kda_diag_device_timeout")
+
+
+def diag_linear_timeout(timeout_cycles: int = 2_000_000, stream=None, device=None) -> None:
+    """diag_device_timeout's check of the wait that linear_prefill's tensor-core kernel uses."""
+    lib = _lib.load()
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    _lib.check(lib.kda_diag_linear_timeout(int(timeout_cycles), _stream(dev, stream)),
+               "kda_diag_linear_timeout")

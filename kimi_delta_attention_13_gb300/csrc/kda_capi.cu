@@ -438,6 +438,12 @@ int kda_diag_device_timeout(int64_t timeout_cycles, void *stream)
     return kda::launch_wait_timeout_probe((long long)timeout_cycles, (cudaStream_t)stream);
 }
 
+int kda_diag_linear_timeout(int64_t timeout_cycles, void *stream)
+{
+    if (timeout_cycles < 1 || timeout_cycles > 4000000000LL) return KDA_ERR_INVALID_ARG;
+    return kda::launch_linear_timeout_probe((uint32_t)timeout_cycles, (cudaStream_t)stream);
+}
+
 int kda_diag_staged_handles(int64_t *created)
 {
     if (!created) return KDA_ERR_INVALID_ARG;

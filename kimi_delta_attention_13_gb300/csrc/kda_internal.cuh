@@ -64,6 +64,8 @@ int read_and_clear_status_cp(cudaStream_t s, int32_t *status);
 int read_and_clear_status_linear(cudaStream_t s, int32_t *status);
 // Launch the one-CTA probe whose bounded device wait expires after `cycles` SM cycles.
 int launch_wait_timeout_probe(long long cycles, cudaStream_t stream);
+// The same with the linear-attention prefill's wait.
+int launch_linear_timeout_probe(uint32_t cycles, cudaStream_t stream);
 // Launch the one-thread run of the shared-memory bounds check on an out-of-window offset; read
 // (and clear) the site number of the first failed bounds check.
 int launch_bounds_check_probe(cudaStream_t stream);

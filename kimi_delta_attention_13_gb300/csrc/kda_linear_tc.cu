@@ -69,8 +69,9 @@ __device__ __forceinline__ void set_regs()
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-constexpr long long kTimeout = 4000000000ll;    // bounded waits: 4e9 SM cycles (~2 s)
-constexpr int kPolls = 1 << 22;
+constexpr long long kTimeout = 4000000000ll;    // bounded waits for work in flight at an end: 4e9 SM cycles (~2 s)
+constexpr uint32_t kWaitCycles = 2000000000u;   // bounded waits between roles: 2e9 SM cycles (~1 s)
+constexpr uint32_t kSleepNs = 100000;           // longest sleep between two looks at the clock
 constexpr uint32_t REGION = C * 128;            // 64 channels x 128 tokens
 
 __device__ int g_linear_tc_error;               // sticky device error word of this translation unit
@@ -108,15 +109,18 @@ constexpr uint32_t TM_SC = 0, TM_D2 = 128, TM_D1 = 256, TM_DST = 384, TM_COLS = 
 
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
-// Waits for phase `phase` of a barrier, giving up after kPolls polls (each of which the hardware may
-// hold for a while): a role that gave up ends, the others run into their own limits, and the
-// kernel's end records it.  As short as it can be, since it stands in some thirty places: the
-// roles' loops together have to fit the instruction cache.
-__device__ __forceinline__ bool wait(Shared *sh, int bar, int phase)
+// Waits for phase `phase` of a barrier, giving up after `cycles` SM cycles (the clock's lower half, which
+// takes 2^32 to come round): a role that gave up ends, the others, which stand at waits of their own by
+// then, give up by the same rule, and the kernel's end records it.  As short as it can be, since it
+// stands in some thirty places: the roles' loops together have to fit the instruction cache.
+__device__ __forceinline__ bool wait(Shared *sh, int bar, int phase, uint32_t cycles = kWaitCycles)
 {
+    if (mbar_try_wait(&sh->bars[bar], phase & 1)) return true;
+    const uint32_t from = (uint32_t)clock();
 #pragma unroll 1
-    for (int i = 0; i < kPolls; ++i)
-        if (mbar_try_wait(&sh->bars[bar], phase & 1)) return true;
+    do {
+        if (mbar_try_wait_sleep(&sh->bars[bar], phase & 1, kSleepNs)) return true;
+    } while ((uint32_t)clock() - from < cycles);
     return false;
 }
 
@@ -124,9 +128,15 @@ __device__ __forceinline__ bool wait(Shared *sh, int bar, int phase)
 __device__ __forceinline__ void give_up(Shared *sh) { *reinterpret_cast<volatile int *>(&sh->abort) = 1; }
 
 // wait for a whole warp: its lanes leave a loop together.
-__device__ __forceinline__ bool wait_warp(Shared *sh, int bar, int phase)
+__device__ __forceinline__ bool wait_warp(Shared *sh, int bar, int phase, uint32_t cycles = kWaitCycles)
 {
-    return __all_sync(0xffffffffu, wait(sh, bar, phase));
+    return __all_sync(0xffffffffu, wait(sh, bar, phase, cycles));
+}
+
+// The kernel's end: one thread tells the device error word that a role gave up.
+__device__ __forceinline__ void record(Shared *sh)
+{
+    if (sh->abort) atomicExch(&g_linear_tc_error, KDA_ERR_DEVICE_TIMEOUT);
 }
 
 // inclusive product over lanes 0 .. lane
@@ -743,7 +753,23 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     if (warp == 25) tmem_dealloc(tm, TM_COLS);
-    if (threadIdx.x == 0 && sh->abort) atomicExch(&g_linear_tc_error, KDA_ERR_DEVICE_TIMEOUT);
+    if (threadIdx.x == 0) record(sh);
+}
+
+// One warp whose wait is for a phase that nothing completes: it gives up after `cycles`, and the end
+// records it, both as in the kernel above.
+__global__ void linear_timeout_probe_kernel(uint32_t cycles)
+{
+    __shared__ Shared sh;
+    if (threadIdx.x == 0) {
+        mbar_init(&sh.bars[B_KFULL], 1);
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (!wait_warp(&sh, B_KFULL, 0, cycles)) give_up(&sh);
+    __syncthreads();
+    if (threadIdx.x == 0) record(&sh);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -815,6 +841,12 @@ int run_tc_path(const Args &p, int out_dtype, cudaStream_t stream)
 }
 
 }  // namespace lin
+
+int launch_linear_timeout_probe(uint32_t cycles, cudaStream_t stream)
+{
+    lin::linear_timeout_probe_kernel<<<1, 32, 0, stream>>>(cycles);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
 
 int read_and_clear_status_linear(cudaStream_t s, int32_t *status)
 {
