@@ -24,7 +24,8 @@ from . import linear_decode, linear_prefill, norm_gate, residual_norm
 
 class LinearLayer:
     """Random-initialised weights of one layer; `prefill` runs packed prompts, `decode` one token per
-    sequence from the states that `prefill` left."""
+    sequence from the states that `prefill` left.  The residual stream may be bf16 or fp32, whatever the
+    layer's dtype; block outputs have the layer's."""
 
     def __init__(self, width: int, heads: int, kv_heads: Optional[int] = None, d_k: int = 128, d_v: int = 128, *,
                  residual_scale: float = 1.0, eps: float = 1e-6, device="cuda", dtype=torch.bfloat16, seed: int = 0):
@@ -32,7 +33,7 @@ class LinearLayer:
         if kv_heads < 1 or heads % kv_heads != 0:
             raise ValueError(f"{heads} query heads cannot share {kv_heads} key/value heads evenly")
         self.heads, self.kv_heads, self.d_k, self.d_v = heads, kv_heads, d_k, d_v
-        self.scale, self.residual_scale, self.eps = d_k ** -0.5, residual_scale, eps
+        self.scale, self.residual_scale, self.eps, self.dtype = d_k ** -0.5, residual_scale, eps, dtype
         gen = torch.Generator(device=device).manual_seed(seed)
         self._split = [heads * d_k, kv_heads * d_k, kv_heads * d_v, heads * d_v, heads]
         normal = lambda *s: torch.randn(*s, generator=gen, device=device)  # noqa: E731
@@ -45,7 +46,8 @@ class LinearLayer:
     def _enter(self, x: torch.Tensor, y: Optional[torch.Tensor]):
         """The residual stream after the block before, and this block's operands."""
         post = None if y is None else self.n_post
-        x, h = residual_norm(x, y, self.n_in, w_post=post, scale=self.residual_scale, eps=self.eps)
+        x, h = residual_norm(x, y, self.n_in, w_post=post, scale=self.residual_scale, eps=self.eps,
+                             out_dtype=self.dtype)
         q, k, v, z, a = (h @ self.w_in).split(self._split, dim=1)
         rows = x.shape[0]
         q = q.reshape(rows, self.heads, self.d_k).contiguous()
