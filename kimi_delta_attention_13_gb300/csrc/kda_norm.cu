@@ -17,13 +17,14 @@
 namespace kda {
 namespace {
 
-// Results rounded to bf16 take the fast exponential and division (relative error about 2^-21); fp32
-// results the full ones.
-template <typename TO>
+// Where every result is rounded to bf16 the gate takes the fast exponential and division, relative
+// error (2 + 1.173 |z|) 2^-23 and 2^-22 as documented (a rounding to bf16 is 2^-8); where one is fp32,
+// the full ones.
+template <bool FULL>
 __device__ __forceinline__ float gate(float z)
 {
-    if constexpr (sizeof(TO) == 2) return __fdividef(1.f, 1.f + __expf(-z));
-    else return 1.f / (1.f + expf(-z));
+    if constexpr (FULL) return 1.f / (1.f + expf(-z));
+    else return __fdividef(1.f, 1.f + __expf(-z));
 }
 
 __device__ __forceinline__ float warp_sum(float x)
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(256) norm_gate_kernel(const TX *o, const TZ *z
         if (ok && r < rows) {
             if (w_heads > 1) load8(w + r % H * d + 8 * lane, wv);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] *= inv * wv[c] * gate<TO>(gv[c]);
+            for (int c = 0; c < 8; ++c) v[c] *= inv * wv[c] * gate<sizeof(TO) == 4>(gv[c]);
             store8(out + r * d + 8 * lane, v);
         }
     }
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(THREADS, fits64<TR, TB, VECS>() ? 1024 / THREA
                 float g[8];
                 zr[i].unpack(g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] *= gate<TB>(g[e]);
+                for (int e = 0; e < 8; ++e) u[e] *= gate<(sizeof(TR) == 4 || sizeof(TB) == 4)>(g[e]);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) r[i][e] += u[e];
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(256) residual_norm_any_kernel(const ResidualAr
         if (y) {
             float t = to_f32(y[c]) * inv_post;
             if (p.w_post) t *= p.w_post[c];
-            if (z) t *= gate<TB>(to_f32(z[c]));
+            if (z) t *= gate<(sizeof(TR) == 4 || sizeof(TB) == 4)>(to_f32(z[c]));
             r += t;
         }
         return r;
