@@ -17,14 +17,24 @@
 namespace kda {
 namespace {
 
-// Where every result is rounded to bf16 the gate takes the fast exponential and division, relative
-// error (2 + 1.173 |z|) 2^-23 and 2^-22 as documented (a rounding to bf16 is 2^-8); where one is fp32,
-// the full ones.
+// sigmoid(z) = (z < 0 ? e : 1) / (1 + e) with e = exp(-|z|), so that neither e nor the denominator, in
+// [1, 2], leaves the range however far out z lies (1 / (1 + exp(-z)) is 0 from z = -88.8 on, where the
+// value is 3e-39 and may meet a large factor).  The reciprocal is good to an ulp.  Where every result is
+// rounded to bf16 (2^-8) the exponential is the hardware's, of half the argument and squared, which
+// keeps a subnormal e: relative error (4 + |z|) 2^-23.  Where one is fp32 it is the full one.
 template <bool FULL>
 __device__ __forceinline__ float gate(float z)
 {
-    if constexpr (FULL) return 1.f / (1.f + expf(-z));
-    else return __fdividef(1.f, 1.f + __expf(-z));
+    float e, r;
+    if constexpr (FULL) {
+        e = expf(-fabsf(z));
+    } else {
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(z) * -0.72134752f));   // log2(e) / 2
+        e *= e;
+    }
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    if (z < 0.f) r *= e;
+    return r;
 }
 
 __device__ __forceinline__ float warp_sum(float x)

@@ -1,11 +1,10 @@
 """The gates of kda_residual_norm and kda_norm_gate, element by element against 64 bits.
 
-Bounds.  A gate is exp(-|z|), a sum with 1 and a quotient; in full precision 2 ulps, half and half one, in
-all with the two products around it 2^-22 + 4 x 2^-24 = 2^-21 of the gated value.  Where every result is
-rounded to bf16 the gate is the fast one, by the documented error of the fast exponential, 2 +
-floor(1.173 |z|) ulps of 2^-23, and of the fast quotient, 2 ulps: with the products (2 |z| + 6) 2^-23, and
-2^-8 for each rounding.  A gate below the smallest normal number is off by half of the smallest
-subnormal one besides, 2^-150 of the ungated value's unit.
+Bounds.  A gate is exp(-|z|) (an ulp), a sum with 1 (half of one), its reciprocal (one) and a product
+(half); with the product of the gate 3.5 x 2^-23, within 2^-21 of the gated value.  Where every result is
+rounded to bf16 the exponential is a fast one, by the documented error of such (2 + floor(1.173 |z|))
+2^-23: (2 |z| + 6) 2^-23 with the rest, and 2^-8 for each rounding.  A gate below the smallest normal
+number is off by half of the smallest subnormal one besides, and so is its product: 2^-149.
 """
 import pytest
 import torch
@@ -57,6 +56,37 @@ def test_bf16_streams_get_the_fast_gate(D):
     want = 0.5 * y.double() * sigmoid(z)
     tol = (2.0 ** -8 + (2 * z.double().abs() + 6) * 2.0 ** -23 * (1 + 2.0 ** -8)) * want.abs()
     assert bool(((res.double() - want).abs() <= tol).all())
+
+
+# z around the points where exp(-z) passes 2^126 and 2^128, and well past them
+FAR = [-80.0, -87.0, -87.5, -88.0, -88.5, -89.0, -92.0, -95.0]
+
+
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32"), ("bf16", "f32")], ids="-".join)
+def test_residual_norm_gates_far_out(types):
+    """Gates of 1e-35 to 1e-42 on parts large enough for them to count."""
+    tr, tb = (TYPES[t] for t in types)
+    z = torch.tensor(FAR, device=DEV).to(tb).repeat(4, 1)
+    y = torch.full((4, 8), 2.0 ** 120, device=DEV).to(tb)
+    res, out = kda.residual_norm(torch.zeros(4, 8, device=DEV, dtype=tr), y, torch.ones(8, device=DEV), z=z, eps=EPS)
+    want = y.double() * sigmoid(z)
+    gate = ((2 * z.double().abs() + 6) * 2.0 ** -23) if types == ("bf16", "bf16") else 2.0 ** -21
+    tol = gate * want + y.double() * 2.0 ** -149
+    tol = tol + (2.0 ** -8 * (want + tol) if tr is torch.bfloat16 else 0)
+    assert bool(((res.double() - want).abs() <= tol).all()), (res[0], want[0])
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_norm_gate_gates_far_out(out_dtype):
+    z = torch.tensor(FAR, device=DEV).repeat(3, 2, 1)
+    o, w = torch.ones(3, 2, 8, device=DEV), torch.full((8,), 2.0 ** 120, device=DEV)
+    out = kda.norm_gate(o, z, w, eps=EPS, out_dtype=TYPES[out_dtype])
+    want = w.double() * sigmoid(z) / (1 + EPS) ** 0.5
+    gate = (2 * z.double().abs() + 6) * 2.0 ** -23 if out_dtype == "bf16" else 2.0 ** -21
+    # the mean of ones and its inverse root: sixteen roundings and function values of 2^-22 at most
+    tol = (gate + 16 * 2.0 ** -22) * want + w.double() * 2.0 ** -149
+    tol = tol + (2.0 ** -8 * (want + tol) if out_dtype == "bf16" else 0)
+    assert bool(((out.double() - want).abs() <= tol).all()), (out[0, 0], want[0, 0])
 
 
 @pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
