@@ -11,7 +11,8 @@ KDA layers:
     y     = (norm_gate(o, z)) W_o           head norm and gate, output projection
 
 The states are [N, H, d_k, d_v] fp32, as the KDA layers' own, so that `state_copy` and
-`prefix_cache.CheckpointStore` hold and restore them too.
+`prefix_cache.CheckpointStore` hold and restore them too (a prompt's final state as one checkpoint, at
+the prompt's length).
 """
 from __future__ import annotations
 
