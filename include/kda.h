@@ -359,7 +359,8 @@ int kda_cp_correct(const float *u, const float *s_start, const int32_t *cu_seg, 
  *                     products, never as quotients, so any such g is safe.
  *   cu_seqlens, n_seqs, total_tokens, init_state, final_state   as for kda_prefill (init_state may
  *                     be final_state).  An empty sequence's final state is its initial one.
- *   out               [total_tokens, H, d_v] `out_dtype`; must not alias an input.
+ *   out               [total_tokens, H, d_v] `out_dtype`.  out, final_state (but for init_state) and
+ *                     workspace must not alias an input or each other.
  *   workspace         device scratch of workspace_bytes >= kda_linear_prefill_workspace(...) bytes,
  *                     NULL if that is 0.  Calls in flight on different streams need one each.
  * Head sizes: multiples of 8 from 8 to 256.
@@ -389,7 +390,8 @@ int64_t kda_linear_prefill_workspace(int32_t n_seqs, int64_t total_tokens, int32
  * updated in place.
  *   q [n_seqs, H, d_k], k [n_seqs, n_kv_heads, d_k], v [n_seqs, n_kv_heads, d_v] (`dtype`);
  *   g fp32 [n_seqs, H] if g_per_token, else [H];  state fp32 [n_seqs, H, d_k, d_v];
- *   out [n_seqs, H, d_v] `out_dtype`.  Head sizes, errors: as for kda_linear_prefill.
+ *   out [n_seqs, H, d_v] `out_dtype`.  out and state alias nothing.  Head sizes, errors: as for
+ *   kda_linear_prefill.
  */
 int kda_linear_decode(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
                       float *state, void *out, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads,
@@ -416,7 +418,7 @@ int kda_norm_gate(const void *o, int32_t o_dtype, const void *z, int32_t z_dtype
  *     out = r rsqrt(mean(r^2) + eps) w
  *   x, res      [tokens, width] `res_dtype`: the residual stream before and after.  res may be x.
  *   y, z, out   [tokens, width] `dtype`.  out may be y or z.
- *   w_post, w   fp32 [width].
+ *   w_post, w   fp32 [width].  No output may alias them, nor res and out each other.
  *   y           NULL: no add, out = x rsqrt(mean(x^2) + eps) w (then z, w_post and res are NULL too).
  *   width       any; rows of whole 16-byte units (a multiple of 8 channels) up to 16384 channels
  *               are read once, other widths three times, channel by channel.

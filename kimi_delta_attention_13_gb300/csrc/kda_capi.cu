@@ -2,6 +2,7 @@
 // Declarations, argument meaning, layouts and error behaviour: include/kda.h.
 #include <cmath>
 #include <cstdio>
+#include <initializer_list>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -94,6 +95,15 @@ bool tc_supported(int32_t d_k, int32_t d_v, int32_t dtype)
 bool bad_linear_dims(int32_t d_k, int32_t d_v)
 {
     return d_k < 8 || d_k > 256 || d_k % 8 != 0 || d_v < 8 || d_v > 256 || d_v % 8 != 0;
+}
+
+// Whether an output's address is one of those it must not share.
+bool aliases(const void *out, std::initializer_list<const void *> others)
+{
+    if (out)
+        for (const void *p : others)
+            if (out == p) return true;
+    return false;
 }
 
 }  // namespace
@@ -318,7 +328,10 @@ int kda_linear_prefill(const void *q, const void *k, const void *v, const float 
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return KDA_ERR_MISALIGNED;
-    if (out && (out == q || out == k || out == v || out == g)) return KDA_ERR_INVALID_ARG;
+    if (aliases(out, {q, k, v, g, cu_seqlens, init_state, final_state, workspace}) ||
+        aliases(final_state, {q, k, v, g, cu_seqlens, workspace}) ||
+        aliases(workspace, {q, k, v, g, cu_seqlens, init_state}))
+        return KDA_ERR_INVALID_ARG;
     const int64_t need = linear_workspace_bytes(n_seqs, total_tokens, n_heads, d_k, d_v, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
     return launch_linear_prefill(q, k, v, g, g_per_token != 0, cu_seqlens, n_seqs, total_tokens, n_heads,
@@ -339,7 +352,7 @@ int kda_linear_decode(const void *q, const void *k, const void *v, const float *
     const void *ptrs[] = {q, k, v, g, state, out};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
-    if (out && (out == q || out == k || out == v || out == g || out == state)) return KDA_ERR_INVALID_ARG;
+    if (aliases(out, {q, k, v, g, state}) || aliases(state, {q, k, v, g})) return KDA_ERR_INVALID_ARG;
     return launch_linear_decode(q, k, v, g, g_per_token != 0, state, out, n_seqs, n_heads, n_kv_heads, d_k,
                                 d_v, scale, dtype, out_dtype, (cudaStream_t)stream);
 }
@@ -378,8 +391,8 @@ int kda_residual_norm(const void *x, int32_t res_dtype, const void *y, const voi
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
     // res may be x (in place), or y of the same element type; out may be y or z
-    if (out && (out == x || out == res || out == w || out == w_post)) return KDA_ERR_INVALID_ARG;
-    if (res && (res == z || (res == y && res_dtype != dtype))) return KDA_ERR_INVALID_ARG;
+    if (aliases(out, {x, res, w, w_post}) || aliases(res, {z, w, w_post})) return KDA_ERR_INVALID_ARG;
+    if (res && res == y && res_dtype != dtype) return KDA_ERR_INVALID_ARG;
     return launch_residual_norm(x, res_dtype, y, z, dtype, w_post, w, scale, eps, res, out, tokens, width,
                                 (cudaStream_t)stream);
 }
