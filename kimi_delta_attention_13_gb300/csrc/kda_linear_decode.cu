@@ -9,7 +9,7 @@
 // `LANES` float4 columns of one (sequence, head); its threads are rows x LANES and each keeps eight
 // rows' loads in flight.  256 sequences of 96 heads (128 x 128): 0.466 ms, 1.03 of the measured copy
 // rate, so the states move by plain wide loads and stores; a handful of states is bound by the
-// launch (about 4 us on the device).
+// launch (32 states 2.7 us on the device).
 #include <type_traits>
 
 #include "kda_internal.cuh"

@@ -17,9 +17,10 @@
 // the outputs, to which a bf16 rounding of the result is added anyway).
 //
 // Every weight is a product of decays over the very tokens it spans, never a quotient or a
-// difference of sums, so any decay in [0, 1] is exact to a few ulps: w_ij = (suffix of j's 32-token
-// block after j) x (whole blocks between) x (prefix of i's block up to i), and inside one block a
-// running product from the diagonal down.
+// difference of sums, so any decay in [0, 1] is safe and a weight is off by at most two ulps a token it
+// spans (an exponential and a product each): w_ij = (suffix of j's 32-token block after j) x (whole
+// blocks between) x (prefix of i's block up to i), and inside one block a running product from the
+// diagonal down.
 //
 // One CTA works through the chunks of one (segment, head).  Roles, joined by mbarriers:
 //   warps 0-7    the state update: 64 (dv = 128) state columns of one key channel per thread, and the
@@ -31,17 +32,20 @@
 // Three issuing warps, because scores, state and outputs of neighbouring chunks overlap.
 //
 // What bounds it.  Bytes: 1 KB a token and head at d = 128 (T = 8192, H = 96: 815 MB, 120 us at the
-// measured copy rate).  Measured: 0.188 ms there (0.64 of that rate) on 96 of the 152 SMs, 5800 cycles
+// measured copy rate).  Measured: 0.187 ms there (0.64 of that rate) on 96 of the 152 SMs, 5800 cycles
 // a chunk; with the row work (V~, P, outputs) taken out the same launches and products take 0.13 ms.
-// TMEM is full (scores and P 128 columns, D1, D2, Dst 128 each) and so is shared memory (7 tiles of
-// 32 KB), so scores and V~ have one buffer each and two cycles of about a chunk's time run side by
-// side: Q K^T -> P -> P V -> Q K^T, and V~ -> K^T V~ -> V~.  The tensor pipe is 42 % busy, shared
+// With outputs TMEM is full (scores and P 128 columns, D1, D2, Dst 128 each) and so is shared memory
+// (7 tiles of 32 KB), so scores, V~ and K have one buffer each and two cycles of about a chunk's time run
+// side by side: Q K^T -> P -> P V -> Q K^T, and V~ -> K^T V~ -> V~, joined by the one K tile (the next
+// one is fetched after K^T V~).  For states alone the same kernel runs with roles left out, on the same
+// single buffers, although the tiles of Q and S and 384 columns lie idle: 64 us of 168 at T = 65536,
+// H = 8, where its bytes take 40.  The tensor pipe is 42 % busy, shared
 // memory's data path about 75 %.  What was tried: one more set of warps on P and on V~ (32 warps):
 // 0.192 ms; outputs staged for TMA stores: no gain; polling or sleeping waits: no gain; the roles'
 // loops unrolled: 0.228 ms, with 2 M instruction-cache misses a call against 0.3 M, so loops here are
 // rolled where registers allow and waits are a few instructions.
 // Few heads: the sequences are cut so that up to 152 CTAs work side by side, which costs a second read
-// of k and v (T = 65536, H = 8: 0.155 ms against 1.44 ms uncut).
+// of k and v (T = 65536, H = 8: 0.162 ms, with an initial state 0.168, against 1.41 ms uncut).
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -59,7 +63,8 @@ constexpr int C = 128;                          // tokens of a chunk
 constexpr int kThreads = 7 * 128;
 // Registers a thread of each warpgroup, 72 at launch: 2 x 88 + 2 x 56 + 64 + 88 + 64 = 7 x 72 with
 // outputs, 2 x 104 + 2 x 24 + 88 + 88 + 64 < 7 x 72 for states alone.  What does not fit spills to local
-// memory, and with this much shared memory nearly every reload of it comes from L2.
+// memory (8 to 16 bytes in the builds that have any), and with this much
+// shared memory nearly every reload of it comes from L2.
 constexpr int kRegsState[2] = {104, 88}, kRegsOut[2] = {24, 56}, kRegsScore[2] = {88, 64};
 constexpr int kRegsValue[2] = {88, 88}, kRegsIssue = 64;
 template <int N>

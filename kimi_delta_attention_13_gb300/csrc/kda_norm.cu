@@ -9,7 +9,8 @@
 // bits, and each output is rounded once (the norm of r is taken before r is rounded).  Measured, of
 // the copy rate: norm_gate 8192 x 96 x 128 bf16 0.093 ms (0.96; one row a thread group at a time 0.109),
 // residual_norm 8192 x 12288 bf16 with both norms and the gate 0.165 ms (0.90; inputs unpacked on
-// arrival, which left one block an SM, 0.297).
+// arrival, which left one block an SM, 0.297).  In fp32 the registers leave room for fewer blocks: norm_gate
+// 0.172 (1.03), residual_norm 0.401 (0.74), an fp32 stream with bf16 blocks 0.270 (0.77).
 #include <type_traits>
 
 #include "kda_internal.cuh"
@@ -234,7 +235,8 @@ __global__ void __launch_bounds__(THREADS, fits64<TR, TB, VECS>() ? 1024 / THREA
     }
 }
 
-// Any width: scalar accesses, r computed once for its sum and once for its use.
+// Any width: scalar accesses, r computed once for its sum and once for its use (8192 rows with both norms
+// and the gate: 1001 channels 35.5 us, 0.34 of the copy rate; 12289 365 us, 0.41).
 template <typename TR, typename TB>
 __global__ void __launch_bounds__(256) residual_norm_any_kernel(const ResidualArgs p)
 {
@@ -286,7 +288,10 @@ void launch_residual(const ResidualArgs &p, cudaStream_t stream)
     const int vecs = p.D / 8;
     // Two or three groups of channels a thread rather than one: more rows share an SM, and their loads
     // cover one another's sums (8192 x 4096, norms and gate: 55.5 us with 192 threads, 65.8 with 512;
-    // 8192 x 1024: 15.5 with 64, 16.3 with 128). At 12288 blocks of 768 were slower than 512.
+    // 8192 x 1024: 15.5 with 64, 16.3 with 128). At 12288 blocks of 768 were slower than 512.  Blocks of 512
+    // from 4104 channels on leave threads idle (8192 rows, norms and gate: 4104 85.8 us, 0.58 of the copy
+    // rate; 5120 92.1, 0.67; 6144 98.3, 0.75; 8192 116, 0.85).  Without an add the registers for y and z
+    // stay reserved: 8192 x 4096 28.5 us, 0.69; 8192 x 12288 83.4, 0.71.
     if (vecs <= 128) residual_norm_kernel<TR, TB, 64, 2><<<rows, 64, 0, stream>>>(p);
     else if (vecs <= 256) residual_norm_kernel<TR, TB, 128, 2><<<rows, 128, 0, stream>>>(p);
     else if (vecs <= 512) residual_norm_kernel<TR, TB, 192, 3><<<rows, 192, 0, stream>>>(p);
