@@ -9,8 +9,10 @@
 // Eight tokens (i, j) are taken at a time.  With a_t = exp(g_t) and S the state before them,
 //     o_i = scale ( (prod_(l <= i) a_l) S^T q_i + sum_(j <= i) (prod_(j < l <= i) a_l) (q_i . k_j) v_j )
 //     S  <- (prod a) S + sum_j k_j (prod_(l > j) a_l v_j)^T
-// so that an element of the state costs one fused multiply-add a token for the read and one for the
-// update, two rows an instruction (decaying it token by token would cost a multiply more).  Key and
+// Every product of decays is the exponential of its own sum of log decays: a product of rounded factors is
+// off by their roundings, which for a constant decay are all alike (over a memory of 256 tokens 3e-6,
+// against 5e-7).  An element of the state costs one fused multiply-add a token for the read and one for
+// the update, two rows an instruction (decaying it token by token would cost a multiply more).  Key and
 // query rows come from shared memory as broadcasts; the next tokens' loads are in flight meanwhile.
 // Bound by the FMA pipe: 2 d_k d_v operations a token and head, 1 in the pass for states alone; the
 // pipe is busy for half of the time (2560 tokens in two sequences, 16 heads of 64 x 128: 53 us the
@@ -85,7 +87,9 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
     __shared__ __align__(16) float sk[TB][DP];
     __shared__ __align__(16) float sq[OUT ? TB : 1][DP];
     __shared__ __align__(16) float sv[TB][kCols];
-    __shared__ float sa[TB];
+    __shared__ float sg[TB];                 // log decays
+    __shared__ float sa[TB + 1];             // the decays after a token in the block; then those of all
+    __shared__ float sall;                   // the sum of the block's log decays
     __shared__ float sw[TB][TB + 1];         // a score's weight times the score; then the prefix of i
     __shared__ __align__(16) float part[OUT ? TB : 1][WARPS][kCols];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
         }
         if (tid < TB) ng = tb + tid < it.t1 ? (p.g_per_token ? p.g[(tb + tid) * p.H + h] : p.g[h]) : 0.f;
     };
-    float whole = 1.f;
+    float whole = 0.f;                       // sum of the segment's log decays
     if (it.t0 < it.t1) fetch(it.t0);
     for (long long tb = it.t0; tb < it.t1; tb += TB) {
         const int n = (int)min((long long)TB, it.t1 - tb);
@@ -151,7 +155,20 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
 #pragma unroll
         for (int u = 0; u < VU; ++u)
             if (tid + u * THREADS < VUNITS) *reinterpret_cast<float4 *>(&sv[0][0] + 4 * (tid + u * THREADS)) = nv[u];
-        if (tid < TB) sa[tid] = expf(ng);
+        if (warp == 0) {   // (lanes from TB on hold 0, the sums that reach past the block stay in it)
+            float after = ng;
+#pragma unroll
+            for (int o = 1; o < TB; o <<= 1) after += __shfl_down_sync(0xffffffffu, after, o);
+            const float rest = __shfl_down_sync(0xffffffffu, after, 1);
+            if (lane < TB) {
+                sg[lane] = ng;
+                sa[lane] = expf(rest);       // (lane TB - 1: of nothing)
+            }
+            if (lane == 0) {
+                sa[TB] = expf(after);
+                sall = after;
+            }
+        }
         __syncthreads();
         if (tb + TB < it.t1) fetch(tb + TB);
         if constexpr (OUT) {
@@ -166,11 +183,11 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
                 }
 #pragma unroll
                 for (int o = SUB / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                float w = 1.f;
-                for (int l = i; l > j; --l) w *= sa[l];
+                float w = 0.f;
+                for (int l = i; l > j; --l) w += sg[l];
                 if (tid % SUB == 0 && j <= i) {
-                    sw[i][j] = sum * w;
-                    if (j == 0) sw[i][TB] = w * sa[0];
+                    sw[i][j] = sum * expf(w);
+                    if (j == 0) sw[i][TB] = expf(w + sg[0]);
                 }
             }
 #pragma unroll 1
@@ -189,20 +206,17 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
                     make_float4(acc[0].x + acc[0].y, acc[1].x + acc[1].y, acc[2].x + acc[2].y, acc[3].x + acc[3].y);
             }
         }
-        float all = 1.f;
-#pragma unroll
-        for (int t = 0; t < TB; ++t) all *= sa[t];   // (1 past the segment's end)
-        if constexpr (!OUT) whole *= all;
+        const float all = sa[TB];   // (tokens past the segment's end do not decay)
+        if constexpr (!OUT) whole += sall;
 #pragma unroll
         for (int r = 0; r < kRows / 2; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) st[r][c] = pair_mul(st[r][c], make_float2(all, all));
-        float suf = 1.f;   // product of the decays after token t
 #pragma unroll 1
         for (int t = n - 1; t >= 0; --t) {
             const float4 x = *reinterpret_cast<const float4 *>(&sv[t][4 * lane]);
+            const float suf = sa[t];
             const float xs[4] = {x.x * suf, x.y * suf, x.z * suf, x.w * suf};
-            suf *= sa[t];
 #pragma unroll
             for (int r = 0; r < kRows / 4; ++r) {
                 const float4 kr = *reinterpret_cast<const float4 *>(&sk[t][warp * kRows + 4 * r]);
@@ -258,7 +272,7 @@ __global__ void __launch_bounds__(32 * WARPS) linear_token_kernel(const Args p)
                     r & 1 ? make_float4(s[0].y, s[1].y, s[2].y, s[3].y) : make_float4(s[0].x, s[1].x, s[2].x, s[3].x);
         }
     }
-    if (!OUT && tid == 0 && blockIdx.y == 0) p.decays[(long long)item * p.H + h] = whole;
+    if (!OUT && tid == 0 && blockIdx.y == 0) p.decays[(long long)item * p.H + h] = expf(whole);
 }
 
 // starts[j + 1] = decays[j] starts[j] + (end of segment j from zeros), for j = 1 .. nseg - 2 of every
