@@ -366,8 +366,9 @@ int kda_cp_correct(const float *u, const float *s_start, const int32_t *cu_seg, 
  * Head sizes: multiples of 8 from 8 to 256.
  * States, sums and decays are fp32.  bf16 inputs with head sizes up to 128 take the tensor-core kernel:
  * there the scores, weighted, and the state that queries read are bf16 operands (each output is within
- * 2^-8 of the sum of its terms' magnitudes, fp32 outputs too), and the update's operand is split in two
- * bf16 parts (states within 2^-16 of theirs).  All else is fp32 throughout, rounded once at the end.
+ * 2^-8 of the sum of its terms' magnitudes, fp32 outputs too); the update's operand is split in three
+ * bf16 parts, exactly its fp32 values, so that states are good to fp32.  All else is fp32 throughout,
+ * rounded once at the end.
  * The tensor-core kernel's waits are bounded (2e9 SM cycles, about 1 s): one that gave up shows as
  * KDA_ERR_DEVICE_TIMEOUT in kda_device_status.  A NaN or infinity in an input of a
  * sequence leaves the other sequences as they are; within its own it may also reach outputs up to

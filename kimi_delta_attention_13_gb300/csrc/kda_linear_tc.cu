@@ -11,10 +11,11 @@
 //     scores = Q K^T         A, B = q, k tiles in shared memory
 //     D2 = P V               A = P = w . scores (bf16, TMEM), B = v tile
 //     D1 = Q S               B = the state as bf16 (shared memory)
-//     Dst = K^T V~           B = V~ = c . v, split in two bf16 parts (two passes)
+//     Dst = K^T V~           B = V~ = c . v, split in three bf16 parts (three passes)
 // The state itself stays in fp32 registers: S <- (prod a) S + Dst.  Its update must be good to fp32,
-// so V~ carries 16 bits; P and the state's copy are rounded to bf16 once each (their products make
-// the outputs, to which a bf16 rounding of the result is added anyway).
+// so V~ keeps the 24 bits of its fp32 products (two parts, 16 bits, left states 4e-6 off against 1e-7, and
+// took 188 us in place of 207 at T = 8192, H = 96); P and the state's copy are rounded to bf16 once each
+// (their products make the outputs, to which a bf16 rounding of the result is added anyway).
 //
 // Every weight is a product of decays over the very tokens it spans, never a quotient or a
 // difference of sums, so any decay in [0, 1] is safe and a weight is off by at most two ulps a token it
@@ -32,20 +33,21 @@
 // Three issuing warps, because scores, state and outputs of neighbouring chunks overlap.
 //
 // What bounds it.  Bytes: 1 KB a token and head at d = 128 (T = 8192, H = 96: 815 MB, 120 us at the
-// measured copy rate).  Measured: 0.187 ms there (0.64 of that rate) on 96 of the 152 SMs, 5800 cycles
-// a chunk; with the row work (V~, P, outputs) taken out the same launches and products take 0.13 ms.
-// With outputs TMEM is full (scores and P 128 columns, D1, D2, Dst 128 each) and so is shared memory
-// (7 tiles of 32 KB), so scores, V~ and K have one buffer each and two cycles of about a chunk's time run
-// side by side: Q K^T -> P -> P V -> Q K^T, and V~ -> K^T V~ -> V~, joined by the one K tile (the next
-// one is fetched after K^T V~).  For states alone the same kernel runs with roles left out, on the same
-// single buffers, although the tiles of Q and S and 384 columns lie idle: 64 us of 168 at T = 65536,
-// H = 8, where its bytes take 40.  The tensor pipe is 42 % busy, shared
-// memory's data path about 75 %.  What was tried: one more set of warps on P and on V~ (32 warps):
-// 0.192 ms; outputs staged for TMA stores: no gain; polling or sleeping waits: no gain; the roles'
-// loops unrolled: 0.228 ms, with 2 M instruction-cache misses a call against 0.3 M, so loops here are
-// rolled where registers allow and waits are a few instructions.
+// measured copy rate).  Measured: 0.208 ms there (0.58 of that rate) on 96 of the 152 SMs, 6300 cycles a
+// chunk.  Shared memory's data path is 81 % busy: a product of two tiles in shared memory reads 8 KB in its
+// 64 cycles, all that the path carries, and the row work (V~, the state's copy, v) moves as much again
+// as a third of that.  The tensor pipe is 45 % busy.  With outputs TMEM is full (scores and P 128
+// columns, D1, D2, Dst 128 each), so scores have one buffer, and shared memory leaves room for one tile of
+// q and k and two pieces of V~, so two cycles of about a chunk's time run side by side: Q K^T -> P -> P V ->
+// Q K^T, and V~ -> K^T V~ -> V~, joined by the one K tile (the next one is fetched after K^T V~).
+// What was tried: one more set of warps on V~ (32 warps): 0.224 ms; pieces made by pairs of warps:
+// 0.240; k fetched by quarters as they fall free: 0.219; decays in four buffers: 0.213; V~ split in
+// packed bf16 arithmetic, 12 instructions a pair: 0.245; pieces made before their place is free: 0.229;
+// outputs staged for TMA stores, polling or sleeping waits: no gain; the roles' loops unrolled: 1.2 times
+// the time, with six times the instruction-cache misses, so loops here are rolled where registers allow
+// and waits are a few instructions.
 // Few heads: the sequences are cut so that up to 152 CTAs work side by side, which costs a second read
-// of k and v (T = 65536, H = 8: 0.162 ms, with an initial state 0.168, against 1.41 ms uncut).
+// of k and v (T = 65536, H = 8: 0.181 ms, 71 us of it the states, against 1.6 ms uncut).
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -78,6 +80,8 @@ constexpr long long kTimeout = 4000000000ll;    // bounded waits for work in fli
 constexpr uint32_t kWaitCycles = 2000000000u;   // bounded waits between roles: 2e9 SM cycles (~1 s)
 constexpr uint32_t kSleepNs = 100000;           // longest sleep between two looks at the clock
 constexpr uint32_t REGION = C * 128;            // 64 channels x 128 tokens
+constexpr int kQuarter = 32;                    // tokens of a piece of V~
+constexpr uint32_t PIECE = kQuarter * 128;      // 64 channels of them
 
 __device__ int g_linear_tc_error;               // sticky device error word of this translation unit
 
@@ -88,8 +92,9 @@ struct Decays {
 };
 
 enum Bar {
-    B_QFULL, B_KFULL, B_VFULL, B_SC_DONE = B_VFULL + 2, B_P_READY, B_PV_DONE, B_QS_DONE = B_PV_DONE + 2, B_VT_READY, B_KV_DONE,
-    B_ST_READY, B_DST_FREE, B_D2_FREE = B_DST_FREE + 2, B_DEC_READY = B_D2_FREE + 2, B_DRAIN = B_DEC_READY + 2, B_COUNT = B_DRAIN + 3
+    B_QFULL, B_KFULL, B_VFULL = B_KFULL + 2, B_SC_DONE = B_VFULL + 2, B_P_READY, B_PV_DONE, B_QS_DONE = B_PV_DONE + 2, B_VT_READY,
+    B_VT_FREE = B_VT_READY + 3, B_KV_DONE = B_VT_FREE + 3, B_K_FREE, B_ST_READY = B_K_FREE + 2, B_DST_FREE,
+    B_D2_FREE = B_DST_FREE + 2, B_DEC_READY = B_D2_FREE + 2, B_DRAIN = B_DEC_READY + 2, B_COUNT = B_DRAIN + 3
 };
 
 struct Shared {
@@ -100,15 +105,20 @@ struct Shared {
     int zero;          // always 0: the abort flag of waits that must not give up early
 };
 
-template <int DK, int DV>
+// Shared memory: tiles of q (with outputs), k (two for states alone), v (two), places for V~'s pieces, the
+// state's copy (with outputs).
+template <int DK, int DV, bool OUT>
 struct Layout {
     static constexpr uint32_t KT = DK / 64 * REGION, VT = DV / 64 * REGION;
-    static constexpr uint32_t Q = 0, K = KT, V = K + KT, HI = V + 2 * VT, LO = HI + VT, S = LO + VT;
+    static constexpr int KS = OUT ? 1 : 2, PLACES = OUT ? 2 : 3;
+    static constexpr uint32_t PART = DV / 64 * PIECE, PLACE = 3 * PART;   // the hi, mid and lo parts of a piece
+    static constexpr uint32_t Q = 0, K = OUT ? KT : 0, V = K + KS * KT, W = V + 2 * VT, S = W + PLACES * PLACE;
     static constexpr uint32_t SREG = DK * 128;   // the state copy: 64 value channels x DK key channels
-    static constexpr uint32_t SHARED = S + DV / 64 * SREG;
+    static constexpr uint32_t SHARED = OUT ? S + DV / 64 * SREG : S;
     static constexpr uint32_t BYTES = SHARED + sizeof(Shared);
 };
-static_assert(Layout<128, 128>::BYTES <= 232448, "shared memory per block");
+static_assert(Layout<128, 128, true>::BYTES <= 232448 && Layout<128, 128, false>::BYTES <= 232448, "shared memory per block");
+static_assert(Layout<128, 128, true>::PLACES <= 3 && Layout<128, 128, false>::PLACES <= 3, "barriers of the places");
 
 constexpr uint32_t TM_SC = 0, TM_D2 = 128, TM_D1 = 256, TM_DST = 384, TM_COLS = 512;
 
@@ -157,18 +167,6 @@ __device__ __forceinline__ float scan_up(float x, int lane)
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
 
-// Two bf16 values times w = w1 + w2 as hi + lo: hi is v w1 rounded; what that leaves is exact in a
-// bf16 (an 8 by 8 bit product less its upper half), and v w2 is added to it with one rounding, of
-// 2^-9 of a 2^-8th.
-__device__ __forceinline__ void split2(uint32_t x, __nv_bfloat162 w1, __nv_bfloat162 w2, uint32_t &hi, uint32_t &lo)
-{
-    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&x);
-    const __nv_bfloat162 h = __hmul2(v, w1);
-    const __nv_bfloat162 l = __hfma2(v, w2, __hfma2(v, w1, __hneg2(h)));
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-}
-
 // products of two pairs (one instruction)
 __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
@@ -193,12 +191,25 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
     return v;
 }
 
+// Two bf16 values times w as hi + mid + lo, exactly the fp32 products: 8 of their 24 bits a part, cut off,
+// so that what a part leaves is exact.
+__device__ __forceinline__ void split3(uint32_t x, float2 w, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    const float2 p = mul2(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), w);
+    const uint32_t px = __float_as_uint(p.x), py = __float_as_uint(p.y);
+    hi = __byte_perm(px, py, 0x7632);
+    const float rx = p.x - __uint_as_float(px & 0xffff0000u), ry = p.y - __uint_as_float(py & 0xffff0000u);
+    const uint32_t ux = __float_as_uint(rx), uy = __float_as_uint(ry);
+    mid = __byte_perm(ux, uy, 0x7632);
+    lo = __byte_perm(__float_as_uint(rx - __uint_as_float(ux & 0xffff0000u)),
+                     __float_as_uint(ry - __uint_as_float(uy & 0xffff0000u)), 0x7632);
+}
 
 template <int DK, int DV, bool OUT>
 __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv, uint8_t *smem,
                           Shared *sh, int h, int hk, long long t0, int nch)
 {
-    using L = Layout<DK, DV>;
+    using L = Layout<DK, DV, OUT>;
     auto load = [&](const CUtensorMap *m, uint32_t off, int bar, int regions, int head, int c) {
         if (elect_one()) {
             mbar_arrive_expect_tx(&sh->bars[bar], regions * REGION);
@@ -222,19 +233,21 @@ __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CU
             nq = c + 1;
             ahead(mq, DK / 64, h, c + 1);
         }
-        if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) break;
-        load(mk, L::K, B_KFULL, DK / 64, hk, c);
+        if (OUT && c > 0 && !wait_warp(sh, B_K_FREE, c - 1)) break;   // (states alone: waited for with the last v)
+        load(mk, L::K + c % L::KS * L::KT, B_KFULL + c % L::KS, DK / 64, hk, c);
         nk = c + 1;
         ahead(mk, DK / 64, hk, c + 1);
         if (c + 1 < nch) {
-            if (OUT && c > 0 && !wait_warp(sh, B_PV_DONE + ((c - 1) & 1), (c - 1) >> 1)) break;
+            if (c > 0 && !(OUT ? wait_warp(sh, B_PV_DONE + ((c - 1) & 1), (c - 1) >> 1)
+                               : wait_warp(sh, B_K_FREE + ((c - 1) & 1), (c - 1) >> 1))) break;
             value(c + 1);
             nv = c + 2;
             ahead(mv, DV / 64, hk, c + 2);
         }
     }
     if (nk < nch || nv < nch) {   // no copy in flight when the CTA leaves
-        if (nk > 0) mbar_wait(&sh->bars[B_KFULL], (nk - 1) & 1, &sh->zero, kTimeout);
+        for (int c = max(0, nk - L::KS); c < nk; ++c)
+            mbar_wait(&sh->bars[B_KFULL + c % L::KS], c / L::KS & 1, &sh->zero, kTimeout);
         for (int c = max(0, nv - 2); c < nv; ++c)
             mbar_wait(&sh->bars[B_VFULL + (c & 1)], (c >> 1) & 1, &sh->zero, kTimeout);
         if (nq > 0) mbar_wait(&sh->bars[B_QFULL], (nq - 1) & 1, &sh->zero, kTimeout);
@@ -247,7 +260,7 @@ __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CU
 template <int DK, int DV>
 __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 {
-    using L = Layout<DK, DV>;
+    using L = Layout<DK, DV, true>;
     constexpr uint32_t I_QK = idesc_bf16(128, 128, 0, 0), I_PV = idesc_bf16(128, DV, 0, 1);
     const uint64_t q = smem_desc(sb + L::Q, 0, 1024), k = smem_desc(sb + L::K, 0, 1024);
     bool ok = true;
@@ -287,25 +300,35 @@ __device__ void score_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
     }
 }
 
-template <int DK, int DV>
+template <int DK, int DV, bool OUT>
 __device__ void update_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 {
-    using L = Layout<DK, DV>;
+    using L = Layout<DK, DV, OUT>;
     constexpr uint32_t I_KV = idesc_bf16(128, DV, 1, 1);
-    const uint64_t k = smem_desc(sb + L::K, REGION, 1024);
-    const uint64_t hi = smem_desc(sb + L::HI, REGION, 1024), lo = smem_desc(sb + L::LO, REGION, 1024);
+    const uint64_t k = smem_desc(sb + L::K, REGION, 1024), w = smem_desc(sb + L::W, PIECE, 1024);
     bool ok = true;
-    for (int c = 0; c < nch; ++c) {
-        ok = wait_warp(sh, B_VT_READY, c) && wait_warp(sh, B_KFULL, c) && (c == 0 || wait_warp(sh, B_DST_FREE + ((c - 1) & 1), (c - 1) >> 1));
+    for (int n = 0; n < 4 * nch; ++n) {
+        const int c = n >> 2, y = 3 - (n & 3), place = n % L::PLACES;   // piece y of chunk c
+        if ((n & 3) == 0)
+            ok = wait_warp(sh, B_KFULL + c % L::KS, c / L::KS) &&
+                 (c == 0 || wait_warp(sh, B_DST_FREE + ((c - 1) & 1), (c - 1) >> 1));
+        ok = ok && wait_warp(sh, B_VT_READY + place, n / L::PLACES);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll 1
-            for (int x = 0; x < C / 16; ++x) {
-                mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(lo, x * 2048), I_KV, x > 0);
-                mma_ss(tm + TM_DST, desc_at(k, x * 2048), desc_at(hi, x * 2048), I_KV, 1);
+            for (int x = 0; x < kQuarter / 16; ++x) {
+                const uint64_t a = desc_at(k, c % L::KS * L::KT + (y * (kQuarter / 16) + x) * 2048);
+                const uint64_t b = desc_at(w, place * L::PLACE + x * 2048);
+                mma_ss(tm + TM_DST, a, desc_at(b, 2 * L::PART), I_KV, (n & 3) + x > 0);
+                mma_ss(tm + TM_DST, a, desc_at(b, L::PART), I_KV, 1);
+                mma_ss(tm + TM_DST, a, b, I_KV, 1);
             }
-            mma_commit(&sh->bars[B_KV_DONE]);
+            mma_commit(&sh->bars[B_VT_FREE + place]);
+            if ((n & 3) == 3) {
+                mma_commit(&sh->bars[B_KV_DONE]);
+                mma_commit(&sh->bars[B_K_FREE + c % L::KS]);
+            }
         }
         __syncwarp();
     }
@@ -319,7 +342,7 @@ __device__ void update_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 template <int DK, int DV>
 __device__ void read_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 {
-    using L = Layout<DK, DV>;
+    using L = Layout<DK, DV, true>;
     constexpr uint32_t I_QS = idesc_bf16(128, DV, 0, 1);
     const uint64_t q = smem_desc(sb + L::Q, 0, 1024), st = smem_desc(sb + L::S, L::SREG, 1024);
     bool ok = true;
@@ -347,7 +370,7 @@ __device__ void read_mma_role(uint32_t sb, Shared *sh, uint32_t tm, int nch)
 template <int DK, int DV>
 __device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len, int nch)
 {
-    using L = Layout<DK, DV>;
+    using L = Layout<DK, DV, true>;
     const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
     const uint32_t tq = tm + TM_SC + ((uint32_t)(32 * blk) << 16);
     for (int c = 0; c < nch; ++c) {
@@ -417,18 +440,19 @@ __device__ void score_role(uint8_t *smem, Shared *sh, uint32_t tm, long long len
     }
 }
 
-// warps 20-23: the chunk's decays, and V~; for states alone warps 16-19 take the first half of a row's
-// channels off them
+// warps 20-23: the chunk's decays, and V~ in pieces of 32 tokens, a token a lane, the channels shared by
+// the warps; for states alone warps 16-19 take half of the channels
 template <int DK, int DV, bool OUT>
 __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long long t0, long long len, int nch)
 {
-    constexpr int UNITS = DV / 8 / (OUT ? 1 : 2);   // 16-byte units of a row for this thread
+    using L = Layout<DK, DV, OUT>;
+    constexpr int WARPS = OUT ? 4 : 8;
+    constexpr int UNITS = DV / 8 / WARPS, KUNITS = DK / 8 / WARPS;   // 16-byte units of a row for this thread
+    const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const bool main = OUT || threadIdx.x >= 20 * 32;
-    const int first = main && !OUT ? UNITS : 0;
-    using L = Layout<DK, DV>;
-    const int blk = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = 32 * blk + lane;
+    const int share = OUT ? blk : (int)(threadIdx.x >> 5) - 16;
     auto log_decay = [&](int c) {
-        const long long t = (long long)c * C + row;
+        const long long t = (long long)c * C + 32 * blk + lane;
         return t < len ? (p.g_per_token ? p.g[(t0 + t) * p.H + h] : p.g[h]) : 0.f;
     };
     auto put = [&](int c, float g) {
@@ -443,69 +467,68 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         if (lane == 0) d.blk[blk] = suf;
         suf = __shfl_down_sync(0xffffffffu, suf, 1);
         if (lane == 31) suf = 1.f;
-        d.a[row] = a;
-        d.suf[row] = suf;
+        d.a[32 * blk + lane] = a;
+        d.suf[32 * blk + lane] = suf;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->bars[B_DEC_READY + (c & 1)]);
     };
+    // unit x of a row (row % 8 = lane % 8) in a tile whose regions of 64 channels are `region` bytes, in an
+    // order that keeps eight rows' accesses in different banks
+    auto at = [&](int x, uint32_t region) { return (x >> 3) * (int)(region / 16) + ((x & 7) ^ (lane & 7)); };
     float g = log_decay(0);
     if constexpr (OUT) {
         put(0, g);
         g = nch > 1 ? log_decay(1) : 0.f;
     }
     for (int c = 0; c < nch; ++c) {
-        // V~'s place is free when the last chunk's K^T V~ has read it.
-        if (c > 0 && !wait_warp(sh, B_KV_DONE, c - 1)) return give_up(sh);
-        if (!OUT && main) {   // (the state update of chunk c - 2, which read these decays' place, came before)
+        if (!OUT && main) {   // the place was chunk c - 2's, whose pieces and state are made
+            if (c > 1 && !wait_warp(sh, B_DST_FREE + (c & 1), (c - 2) >> 1)) return give_up(sh);
             put(c, g);
             if (c + 1 < nch) g = log_decay(c + 1);
         }
         if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) return give_up(sh);
-        float w = sh->dec[c & 1].suf[row];
-        for (int x = blk + 1; x < 4; ++x) w *= sh->dec[c & 1].blk[x];
-        const __nv_bfloat16 w1 = __float2bfloat16_rn(w), w2 = __float2bfloat16_rn(w - __bfloat162float(w1));
-        const __nv_bfloat162 ww1 = __halves2bfloat162(w1, w1), ww2 = __halves2bfloat162(w2, w2);
-        const bool live = (long long)c * C + row < len;
-        const uint4 *v = reinterpret_cast<const uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
-        uint4 *hi = reinterpret_cast<uint4 *>(smem + L::HI + row * 128);
-        uint4 *lo = reinterpret_cast<uint4 *>(smem + L::LO + row * 128);
-        // unit x of the row, in an order that keeps eight rows' accesses in different banks
-        auto at = [&](int x) { return (x >> 3) * (int)(REGION / 16) + ((x & 7) ^ (lane & 7)); };
-        if (live) {
+        if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL + c % L::KS, c / L::KS)) return give_up(sh);
+        const Decays &d = sh->dec[c & 1];
+        float later = 1.f;   // the product over the blocks after the piece
 #pragma unroll 1
-            for (int b = first; b < first + UNITS; b += UNITS < 8 ? UNITS : 8) {
-                constexpr int VB = UNITS < 8 ? UNITS : 8;
-                uint4 in[VB];
+        for (int x = 0; x < 4; ++x) {   // from the last tokens back
+            const int y = 3 - x, n = 4 * c + x, place = n % L::PLACES, row = 32 * y + lane;
+            const uint4 *v = reinterpret_cast<const uint4 *>(smem + L::V + (c & 1) * L::VT + row * 128);
+            uint4 *to = reinterpret_cast<uint4 *>(smem + L::W + place * L::PLACE + lane * 128);
+            const bool live = (long long)c * C + row < len;
+            uint4 in[UNITS];
 #pragma unroll
-                for (int i = 0; i < VB; ++i) in[i] = v[at(b + i)];
+            for (int i = 0; i < UNITS; ++i) in[i] = v[at(share * UNITS + i, REGION)];
+            const float f = d.suf[row] * later;
+            later *= d.blk[y];
+            const float2 w = make_float2(f, f);
+            if (n >= L::PLACES && !wait_warp(sh, B_VT_FREE + place, n / L::PLACES - 1)) return give_up(sh);
 #pragma unroll
-                for (int i = 0; i < VB; ++i) {
-                    uint4 hi4, lo4;
-                    split2(in[i].x, ww1, ww2, hi4.x, lo4.x);
-                    split2(in[i].y, ww1, ww2, hi4.y, lo4.y);
-                    split2(in[i].z, ww1, ww2, hi4.z, lo4.z);
-                    split2(in[i].w, ww1, ww2, hi4.w, lo4.w);
-                    hi[at(b + i)] = hi4;
-                    lo[at(b + i)] = lo4;
-                }
+            for (int i = 0; i < UNITS; ++i) {
+                uint4 hi, mid, lo;
+                if (!live) in[i] = zero4();   // a row of another sequence: 0 x NaN must not get into the state
+                split3(in[i].x, w, hi.x, mid.x, lo.x);
+                split3(in[i].y, w, hi.y, mid.y, lo.y);
+                split3(in[i].z, w, hi.z, mid.z, lo.z);
+                split3(in[i].w, w, hi.w, mid.w, lo.w);
+                uint4 *u = to + at(share * UNITS + i, PIECE);
+                u[0] = hi;
+                u[L::PART / 16] = mid;
+                u[2 * (L::PART / 16)] = lo;
             }
-        } else {   // a row of another sequence: 0 x NaN must not get into the state
-#pragma unroll 1
-            for (int x = first; x < first + UNITS; ++x) hi[at(x)] = lo[at(x)] = zero4();
+            if (!live) {
+                uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + c % L::KS * L::KT + row * 128);
+#pragma unroll
+                for (int i = 0; i < KUNITS; ++i) k[at(share * KUNITS + i, REGION)] = zero4();
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->bars[B_VT_READY + place]);
         }
-        if ((long long)(c + 1) * C > len && !wait_warp(sh, B_KFULL, c)) return give_up(sh);
-        if (!live) {
-            uint4 *k = reinterpret_cast<uint4 *>(smem + L::K + row * 128);
-#pragma unroll 1
-            for (int x = 0; x < DK / 8; ++x) k[(x >> 3) * (REGION / 16) + (x & 7)] = zero4();
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->bars[B_VT_READY]);
         if constexpr (OUT) {
             if (c + 1 < nch) {   // the place was chunk c - 1's, whose P and outputs are made
-                const int s = (c - 1) & 1, f = (c - 1) >> 1;
-                if (c > 0 && !(wait_warp(sh, B_D2_FREE + s, f) && wait_warp(sh, B_DST_FREE + s, f))) return give_up(sh);
+                const int s = (c - 1) & 1, e = (c - 1) >> 1;
+                if (c > 0 && !(wait_warp(sh, B_D2_FREE + s, e) && wait_warp(sh, B_DST_FREE + s, e))) return give_up(sh);
                 put(c + 1, g);
                 if (c + 2 < nch) g = log_decay(c + 2);
             }
@@ -553,7 +576,7 @@ template <int DK, int DV, bool OUT>
 __device__ void state_role(const Args &p, uint8_t *smem, Shared *sh, uint32_t tm, const Item &it, int item, int h,
                            int nch)
 {
-    using L = Layout<DK, DV>;
+    using L = Layout<DK, DV, OUT>;
     constexpr int N = DV / 2;
     const int warp = threadIdx.x >> 5, blk = warp & 3, half = warp >> 2, lane = threadIdx.x & 31;
     const int row = 32 * blk + lane, c0 = half * N;
@@ -696,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const Args p)
 {
-    using L = Layout<DK, DV>;
+    using L = Layout<DK, DV, OUT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared *sh = reinterpret_cast<Shared *>(smem + L::SHARED);
     const int warp = threadIdx.x >> 5;
@@ -711,8 +734,8 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int b = 0; b < B_COUNT; ++b) {
             int n = 1;
-            if (b == B_P_READY || b == B_VT_READY || b == B_DEC_READY || b == B_DEC_READY + 1) n = 4;
-            if (b == B_VT_READY && !OUT) n = 8;
+            if (b == B_P_READY || b == B_DEC_READY || b == B_DEC_READY + 1) n = 4;
+            if (b >= B_VT_READY && b < B_VT_FREE) n = OUT ? 4 : 8;
             if (b >= B_ST_READY && b < B_DEC_READY) n = 8;
             mbar_init(&sh->bars[b], n);
         }
@@ -751,7 +774,7 @@ linear_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         if (warp == 24 && nch > 0)
             load_role<DK, DV, OUT>(&mq, &mk, &mv, smem, sh, h, h / p.group, it.t0, nch);
         if (warp == 25 && OUT && nch > 0) score_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
-        if (warp == 26 && nch > 0) update_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
+        if (warp == 26 && nch > 0) update_mma_role<DK, DV, OUT>(smem_u32(smem), sh, tm, nch);
         if (warp == 27 && OUT && nch > 0) read_mma_role<DK, DV>(smem_u32(smem), sh, tm, nch);
     }
     tc_fence_before();
@@ -812,7 +835,7 @@ bool make_map(CUtensorMap *map, const void *base, int heads, int d, long long T)
 template <int DK, int DV, typename TO, bool OUT>
 bool launch_one(const CUtensorMap *m, const Args &p, cudaStream_t stream)
 {
-    const int bytes = (int)Layout<DK, DV>::BYTES;
+    const int bytes = (int)Layout<DK, DV, OUT>::BYTES;
     // a function attribute belongs to the current device: set it on every launch
     if (cudaFuncSetAttribute(linear_tc_kernel<DK, DV, TO, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess)
