@@ -355,8 +355,8 @@ int kda_cp_correct(const float *u, const float *s_start, const int32_t *cu_seg, 
  *                     n_kv_heads, d_v]; `dtype`.  Query head h reads key/value head
  *                     h / (H / n_kv_heads); every query head has a state of its own.
  *   g                 fp32 log decays: [total_tokens, H] if g_per_token, else [H].  g <= 0; -inf
- *                     forgets everything before the token.  Products of decays are formed as
- *                     products, never as quotients, so any such g is safe.
+ *                     forgets everything before the token.  Products of decays are formed from the
+ *                     g of the very tokens they span, never as quotients, so any such g is safe.
  *   cu_seqlens, n_seqs, total_tokens, init_state, final_state   as for kda_prefill (init_state may
  *                     be final_state).  An empty sequence's final state is its initial one.
  *   out               [total_tokens, H, d_v] `out_dtype`.  out, final_state (but for init_state) and

@@ -14,14 +14,16 @@
 //     Dst = K^T V~           B = V~ = c . v, split in three bf16 parts (three passes)
 // The state itself stays in fp32 registers: S <- (prod a) S + Dst.  Its update must be good to fp32,
 // so V~ keeps the 24 bits of its fp32 products (two parts, 16 bits, left states 4e-6 off against 1e-7, and
-// took 188 us in place of 207 at T = 8192, H = 96); P and the state's copy are rounded to bf16 once each
+// took 188 us in place of 208 at T = 8192, H = 96); P and the state's copy are rounded to bf16 once each
 // (their products make the outputs, to which a bf16 rounding of the result is added anyway).
 //
-// Every weight is a product of decays over the very tokens it spans, never a quotient or a
-// difference of sums, so any decay in [0, 1] is safe and a weight is off by at most two ulps a token it
-// spans (an exponential and a product each): w_ij = (suffix of j's 32-token block after j) x (whole
-// blocks between) x (prefix of i's block up to i), and inside one block a running product from the
-// diagonal down.
+// Every weight is made of the decays of the very tokens it spans, never as a quotient or a difference of
+// sums, so any decay in [0, 1] is safe: w_ij = (suffix of j's 32-token block after j) x (whole blocks
+// between) x (prefix of i's block up to i).  What goes into the state (suffixes and whole blocks) is the
+// exponential of a block's own sum of log decays: a product of 32 rounded factors is off by all their
+// roundings, which for a constant decay are alike (a memory of 256 tokens: 2.7e-6 of the state, so 5e-7).
+// What a bf16 operand or output takes (prefixes, and inside a block a running product from the
+// diagonal down) is a product.
 //
 // One CTA works through the chunks of one (segment, head).  Roles, joined by mbarriers:
 //   warps 0-7    the state update: 64 (dv = 128) state columns of one key channel per thread, and the
@@ -455,18 +457,22 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         const long long t = (long long)c * C + 32 * blk + lane;
         return t < len ? (p.g_per_token ? p.g[(t0 + t) * p.H + h] : p.g[h]) : 0.f;
     };
-    auto put = [&](int c, float g) {
-        Decays &d = sh->dec[c & 1];
-        const float a = expf(g);
-        float suf = a;   // inclusive product from this lane up, then without the lane's own
+    float a, suf, all;   // of the lane's token and its block, made before their place is free
+    auto make = [&](float g) {
+        float rest = g;   // sum from this lane up, then without the lane's own
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float y = __shfl_down_sync(0xffffffffu, suf, o);
-            if (lane + o < 32) suf *= y;
+            const float y = __shfl_down_sync(0xffffffffu, rest, o);
+            if (lane + o < 32) rest += y;
         }
-        if (lane == 0) d.blk[blk] = suf;
-        suf = __shfl_down_sync(0xffffffffu, suf, 1);
-        if (lane == 31) suf = 1.f;
+        all = expf(rest);   // (of lane 0)
+        rest = __shfl_down_sync(0xffffffffu, rest, 1);
+        suf = expf(lane == 31 ? 0.f : rest);
+        a = expf(g);
+    };
+    auto put = [&](int c) {
+        Decays &d = sh->dec[c & 1];
+        if (lane == 0) d.blk[blk] = all;
         d.a[32 * blk + lane] = a;
         d.suf[32 * blk + lane] = suf;
         __syncwarp();
@@ -477,13 +483,15 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
     auto at = [&](int x, uint32_t region) { return (x >> 3) * (int)(region / 16) + ((x & 7) ^ (lane & 7)); };
     float g = log_decay(0);
     if constexpr (OUT) {
-        put(0, g);
+        make(g);
+        put(0);
         g = nch > 1 ? log_decay(1) : 0.f;
     }
     for (int c = 0; c < nch; ++c) {
         if (!OUT && main) {   // the place was chunk c - 2's, whose pieces and state are made
+            make(g);
             if (c > 1 && !wait_warp(sh, B_DST_FREE + (c & 1), (c - 2) >> 1)) return give_up(sh);
-            put(c, g);
+            put(c);
             if (c + 1 < nch) g = log_decay(c + 1);
         }
         if (!wait_warp(sh, B_DEC_READY + (c & 1), c >> 1) || !wait_warp(sh, B_VFULL + (c & 1), c >> 1)) return give_up(sh);
@@ -528,8 +536,9 @@ __device__ void value_role(const Args &p, uint8_t *smem, Shared *sh, int h, long
         if constexpr (OUT) {
             if (c + 1 < nch) {   // the place was chunk c - 1's, whose P and outputs are made
                 const int s = (c - 1) & 1, e = (c - 1) >> 1;
+                make(g);
                 if (c > 0 && !(wait_warp(sh, B_D2_FREE + s, e) && wait_warp(sh, B_DST_FREE + s, e))) return give_up(sh);
-                put(c + 1, g);
+                put(c + 1);
                 if (c + 2 < nch) g = log_decay(c + 2);
             }
         }

@@ -41,7 +41,7 @@ def slow(heads):
     return torch.tensor(gs, device=DEV)
 
 
-@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("lengths,H,dk,dv", [([4 * MEMORY], 4, 64, 64), ([4 * MEMORY, 3000], 2, 128, 128),
                                              ([4 * MEMORY, 300] + [1] * 40, 16, 64, 128)], ids=["cut", "two", "many"])
 def test_states_with_slow_decays(lengths, H, dk, dv, dtype):
