@@ -15,11 +15,11 @@
 // the update, two rows an instruction (decaying it token by token would cost a multiply more).  Key and
 // query rows come from shared memory as broadcasts; the next tokens' loads are in flight meanwhile.
 // Bound by the FMA pipe: 2 d_k d_v operations a token and head, 1 in the pass for states alone; the
-// pipe is busy for half of the time (2560 tokens in two sequences, 16 heads of 64 x 128: 53 us the
-// outputs, 25 us the states, 9 us the join; token by token with the decay 131 us in all).  A block has
-// its 128 columns and a warp its 16 channels whatever the head's size: 64 x 64 takes the 85 us of 64 x
-// 128, 32 x 32 takes 82.  bf16 heads over 128 come here too: 8192 tokens, 16 heads of 128 x 256 0.84 ms,
-// 256 x 128 1.06, 256 x 256 2.7, where the tensor-core kernel takes 0.073 for 128 x 128.
+// pipe is busy for half of the time (2560 tokens in two sequences, 16 heads of 64 x 128: 55 us the
+// outputs, 26 us the states, 10 us the join; token by token with the decay 131 us in all).  A block has
+// its 128 columns and a warp its 16 channels whatever the head's size: 64 x 64 takes 87 us, 64 x
+// 128 88, 32 x 32 still 85.  bf16 heads over 128 come here too: 8192 tokens, 16 heads of 128 x 256 0.89 ms,
+// 256 x 128 1.10, 256 x 256 2.8, where the tensor-core kernel takes 0.078 for 128 x 128.
 //
 // Long sequences are cut into segments worked on side by side: linear_token_kernel<.., false>
 // leaves the end state of every segment but a sequence's last (from zeros; a first segment from
@@ -361,11 +361,12 @@ int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream)
 //
 // Tensor-core kernel: the cut sequences give at most one block an SM, and are taken where they are the
 // faster for sequences of one length, by a fit to measured times (us): 8 + 3 a chunk of an uncut sequence,
-// 17 + 5.5 a chunk of a segment (two passes and the join).  T x H cut, uncut: 512 x 8 22.8, 19.8; 768 x 8
-// 23.1, 26.0; 65536 x 8 162, 1410; 1400 x 32 33, 42; 8192 x 32 109, 188; 2048 x 64 70, 54; 8192 x 96 248, 187.
+// 17 + 5.5 a chunk of a segment (two passes and the join).  T x H cut, uncut, in a graph: 512 x 8 22.8, 19.4;
+// 640 x 8 22.9, 22.5; 768 x 8 23.3, 25.6; 65536 x 8 169, 1512; 1400 x 32 33, 42; 8192 x 32 107, 201; 2048 x 64
+// 65, 58; 4096 x 64 106, 108; four of 2048 x 8 45, 57; eight of 2048 x 8 80, 57.
 // The lengths are on the device, so the mean stands for the longest: a long sequence among short ones stays
-// whole (65,536 tokens with 8 short sequences, 8 heads: 1410 where it alone takes 168; 32,768 with one of
-// 232, 32 heads: 722 where it alone takes 346).  Such prompts are faster in a call of their own.
+// whole (65,536 tokens with 8 short sequences, 8 heads: 1517 where it alone takes 181; 32,768 with one of
+// 232, 32 heads: 784 where it alone takes 368).  Such prompts are faster in a call of their own.
 // Token kernel: cut to 16 warps an SM where there are less (2560 tokens, 16 heads: 64 x 128 in blocks of
 // four warps 85, 78, 91 us at 8, 16, 32 warps; 128 x 128 in blocks of eight 135 us at 16, 149 at 32).
 int plan_segments(int n_seqs, int64_t T, int H, int d_k, int d_v, int dtype)

@@ -14,7 +14,7 @@
 //     Dst = K^T V~           B = V~ = c . v, split in three bf16 parts (three passes)
 // The state itself stays in fp32 registers: S <- (prod a) S + Dst.  Its update must be good to fp32,
 // so V~ keeps the 24 bits of its fp32 products (two parts, 16 bits, left states 4e-6 off against 1e-7, and
-// took 188 us in place of 208 at T = 8192, H = 96); P and the state's copy are rounded to bf16 once each
+// took 188 us in place of 210 at T = 8192, H = 96); P and the state's copy are rounded to bf16 once each
 // (their products make the outputs, to which a bf16 rounding of the result is added anyway).
 //
 // Every weight is made of the decays of the very tokens it spans, never as a quotient or a difference of
@@ -35,7 +35,7 @@
 // Three issuing warps, because scores, state and outputs of neighbouring chunks overlap.
 //
 // What bounds it.  Bytes: 1 KB a token and head at d = 128 (T = 8192, H = 96: 815 MB, 120 us at the
-// measured copy rate).  Measured: 0.208 ms there (0.58 of that rate) on 96 of the 152 SMs, 6300 cycles a
+// measured copy rate).  Measured: 0.210 ms there (0.57 of that rate) on 96 of the 152 SMs, 6300 cycles a
 // chunk.  Shared memory's data path is 81 % busy: a product of two tiles in shared memory reads 8 KB in its
 // 64 cycles, all that the path carries, and the row work (V~, the state's copy, v) moves as much again
 // as a third of that.  The tensor pipe is 45 % busy.  With outputs TMEM is full (scores and P 128
@@ -49,7 +49,8 @@
 // the time, with six times the instruction-cache misses, so loops here are rolled where registers allow
 // and waits are a few instructions.
 // Few heads: the sequences are cut so that up to 152 CTAs work side by side, which costs a second read
-// of k and v (T = 65536, H = 8: 0.181 ms, 71 us of it the states, against 1.6 ms uncut).
+// of k and v (T = 65536, H = 8: 0.173 ms, with an initial state 0.181, 71 us of it the states, against
+// 1.51 ms uncut).
 #include <cudaTypedefs.h>
 
 #include <mutex>
