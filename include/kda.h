@@ -30,7 +30,7 @@
  *     (fp32, the accumulation precision, or bf16).  States and checkpoints are always fp32 and
  *     all accumulation is fp32.  Rounding outputs to bf16 costs up to 2^-9 of the largest |o|,
  *     which on the synthetic workloads is ~3.5e-2 of RMS(o): fp32 outputs are the precise form.
- *   - Every pointer passed must be 16-byte aligned.
+ *   - Every pointer passed must be 16-byte aligned (fp32 g and beta of the kda_delta calls: 4-byte).
  *   - Return value: KDA_OK (0) or a kda_status code; nothing is enqueued on error.  Checks that
  *     need device data (monotone cu_seqlens, finite inputs) are not made.  A bounded device
  *     wait that expires, or a state index out of range, sets a sticky per-device error word
@@ -52,7 +52,7 @@ typedef enum {
     KDA_ERR_MISALIGNED = 3,        /* a pointer not 16-byte aligned                           */
     KDA_ERR_CUDA = 4,              /* a CUDA runtime call or kernel launch failed             */
     KDA_ERR_DEVICE_TIMEOUT = 5,    /* a bounded device-side wait expired (device error word)  */
-    KDA_ERR_INDEX_RANGE = 6,       /* kda_state_copy met an index outside its slot range      */
+    KDA_ERR_INDEX_RANGE = 6,       /* kda_state_copy, _pack, _unpack met an index out of range  */
     KDA_ERR_DEVICE_BOUNDS = 7      /* a device-side bounds check failed (library built with
                                       -DKDA_DEBUG, or kda_diag_bounds_check)                    */
 } kda_status;
@@ -397,6 +397,80 @@ int64_t kda_linear_prefill_workspace(int32_t n_seqs, int64_t total_tokens, int32
 int kda_linear_decode(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
                       float *state, void *out, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads,
                       int32_t d_k, int32_t d_v, float scale, int32_t dtype, int32_t out_dtype, void *stream);
+
+/*
+ * kda_delta_prefill -- varlen prefill of the gated delta rule with one decay per head.
+ *
+ *     S' = exp(g_t) S_(t-1),   S_t = S' + beta_t k_t (v_t - S'^T k_t)^T,   o_t = scale S_t^T q_t
+ *
+ * KDA's recurrence with a scalar retention in place of the channel-wise one, without its floor, and with
+ * queries and keys that value heads share; the states have kda_prefill's layout.
+ *
+ *   q, k              [total_tokens, n_key_heads, d_k], v [total_tokens, H, d_v]; `dtype`.  Value head h
+ *                     reads query/key head h / (H / n_key_heads); every value head has a state of its own.
+ *   g                 fp32 log decays: [total_tokens, H] if g_per_token, else [H].  g <= 0; -inf forgets
+ *                     everything before the token.
+ *   beta              fp32 write gates [total_tokens, H].  With keys of norm at most 1 the recurrence is
+ *                     stable for beta in [0, 2]; nothing is clamped.
+ *   cu_seqlens, n_seqs, total_tokens, init_state, final_state   as for kda_prefill (init_state may
+ *                     be final_state).  An empty sequence's final state is its initial one.
+ *   out               [total_tokens, H, d_v] `out_dtype`.  out and final_state (but for init_state) must
+ *                     not alias an input or each other.
+ * Head sizes: multiples of 8 from 8 to 256.
+ * States, sums and decays are fp32, rounded once at the end.
+ * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_MISALIGNED, KDA_ERR_CUDA.
+ */
+int kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                      const float *beta, const int32_t *cu_seqlens, int32_t n_seqs, int64_t total_tokens,
+                      int32_t n_heads, int32_t n_key_heads, int32_t d_k, int32_t d_v, float scale, int32_t dtype,
+                      int32_t out_dtype, const float *init_state, void *out, float *final_state, void *stream);
+
+/*
+ * kda_delta_decode -- kda_delta_prefill's recurrence for one new token per sequence, state updated in
+ * place.
+ *   q, k [n_seqs, n_key_heads, d_k], v [n_seqs, H, d_v] (`dtype`);  g fp32 [n_seqs, H] if g_per_token,
+ *   else [H];  beta fp32 [n_seqs, H];  state fp32 [n_seqs, H, d_k, d_v];  out [n_seqs, H, d_v]
+ *   `out_dtype`.  out and state alias nothing.  Head sizes, errors: as for kda_delta_prefill.
+ */
+int kda_delta_decode(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                     const float *beta, float *state, void *out, int32_t n_seqs, int32_t n_heads,
+                     int32_t n_key_heads, int32_t d_k, int32_t d_v, float scale, int32_t dtype, int32_t out_dtype,
+                     void *stream);
+
+/* How a pool holds states in fewer bits (kda_state_pack). */
+typedef enum {
+    KDA_STATE_BF16 = 0, /* values rounded to bf16                                              */
+    KDA_STATE_INT8 = 1  /* whole numbers from -127 to 127, and an fp32 scale a row             */
+} kda_state_format;
+
+/*
+ * kda_state_pack -- states into slots of a pool that holds them in fewer bits:
+ *     dst[dst_idx[i]] = packed(src[src_idx[i]]),  i = 0 .. n-1,   src[i] of [H, d_k, d_v] fp32
+ * in the indexed form of kda_state_copy (prefix-reuse paragraph of the section cited above: states are
+ * kept at sparse checkpoints), for half or a quarter of the memory.
+ *
+ *   KDA_STATE_BF16    dst [n_dst_slots, H, d_k, d_v] bf16; dst_scales NULL.
+ *   KDA_STATE_INT8    dst int8 of that shape, dst_scales fp32 [n_dst_slots, H, d_k]: a row's scale
+ *                     s = max |x| / 127 (rounded to fp32) over its d_v values, its codes x / s rounded to
+ *                     the nearest whole number (the exact quotient, ties to even).  A row with a NaN
+ *                     or an infinity gets a NaN scale: it reads back as NaN throughout.
+ *   dst_idx, src_idx  device int64 [n] or NULL (identity).  An index outside its slot range skips that
+ *                     pair and shows as KDA_ERR_INDEX_RANGE in kda_device_status.  Two entries of dst_idx
+ *                     must not be the same.
+ * d_v a multiple of 4 up to 256, d_k up to 256.  dst, dst_scales and src share no memory (KDA_ERR_INVALID_ARG).
+ */
+int kda_state_pack(void *dst, float *dst_scales, int32_t format, const int64_t *dst_idx, int64_t n_dst_slots,
+                   const float *src, const int64_t *src_idx, int64_t n_src_slots, int64_t n, int32_t n_heads,
+                   int32_t d_k, int32_t d_v, void *stream);
+
+/*
+ * kda_state_unpack -- states read back from a pool that kda_state_pack filled:
+ *     dst[dst_idx[i]] = values(src[src_idx[i]]),   a bf16 value as it is, a code times its row's scale
+ * (rounded to fp32).  Arguments as for kda_state_pack, with dst fp32 and src the pool.
+ */
+int kda_state_unpack(float *dst, const int64_t *dst_idx, int64_t n_dst_slots, const void *src,
+                     const float *src_scales, int32_t format, const int64_t *src_idx, int64_t n_src_slots, int64_t n,
+                     int32_t n_heads, int32_t d_k, int32_t d_v, void *stream);
 
 /*
  * kda_norm_gate -- the norm over a head's channels on the mixer's output, with its gate:

@@ -22,7 +22,8 @@ from ._lib import KDAError
 
 __all__ = ["prefill", "prefill_recurrent", "decode", "state_copy", "device_status", "prefill_path",
            "num_checkpoints", "KDAError", "load", "diag_device_timeout", "diag_linear_timeout", "premix", "output_gate",
-           "prefill_staged", "linear_prefill", "linear_decode", "norm_gate", "residual_norm"]
+           "prefill_staged", "linear_prefill", "linear_decode", "norm_gate", "residual_norm", "delta_prefill",
+           "delta_decode", "state_pack", "state_unpack"]
 
 _DTYPES = {torch.bfloat16: _lib.KDA_BF16, torch.float32: _lib.KDA_F32}
 
@@ -336,6 +337,90 @@ def linear_decode(q, k, v, g, state, *, scale: float = 1.0, out=None, out_dtype=
     return out
 
 
+def _on_device(device: torch.device):
+    """A context in which `device` is the current one: where a call's kernels are launched."""
+    import contextlib
+
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _delta_inputs(q, k, v, g, beta):
+    """Checks shared by delta_prefill and delta_decode; returns the arguments that both C calls begin
+    with and their sizes: ((q, k, v, g, per_token, beta), rows, H, H_k, d_k, d_v)."""
+    if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor) or q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be tensors [T, heads, d]")
+    dev, dtype = q.device, q.dtype
+    if dtype not in _DTYPES:
+        raise ValueError("q/k/v must be bfloat16 or float32")
+    rows, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    if Hk < 1 or H < 1 or H % Hk != 0:
+        raise ValueError(f"{H} value heads cannot share {Hk} query/key heads evenly")
+    per_token = isinstance(g, torch.Tensor) and g.dim() == 2
+    _require(q, "q", dev, dtype)
+    _require(k, "k", dev, dtype, (rows, Hk, dk))
+    _require(v, "v", dev, dtype, (rows, H, dv))
+    _require(g, "g", dev, torch.float32, (rows, H) if per_token else (H,))
+    _require(beta, "beta", dev, torch.float32, (rows, H))
+    return (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), per_token, beta.data_ptr()), rows, H, Hk, dk, dv
+
+
+def delta_prefill(q, k, v, g, beta, cu_seqlens=None, init_state=None, *, scale: float = 1.0, out=None,
+                  final_state=True, out_dtype=None, stream=None):
+    """Varlen prefill of the gated delta rule with one decay per head (kda_delta_prefill):
+    S' = exp(g_t) S_(t-1), S_t = S' + beta_t k_t (v_t - S'^T k_t)^T, o_t = scale S_t^T q_t.
+
+    q, k: [T, H_k, d_k]; v: [T, H, d_v] (bf16 or fp32, contiguous, CUDA; H a multiple of H_k); g: fp32
+    log decays <= 0 (-inf forgets), [T, H] per token or [H] constant; beta: fp32 [T, H]; cu_seqlens: int32
+    [N+1] on the device or None for one sequence; init_state: fp32 [N, H, d_k, d_v] or None (zeros).
+    final_state: True to allocate, a tensor to fill (init_state itself for an in-place resume), or
+    None/False.  out_dtype defaults to out's, else q's.  Returns (out, final_state)."""
+    lib = _lib.load()
+    head, T, H, Hk, dk, dv = _delta_inputs(q, k, v, g, beta)
+    dev, dtype = q.device, q.dtype
+    n, cu = 1, None
+    if cu_seqlens is not None:
+        _require(cu_seqlens, "cu_seqlens", dev, torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [N + 1]")
+        n, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+    shape = (n, H, dk, dv)
+    if init_state is not None:
+        _require(init_state, "init_state", dev, torch.float32, shape)
+    with _on_stream(dev, stream):   # new outputs come from the pool of the stream that writes them
+        out = _out(out, out_dtype or (dtype if out is None else out.dtype), dev, (T, H, dv))
+        if final_state is True:
+            final_state = torch.empty(shape, device=dev, dtype=torch.float32)
+        elif final_state is False or final_state is None:
+            final_state = None
+        else:
+            _require(final_state, "final_state", dev, torch.float32, shape)
+    with _on_device(dev):
+        rc = lib.kda_delta_prefill(*head, cu, n, T, H, Hk, dk, dv, scale, _DTYPES[dtype], _DTYPES[out.dtype],
+                                   _ptr(init_state), out.data_ptr(), _ptr(final_state), _stream(dev, stream))
+    if rc:
+        _lib.check(rc, "kda_delta_prefill")
+    return out, final_state
+
+
+def delta_decode(q, k, v, g, beta, state, *, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """delta_prefill's recurrence for one token per sequence (kda_delta_decode): state [N, H, d_k, d_v]
+    fp32 is updated in place.  q, k: [N, H_k, d_k]; v: [N, H, d_v]; g: fp32 [N, H] or [H]; beta: fp32
+    [N, H].  Returns out [N, H, d_v] (out_dtype, default out's, else q's)."""
+    lib = _lib.load()
+    head, N, H, Hk, dk, dv = _delta_inputs(q, k, v, g, beta)
+    dev, dtype = q.device, q.dtype
+    _require(state, "state", dev, torch.float32, (N, H, dk, dv))
+    with _on_stream(dev, stream):
+        out = _out(out, out_dtype or (dtype if out is None else out.dtype), dev, (N, H, dv))
+    with _on_device(dev):
+        rc = lib.kda_delta_decode(*head, state.data_ptr(), out.data_ptr(), N, H, Hk, dk, dv, scale, _DTYPES[dtype],
+                                  _DTYPES[out.dtype], _stream(dev, stream))
+    if rc:
+        _lib.check(rc, "kda_delta_decode")
+    return out
+
+
 def norm_gate(o, z, w, *, eps: float = 1e-6, out=None, out_dtype=None, stream=None):
     """Norm over a head's channels with the output gate (kda_norm_gate):
     out = o * rsqrt(mean(o^2) + eps) * w * sigmoid(z).
@@ -494,6 +579,70 @@ def state_copy(dst, src, dst_idx=None, src_idx=None, n: Optional[int] = None, st
     rc = lib.kda_state_copy(_ptr(dst), _ptr(dst_idx), dst.shape[0], _ptr(src), _ptr(src_idx),
                             src.shape[0], int(n), H, dk, dv, _stream(dev, stream))
     _lib.check(rc, "kda_state_copy")
+    return dst
+
+
+_FORMATS = {torch.bfloat16: _lib.KDA_STATE_BF16, torch.int8: _lib.KDA_STATE_INT8}
+
+
+def _pack_inputs(held, scales, held_idx, full, full_idx, n):
+    """Checks shared by state_pack and state_unpack of a pool `held` and states `full`; returns (device,
+    n, H, d_k, d_v)."""
+    if not isinstance(held, torch.Tensor) or not isinstance(full, torch.Tensor):
+        raise TypeError("dst and src must be torch.Tensors")
+    dev = held.device
+    if held.dtype not in _FORMATS:
+        raise ValueError("a pool of packed states is bfloat16 or int8")
+    _require(held, "the pool", dev)
+    _require(full, "the states", dev, torch.float32)
+    if held.dim() != 4 or full.dim() != 4 or held.shape[1:] != full.shape[1:]:
+        raise ValueError("dst and src must be [slots, H, d_k, d_v] with the same H, d_k, d_v")
+    if held.dtype is torch.int8:
+        if scales is None:
+            raise ValueError("an int8 pool needs its scales")
+        _require(scales, "scales", dev, torch.float32, held.shape[:3])
+    elif scales is not None:
+        raise ValueError("scales belong to an int8 pool")
+    counts = []
+    for t, name in ((held_idx, "the pool's indices"), (full_idx, "the states' indices")):
+        if t is not None:
+            _require(t, name, dev, torch.int64)
+            counts.append(t.numel())
+    if n is None:   # as many as the indices name, else as there are slots
+        n = min(counts) if counts else min(held.shape[0], full.shape[0])
+        if counts and max(counts) != n:
+            raise ValueError(f"index arrays of {counts[0]} and {counts[1]} entries")
+    if any(int(n) > c for c in counts):   # the kernel reads n entries of each
+        raise ValueError(f"n = {n} exceeds the {min(counts)} entries of an index array")
+    return dev, int(n), *held.shape[1:]
+
+
+def state_pack(dst, src, dst_idx=None, src_idx=None, *, scales=None, n: Optional[int] = None, stream=None):
+    """dst[dst_idx[i]] = packed(src[src_idx[i]]) over whole states (kda_state_pack).
+    src: fp32 [slots, H, d_k, d_v]; dst: a pool of int8 [slots, H, d_k, d_v] with scales fp32 [slots, H, d_k]
+    (a row's max |x| / 127), or of bf16 without scales; indices: int64 device tensors or None (identity),
+    those of dst all different.  Returns dst."""
+    lib = _lib.load()
+    dev, n, H, dk, dv = _pack_inputs(dst, scales, dst_idx, src, src_idx, n)
+    with _on_device(dev):
+        rc = lib.kda_state_pack(dst.data_ptr(), _ptr(scales), _FORMATS[dst.dtype], _ptr(dst_idx), dst.shape[0],
+                                src.data_ptr(), _ptr(src_idx), src.shape[0], n, H, dk, dv, _stream(dev, stream))
+    if rc:
+        _lib.check(rc, "kda_state_pack")
+    return dst
+
+
+def state_unpack(dst, src, dst_idx=None, src_idx=None, *, scales=None, n: Optional[int] = None, stream=None):
+    """dst[dst_idx[i]] = values(src[src_idx[i]]) over whole states (kda_state_unpack): state_pack's way
+    back, dst fp32 and src the pool with its scales.  Returns dst."""
+    lib = _lib.load()
+    dev, n, H, dk, dv = _pack_inputs(src, scales, src_idx, dst, dst_idx, n)
+    with _on_device(dev):
+        rc = lib.kda_state_unpack(dst.data_ptr(), _ptr(dst_idx), dst.shape[0], src.data_ptr(), _ptr(scales),
+                                  _FORMATS[src.dtype], _ptr(src_idx), src.shape[0], n, H, dk, dv,
+                                  _stream(dev, stream))
+    if rc:
+        _lib.check(rc, "kda_state_unpack")
     return dst
 
 

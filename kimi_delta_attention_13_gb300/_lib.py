@@ -12,6 +12,8 @@ from . import build as _build
 KDA_OK = 0
 KDA_BF16 = 0
 KDA_F32 = 1
+KDA_STATE_BF16 = 0
+KDA_STATE_INT8 = 1
 STATUS_NAMES = {
     0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED_SHAPE", 3: "KDA_ERR_MISALIGNED",
     4: "KDA_ERR_CUDA", 5: "KDA_ERR_DEVICE_TIMEOUT", 6: "KDA_ERR_INDEX_RANGE", 7: "KDA_ERR_DEVICE_BOUNDS",
@@ -46,6 +48,12 @@ SIGNATURES = {
     "kda_linear_prefill_workspace": (ctypes.c_int64, [_i32, _i64, _i32, _i32, _i32, _i32]),
     "kda_linear_decode": (ctypes.c_int, [_vp] * 4 + [_i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                           ctypes.c_float, _i32, _i32, _vp]),
+    "kda_delta_prefill": (ctypes.c_int, [_vp] * 4 + [_i32, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _i32,
+                                          ctypes.c_float, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "kda_delta_decode": (ctypes.c_int, [_vp] * 4 + [_i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                         ctypes.c_float, _i32, _i32, _vp]),
+    "kda_state_pack": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp]),
+    "kda_state_unpack": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _i64, _i32, _i32, _i32, _vp]),
     "kda_norm_gate": (ctypes.c_int, [_vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i64, _i32, _i32,
                                       ctypes.c_float, _vp]),
     "kda_residual_norm": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, ctypes.c_float,

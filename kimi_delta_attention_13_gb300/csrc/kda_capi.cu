@@ -97,6 +97,8 @@ bool bad_linear_dims(int32_t d_k, int32_t d_v)
     return d_k < 8 || d_k > 256 || d_k % 8 != 0 || d_v < 8 || d_v > 256 || d_v % 8 != 0;
 }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // Whether an output's address is one of those it must not share.
 bool aliases(const void *out, std::initializer_list<const void *> others)
 {
@@ -104,6 +106,36 @@ bool aliases(const void *out, std::initializer_list<const void *> others)
         for (const void *p : others)
             if (out == p) return true;
     return false;
+}
+
+// Whether two ranges of memory meet.
+bool meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && a_bytes > 0 && b_bytes > 0 && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+// Validation shared by kda_state_pack and kda_state_unpack: the pool (`held`, `scales`) and the states.
+int check_pack(const void *held, const float *scales, int32_t format, const int64_t *held_idx, int64_t n_held,
+               const float *full, const int64_t *full_idx, int64_t n_full, int64_t n, int32_t n_heads, int32_t d_k,
+               int32_t d_v)
+{
+    if (n < 0 || n_held < 0 || n_full < 0 || n_heads < 1 || d_k < 1 || d_v < 1 ||
+        (format != KDA_STATE_BF16 && format != KDA_STATE_INT8))
+        return KDA_ERR_INVALID_ARG;
+    if (d_k > 256 || d_v > 256 || d_v % 4 != 0) return KDA_ERR_UNSUPPORTED_SHAPE;
+    if (n > 0 && (!held || !full)) return KDA_ERR_INVALID_ARG;
+    if (format == KDA_STATE_INT8 ? n > 0 && !scales : scales != nullptr) return KDA_ERR_INVALID_ARG;
+    if ((!held_idx && n > n_held) || (!full_idx && n > n_full)) return KDA_ERR_INVALID_ARG;
+    const void *ptrs[] = {held, scales, held_idx, full, full_idx};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    const int64_t rows = (int64_t)n_heads * d_k, held_bytes = n_held * rows * d_v * (format == KDA_STATE_INT8 ? 1 : 2);
+    const int64_t full_bytes = n_full * rows * d_v * 4, scale_bytes = n_held * rows * 4;
+    if (meet(held, held_bytes, full, full_bytes) || meet(scales, scale_bytes, full, full_bytes) ||
+        meet(scales, scale_bytes, held, held_bytes))
+        return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
 }
 
 }  // namespace
@@ -357,6 +389,76 @@ int kda_linear_decode(const void *q, const void *k, const void *v, const float *
                                 d_v, scale, dtype, out_dtype, (cudaStream_t)stream);
 }
 
+int kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                      const float *beta, const int32_t *cu_seqlens, int32_t n_seqs, int64_t total_tokens,
+                      int32_t n_heads, int32_t n_key_heads, int32_t d_k, int32_t d_v, float scale, int32_t dtype,
+                      int32_t out_dtype, const float *init_state, void *out, float *final_state, void *stream)
+{
+    const CallRange range("kda_delta_prefill");
+    if (n_seqs < 0 || total_tokens < 0 || n_heads < 1 || n_key_heads < 1 || n_heads % n_key_heads != 0 ||
+        d_k < 1 || d_v < 1 || bad_dtype(dtype) || bad_dtype(out_dtype) || !std::isfinite(scale))
+        return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!q || !k || !v || !g || !beta || !out)) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && n_seqs == 0) return KDA_ERR_INVALID_ARG;
+    if (!cu_seqlens && n_seqs > 1) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;   // cu_seqlens are int32
+    if (bad_linear_dims(d_k, d_v)) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const void *ptrs[] = {q, k, v, init_state, out, final_state};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    if (!aligned4(g) || !aligned4(beta) || !aligned4(cu_seqlens)) return KDA_ERR_MISALIGNED;
+    if (aliases(out, {q, k, v, g, beta, cu_seqlens, init_state, final_state}) ||
+        aliases(final_state, {q, k, v, g, beta, cu_seqlens}))
+        return KDA_ERR_INVALID_ARG;
+    return launch_delta_prefill(q, k, v, g, g_per_token != 0, beta, cu_seqlens, n_seqs, total_tokens, n_heads,
+                                n_key_heads, d_k, d_v, scale, dtype, out_dtype, init_state, out, final_state,
+                                (cudaStream_t)stream);
+}
+
+int kda_delta_decode(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                     const float *beta, float *state, void *out, int32_t n_seqs, int32_t n_heads,
+                     int32_t n_key_heads, int32_t d_k, int32_t d_v, float scale, int32_t dtype, int32_t out_dtype,
+                     void *stream)
+{
+    const CallRange range("kda_delta_decode");
+    if (n_seqs < 0 || n_heads < 1 || n_key_heads < 1 || n_heads % n_key_heads != 0 || d_k < 1 || d_v < 1 ||
+        bad_dtype(dtype) || bad_dtype(out_dtype) || !std::isfinite(scale))
+        return KDA_ERR_INVALID_ARG;
+    if (n_seqs > 0 && (!q || !k || !v || !g || !beta || !state || !out)) return KDA_ERR_INVALID_ARG;
+    if (bad_linear_dims(d_k, d_v)) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const void *ptrs[] = {q, k, v, state, out};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
+    if (!aligned4(g) || !aligned4(beta)) return KDA_ERR_MISALIGNED;
+    if (aliases(out, {q, k, v, g, beta, state}) || aliases(state, {q, k, v, g, beta})) return KDA_ERR_INVALID_ARG;
+    return launch_delta_decode(q, k, v, g, g_per_token != 0, beta, state, out, n_seqs, n_heads, n_key_heads, d_k,
+                               d_v, scale, dtype, out_dtype, (cudaStream_t)stream);
+}
+
+int kda_state_pack(void *dst, float *dst_scales, int32_t format, const int64_t *dst_idx, int64_t n_dst_slots,
+                   const float *src, const int64_t *src_idx, int64_t n_src_slots, int64_t n, int32_t n_heads,
+                   int32_t d_k, int32_t d_v, void *stream)
+{
+    const CallRange range("kda_state_pack");
+    const int rc = check_pack(dst, dst_scales, format, dst_idx, n_dst_slots, src, src_idx, n_src_slots, n, n_heads,
+                              d_k, d_v);
+    if (rc != KDA_OK) return rc;
+    return launch_state_pack(dst, dst_scales, format, dst_idx, n_dst_slots, src, src_idx, n_src_slots, n,
+                             (int64_t)n_heads * d_k, d_v, (cudaStream_t)stream);
+}
+
+int kda_state_unpack(float *dst, const int64_t *dst_idx, int64_t n_dst_slots, const void *src,
+                     const float *src_scales, int32_t format, const int64_t *src_idx, int64_t n_src_slots, int64_t n,
+                     int32_t n_heads, int32_t d_k, int32_t d_v, void *stream)
+{
+    const CallRange range("kda_state_unpack");
+    const int rc = check_pack(src, src_scales, format, src_idx, n_src_slots, dst, dst_idx, n_dst_slots, n, n_heads,
+                              d_k, d_v);
+    if (rc != KDA_OK) return rc;
+    return launch_state_unpack(dst, dst_idx, n_dst_slots, src, src_scales, format, src_idx, n_src_slots, n,
+                               (int64_t)n_heads * d_k, d_v, (cudaStream_t)stream);
+}
+
 int kda_norm_gate(const void *o, int32_t o_dtype, const void *z, int32_t z_dtype, const float *w,
                   int32_t w_heads, void *out, int32_t out_dtype, int64_t tokens, int32_t n_heads, int32_t d,
                   float eps, void *stream)
@@ -498,6 +600,10 @@ int kda_device_status(int32_t *status, void *stream)
     rc = read_and_clear_status_linear((cudaStream_t)stream, &lt);
     if (rc != KDA_OK) return rc;
     if (c == KDA_OK) c = lt;
+    int32_t pk = 0;
+    rc = read_and_clear_status_state_pack((cudaStream_t)stream, &pk);
+    if (rc != KDA_OK) return rc;
+    if (a == KDA_OK) a = pk;
     *status = b != KDA_OK ? b : (c != KDA_OK ? c : a);
     return KDA_OK;
 }

@@ -62,6 +62,7 @@ int read_and_clear_status_prefill_tc_precise(cudaStream_t s, int32_t *status);
 int read_and_clear_status_decode(cudaStream_t s, int32_t *status);
 int read_and_clear_status_cp(cudaStream_t s, int32_t *status);
 int read_and_clear_status_linear(cudaStream_t s, int32_t *status);
+int read_and_clear_status_state_pack(cudaStream_t s, int32_t *status);
 // Launch the one-CTA probe whose bounded device wait expires after `cycles` SM cycles.
 int launch_wait_timeout_probe(long long cycles, cudaStream_t stream);
 // The same with the linear-attention prefill's wait.
@@ -98,6 +99,19 @@ int launch_linear_prefill(const void *q, const void *k, const void *v, const flo
 int launch_linear_decode(const void *q, const void *k, const void *v, const float *g, int g_per_token,
                          float *state, void *out, int n_seqs, int H, int Hkv, int d_k, int d_v, float scale,
                          int dtype, int out_dtype, cudaStream_t stream);
+int launch_delta_prefill(const void *q, const void *k, const void *v, const float *g, int g_per_token,
+                         const float *beta, const int32_t *cu, int n_seqs, int64_t T, int H, int Hk, int d_k,
+                         int d_v, float scale, int dtype, int out_dtype, const float *init, void *out,
+                         float *final_state, cudaStream_t stream);
+int launch_delta_decode(const void *q, const void *k, const void *v, const float *g, int g_per_token,
+                        const float *beta, float *state, void *out, int n_seqs, int H, int Hk, int d_k, int d_v,
+                        float scale, int dtype, int out_dtype, cudaStream_t stream);
+// states into (from) the slots of a pool of fewer bits; rows = n_heads d_k of a state
+int launch_state_pack(void *dst, float *scales, int format, const int64_t *dst_idx, int64_t n_dst, const float *src,
+                      const int64_t *src_idx, int64_t n_src, int64_t n, int64_t rows, int dv, cudaStream_t stream);
+int launch_state_unpack(float *dst, const int64_t *dst_idx, int64_t n_dst, const void *src, const float *scales,
+                        int format, const int64_t *src_idx, int64_t n_src, int64_t n, int64_t rows, int dv,
+                        cudaStream_t stream);
 int launch_norm_gate(const void *o, int o_dtype, const void *z, int z_dtype, const float *w, int w_heads,
                      void *out, int out_dtype, int64_t T, int H, int d, float eps, cudaStream_t stream);
 int launch_residual_norm(const void *x, int res_dtype, const void *y, const void *z, int dtype,

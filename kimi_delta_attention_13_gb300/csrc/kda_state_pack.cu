@@ -1,0 +1,244 @@
+// kda_state_pack.cu -- states kept in fewer bits: written into slots of a pool and read back.
+//
+//     bf16:  held = x rounded to bf16
+//     int8:  s = max |row| / 127 in fp32,  held = x / s rounded to the nearest whole number, ties to even,
+//            per row of a state (one key channel's value channels);   read back as held s
+//
+// A row has a scale of its own because a state's key channels differ in magnitude by what was written under
+// them.  The code is that of the exact quotient: the remainder x - code s is exact in one fused
+// multiply-add, and a code that it shows to be the wrong neighbour is moved by one.
+// Bound by HBM: 4 bytes an element on one side, 1 (and 4 a row) or 2 on the other.  LANES lanes take a row,
+// four columns each (a row past 128 columns in two pieces), and a warp has four loads in flight.
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kDepth = 4;             // rows (or pieces of them) in flight a thread
+
+__device__ int g_state_pack_error;    // sticky device error word of this translation unit
+
+struct Move {
+    void *held;                 // pool [n_held, rows, dv] of int8 or bf16
+    float *scales;              // [n_held, rows] (int8)
+    float *full;                // states [n_full, rows, dv] fp32
+    const int64_t *held_idx, *full_idx;
+    int64_t n_held, n_full, n;
+    int64_t rows;               // of a state: H dk
+    int dv;
+};
+
+// the slots of pair i; false (and the error word) where one is out of range
+__device__ __forceinline__ bool slots(const Move &m, int64_t i, int64_t &held, int64_t &full)
+{
+    held = m.held_idx ? m.held_idx[i] : i;
+    full = m.full_idx ? m.full_idx[i] : i;
+    if (held >= 0 && held < m.n_held && full >= 0 && full < m.n_full) return true;
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicExch(&g_state_pack_error, KDA_ERR_INDEX_RANGE);
+    return false;
+}
+
+__device__ __forceinline__ uint32_t code8(float x, float s, float inv)
+{
+    float r = rintf(inv > 0.f ? x * inv : x / s);
+    const float left = fmaf(-r, s, x);               // exact: at most about s / 2, in units of the smaller ulp
+    const float twice = 2.f * fabsf(left);
+    if (twice > s || (twice == s && ((int)r & 1))) r += copysignf(1.f, left);
+    return (uint32_t)(int)fminf(fmaxf(r, -127.f), 127.f) & 0xffu;
+}
+
+// LANES lanes a row of at most 4 LANES V columns
+template <int LANES, int V>
+__global__ void __launch_bounds__(kThreads) state_pack8_kernel(const Move m)
+{
+    constexpr int SIDE = kThreads / LANES;           // rows of the block side by side
+    constexpr int U = V == 1 ? kDepth : kDepth / 2;
+    const int lane = threadIdx.x % LANES, side = threadIdx.x / LANES;
+    for (int64_t i = blockIdx.y; i < m.n; i += gridDim.y) {
+        int64_t hs, fs;
+        if (!slots(m, i, hs, fs)) continue;
+        const float *from = m.full + fs * m.rows * m.dv;
+        uint8_t *to = static_cast<uint8_t *>(m.held) + hs * m.rows * m.dv;
+        float *scales = m.scales + hs * m.rows;
+        for (int64_t r0 = (int64_t)blockIdx.x * SIDE * U; r0 < m.rows; r0 += (int64_t)gridDim.x * SIDE * U) {
+            float4 x[U][V];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    const int64_t row = r0 + u * SIDE + side;
+                    const int col = 4 * (lane + c * LANES);
+                    x[u][c] = row < m.rows && col < m.dv ? __ldcs(reinterpret_cast<const float4 *>(from + row * m.dv + col))
+                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                uint32_t top = 0;                    // magnitudes as bits: infinities and NaN are the largest
+#pragma unroll
+                for (int c = 0; c < V; ++c)
+                    top = max(top, max(max(__float_as_uint(x[u][c].x) & 0x7fffffffu, __float_as_uint(x[u][c].y) & 0x7fffffffu),
+                                       max(__float_as_uint(x[u][c].z) & 0x7fffffffu, __float_as_uint(x[u][c].w) & 0x7fffffffu)));
+#pragma unroll
+                for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float s = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(top), 127.f);
+                // (the reciprocal of a scale that is all but 0 would overflow)
+                const float inv = s >= 1e-30f ? 1.f / s : 0.f;
+                const int64_t row = r0 + u * SIDE + side;
+                if (row >= m.rows) continue;
+                if (lane == 0) scales[row] = s;
+                const bool any = s > 0.f;            // else a row of zeros, or one not finite: codes 0
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    const int col = 4 * (lane + c * LANES);
+                    if (col >= m.dv) continue;
+                    const float4 f = x[u][c];
+                    uint32_t w = 0;
+                    if (any)
+                        w = code8(f.x, s, inv) | code8(f.y, s, inv) << 8 | code8(f.z, s, inv) << 16 | code8(f.w, s, inv) << 24;
+                    *reinterpret_cast<uint32_t *>(to + row * m.dv + col) = w;
+                }
+            }
+        }
+    }
+}
+
+template <int LANES, int V>
+__global__ void __launch_bounds__(kThreads) state_unpack8_kernel(const Move m)
+{
+    constexpr int SIDE = kThreads / LANES;
+    constexpr int U = 2 * (V == 1 ? kDepth : kDepth / 2);
+    const int lane = threadIdx.x % LANES, side = threadIdx.x / LANES;
+    for (int64_t i = blockIdx.y; i < m.n; i += gridDim.y) {
+        int64_t hs, fs;
+        if (!slots(m, i, hs, fs)) continue;
+        float *to = m.full + fs * m.rows * m.dv;
+        const uint8_t *from = static_cast<const uint8_t *>(m.held) + hs * m.rows * m.dv;
+        const float *scales = m.scales + hs * m.rows;
+        for (int64_t r0 = (int64_t)blockIdx.x * SIDE * U; r0 < m.rows; r0 += (int64_t)gridDim.x * SIDE * U) {
+            uint32_t w[U][V];
+            float s[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = r0 + u * SIDE + side;
+                s[u] = row < m.rows ? __ldg(scales + row) : 0.f;
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    const int col = 4 * (lane + c * LANES);
+                    w[u][c] = row < m.rows && col < m.dv ? __ldcs(reinterpret_cast<const uint32_t *>(from + row * m.dv + col)) : 0u;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < V; ++c) {
+                    const int64_t row = r0 + u * SIDE + side;
+                    const int col = 4 * (lane + c * LANES);
+                    if (row < m.rows && col < m.dv) {
+                        const uint32_t x = w[u][c];
+                        __stcs(reinterpret_cast<float4 *>(to + row * m.dv + col),
+                               make_float4((float)(int8_t)(x & 0xffu) * s[u], (float)(int8_t)(x >> 8 & 0xffu) * s[u],
+                                           (float)(int8_t)(x >> 16 & 0xffu) * s[u], (float)(int8_t)(x >> 24) * s[u]));
+                    }
+                }
+        }
+    }
+}
+
+template <bool PACK>
+__global__ void __launch_bounds__(kThreads) state_bf16_kernel(const Move m)
+{
+    constexpr int U = 4;
+    const int64_t vecs = m.rows * m.dv / 4, stride = (int64_t)gridDim.x * kThreads;
+    for (int64_t i = blockIdx.y; i < m.n; i += gridDim.y) {
+        int64_t hs, fs;
+        if (!slots(m, i, hs, fs)) continue;
+        float4 *full = reinterpret_cast<float4 *>(m.full) + fs * vecs;
+        uint2 *held = static_cast<uint2 *>(m.held) + hs * vecs;
+        for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < vecs; e += U * stride) {
+            if constexpr (PACK) {
+                float4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (e + u * stride < vecs) x[u] = __ldcs(full + e + u * stride);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (e + u * stride < vecs) {
+                        const __nv_bfloat162 a = __floats2bfloat162_rn(x[u].x, x[u].y), b = __floats2bfloat162_rn(x[u].z, x[u].w);
+                        held[e + u * stride] = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+                    }
+            } else {
+                uint2 w[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (e + u * stride < vecs) w[u] = __ldcs(held + e + u * stride);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (e + u * stride < vecs)
+                        __stcs(full + e + u * stride,
+                               make_float4(__uint_as_float(w[u].x << 16), __uint_as_float(w[u].x & 0xffff0000u),
+                                           __uint_as_float(w[u].y << 16), __uint_as_float(w[u].y & 0xffff0000u)));
+            }
+        }
+    }
+}
+
+int run(const Move &m, int format, bool pack, cudaStream_t stream)
+{
+    if (m.n == 0) return KDA_OK;
+    if (m.dv % 4 != 0 || m.dv > 256) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const unsigned ys = (unsigned)(m.n < 65535 ? m.n : 65535);
+    auto blocks = [&](int64_t each) {   // of a state, `each` rows or vectors a block
+        const int64_t rows = format == KDA_STATE_INT8 ? m.rows : m.rows * m.dv / 4;
+        const int64_t b = (rows + each - 1) / each;
+        return dim3((unsigned)(b < 65536 ? b : 65536), ys);
+    };
+    if (format == KDA_STATE_BF16) {
+        if (pack) state_bf16_kernel<true><<<blocks(4 * kThreads), kThreads, 0, stream>>>(m);
+        else state_bf16_kernel<false><<<blocks(4 * kThreads), kThreads, 0, stream>>>(m);
+    } else {
+        const int depth = m.dv <= 128 ? kDepth : kDepth / 2;
+        if (pack) {
+            if (m.dv <= 32) state_pack8_kernel<8, 1><<<blocks(kThreads / 8 * depth), kThreads, 0, stream>>>(m);
+            else if (m.dv <= 64) state_pack8_kernel<16, 1><<<blocks(kThreads / 16 * depth), kThreads, 0, stream>>>(m);
+            else if (m.dv <= 128) state_pack8_kernel<32, 1><<<blocks(kThreads / 32 * depth), kThreads, 0, stream>>>(m);
+            else state_pack8_kernel<32, 2><<<blocks(kThreads / 32 * depth), kThreads, 0, stream>>>(m);
+        } else {
+            if (m.dv <= 32) state_unpack8_kernel<8, 1><<<blocks(kThreads / 8 * 2 * depth), kThreads, 0, stream>>>(m);
+            else if (m.dv <= 64) state_unpack8_kernel<16, 1><<<blocks(kThreads / 16 * 2 * depth), kThreads, 0, stream>>>(m);
+            else if (m.dv <= 128) state_unpack8_kernel<32, 1><<<blocks(kThreads / 32 * 2 * depth), kThreads, 0, stream>>>(m);
+            else state_unpack8_kernel<32, 2><<<blocks(kThreads / 32 * 2 * depth), kThreads, 0, stream>>>(m);
+        }
+    }
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_state_pack(void *dst, float *scales, int format, const int64_t *dst_idx, int64_t n_dst, const float *src,
+                      const int64_t *src_idx, int64_t n_src, int64_t n, int64_t rows, int dv, cudaStream_t stream)
+{
+    const Move m{dst, scales, const_cast<float *>(src), dst_idx, src_idx, n_dst, n_src, n, rows, dv};
+    return run(m, format, true, stream);
+}
+
+int launch_state_unpack(float *dst, const int64_t *dst_idx, int64_t n_dst, const void *src, const float *scales,
+                        int format, const int64_t *src_idx, int64_t n_src, int64_t n, int64_t rows, int dv,
+                        cudaStream_t stream)
+{
+    const Move m{const_cast<void *>(src), const_cast<float *>(scales), dst, src_idx, dst_idx, n_src, n_dst, n, rows, dv};
+    return run(m, format, false, stream);
+}
+
+int read_and_clear_status_state_pack(cudaStream_t s, int32_t *status)
+{
+    int host = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&host, g_state_pack_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_state_pack_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    *status = host;
+    return KDA_OK;
+}
+
+}  // namespace kda

@@ -7,10 +7,13 @@ first tokens match a cached sequence therefore:
 1. restores the state of the longest checkpoint within the shared prefix (`kda_state_copy`);
 2. prefills only the tokens after it, starting from that state (`kda_prefill` with `init_state`).
 
+States may be kept in fewer bits than they are worked on in (`CheckpointStore(..., dtype=...)`): packed as
+they are stored (`kda_state_pack`), read back as they are restored (`kda_state_unpack`).
+
 `CheckpointStore` is a device pool of checkpoint slots with a host-side index. It takes the
 checkpoints a prefill emitted (`ckpt_stride`, `ckpts`), and answers "which slot holds the state
 after n tokens of sequence `key`". `resume_prefill` restores a batch of requests from their slots in
-one `kda_state_copy` and runs one varlen `kda_prefill` over their remaining tokens.
+one `kda_state_copy` (or `kda_state_unpack`) and runs one varlen `kda_prefill` over their remaining tokens.
 
 All device work goes through the library's C ABI; this module only keeps the index.
 """
@@ -20,17 +23,24 @@ from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
 
-from . import num_checkpoints, prefill, state_copy
+from . import num_checkpoints, prefill, state_copy, state_pack, state_unpack
 
 
 class CheckpointStore:
-    """A pool of `n_slots` fp32 states [n_slots, H, d_k, d_v] on `device`, filled round-robin
-    (the oldest entry is overwritten when the pool is full), indexed by (key, tokens covered)."""
+    """A pool of `n_slots` states [n_slots, H, d_k, d_v] on `device`, filled round-robin
+    (the oldest entry is overwritten when the pool is full), indexed by (key, tokens covered).
+    dtype: float32 (as they are), int8 (a quarter of the memory: a value is off by at most 1/254 of its
+    row's largest, rows being key channels, whose scales are `scales`), or bfloat16 (half: at most 2^-9 of
+    the value)."""
 
-    def __init__(self, n_slots: int, heads: int, d_k: int = 128, d_v: int = 128, device=None):
+    def __init__(self, n_slots: int, heads: int, d_k: int = 128, d_v: int = 128, device=None,
+                 dtype: torch.dtype = torch.float32):
         if n_slots < 1:
             raise ValueError("n_slots must be positive")
-        self.states = torch.empty(n_slots, heads, d_k, d_v, device=device, dtype=torch.float32)
+        if dtype not in (torch.float32, torch.bfloat16, torch.int8):
+            raise ValueError("a store holds float32, bfloat16 or int8 states")
+        self.states = torch.empty(n_slots, heads, d_k, d_v, device=device, dtype=dtype)
+        self.scales = torch.empty(n_slots, heads, d_k, device=device) if dtype is torch.int8 else None
         self._index: Dict[Tuple[object, int], int] = {}
         self._owner: List[Optional[Tuple[object, int]]] = [None] * n_slots
         self._next = 0
@@ -38,6 +48,20 @@ class CheckpointStore:
     @property
     def n_slots(self) -> int:
         return self.states.shape[0]
+
+    def write(self, slots: torch.Tensor, states: torch.Tensor, rows: torch.Tensor, stream=None) -> None:
+        """states[rows[i]] into slot slots[i] (int64 device tensors, the slots all different)."""
+        if self.states.dtype is torch.float32:
+            state_copy(self.states, states, slots, rows, stream=stream)
+        else:
+            state_pack(self.states, states, slots, rows, scales=self.scales, stream=stream)
+
+    def read(self, states: torch.Tensor, rows: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+        """states[rows[i]] = what slot slots[i] holds, in fp32."""
+        if self.states.dtype is torch.float32:
+            state_copy(states, self.states, rows, slots, stream=stream)
+        else:
+            state_unpack(states, self.states, rows, slots, scales=self.scales, stream=stream)
 
     def _take_slot(self, entry: Tuple[object, int]) -> int:
         slot = self._next
@@ -73,7 +97,7 @@ class CheckpointStore:
         dst = [self._take_slot(e) for e in entries]
         if entries:
             dev = self.states.device
-            state_copy(self.states, ckpts, torch.tensor(dst, device=dev, dtype=torch.int64),
+            self.write(torch.tensor(dst, device=dev, dtype=torch.int64), ckpts,
                        torch.tensor(src, device=dev, dtype=torch.int64), stream=stream)
         return [(k, n, s) for (k, n), s in zip(entries, dst)]
 
@@ -101,8 +125,7 @@ def resume_prefill(store: CheckpointStore, slots: Sequence[Optional[int]], q, k,
     init = torch.zeros(n, H, dk, dv, device=dev, dtype=torch.float32)
     pairs = [(i, s) for i, s in enumerate(slots) if s is not None]
     if pairs:
-        state_copy(init, store.states,
-                   torch.tensor([i for i, _ in pairs], device=dev, dtype=torch.int64),
+        store.read(init, torch.tensor([i for i, _ in pairs], device=dev, dtype=torch.int64),
                    torch.tensor([s for _, s in pairs], device=dev, dtype=torch.int64), stream=stream)
     o, f, _ = prefill(q, k, v, g, beta, cu_seqlens, init, out=out, final_state=final_state,
                       lengths=lengths, out_dtype=out_dtype, stream=stream)
