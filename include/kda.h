@@ -417,7 +417,14 @@ int kda_linear_decode(const void *q, const void *k, const void *v, const float *
  *   out               [total_tokens, H, d_v] `out_dtype`.  out and final_state (but for init_state) must
  *                     not alias an input or each other.
  * Head sizes: multiples of 8 from 8 to 256.
- * States, sums and decays are fp32, rounded once at the end.
+ * States, sums and decays are fp32.  bf16 inputs with head sizes up to 128 take the tensor-core kernel
+ * (but for batches of a few tokens a sequence): chunks of 64 tokens, whose new values are good to fp32 (operands
+ * in three bf16 parts), and with them the states; what outputs sum is rounded once to bf16 where it is a
+ * weighted score (each output is within 2^-8 of the sum of its terms' magnitudes, fp32 outputs too).  All else
+ * is fp32 throughout, rounded once at the end.
+ * The tensor-core kernel's waits are bounded (2e9 SM cycles, about 1 s): one that gave up shows as
+ * KDA_ERR_DEVICE_TIMEOUT in kda_device_status.  A NaN or infinity in an input of a sequence leaves the other
+ * sequences as they are; within its own it may also reach outputs up to 15 tokens before it.
  * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_MISALIGNED, KDA_ERR_CUDA.
  */
 int kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
@@ -516,7 +523,7 @@ int kda_device_status(int32_t *status, void *stream);
  * device wait is on a barrier that nothing completes; after `timeout_cycles` SM clock cycles
  * (1 .. 4e9; 2e6 is about 1 ms) the wait gives up and records KDA_ERR_DEVICE_TIMEOUT in the device
  * error word, through the wait routine of the library's kernels (kda_linear_prefill's has one of its
- * own, see kda_diag_linear_timeout).  A following
+ * own, see kda_diag_linear_timeout, kda_diag_delta_timeout).  A following
  * kda_device_status() returns that code and clears it; the CUDA context stays usable.  The pages
  * have no counterpart: it exists so that a caller (or a test) can see an expired device wait
  * surface as an error status instead of a hang.
@@ -530,6 +537,9 @@ int kda_diag_device_timeout(int64_t timeout_cycles, void *stream);
  * 2e9 SM cycles (about 1 s).  Arguments and errors as there.
  */
 int kda_diag_linear_timeout(int64_t timeout_cycles, void *stream);
+
+/* kda_diag_delta_timeout -- the same for the wait of kda_delta_prefill's tensor-core kernel. */
+int kda_diag_delta_timeout(int64_t timeout_cycles, void *stream);
 
 /*
  * kda_diag_bounds_check -- the device-side bounds check of a debug build, shown to work.  A library

@@ -559,6 +559,12 @@ int kda_diag_linear_timeout(int64_t timeout_cycles, void *stream)
     return kda::launch_linear_timeout_probe((uint32_t)timeout_cycles, (cudaStream_t)stream);
 }
 
+int kda_diag_delta_timeout(int64_t timeout_cycles, void *stream)
+{
+    if (timeout_cycles < 1 || timeout_cycles > 4000000000LL) return KDA_ERR_INVALID_ARG;
+    return kda::launch_delta_timeout_probe((uint32_t)timeout_cycles, (cudaStream_t)stream);
+}
+
 int kda_diag_staged_handles(int64_t *created)
 {
     if (!created) return KDA_ERR_INVALID_ARG;
@@ -600,6 +606,10 @@ int kda_device_status(int32_t *status, void *stream)
     rc = read_and_clear_status_linear((cudaStream_t)stream, &lt);
     if (rc != KDA_OK) return rc;
     if (c == KDA_OK) c = lt;
+    int32_t dt = 0;
+    rc = read_and_clear_status_delta((cudaStream_t)stream, &dt);
+    if (rc != KDA_OK) return rc;
+    if (c == KDA_OK) c = dt;
     int32_t pk = 0;
     rc = read_and_clear_status_state_pack((cudaStream_t)stream, &pk);
     if (rc != KDA_OK) return rc;

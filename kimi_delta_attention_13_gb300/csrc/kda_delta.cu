@@ -170,6 +170,12 @@ int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream)
     return out_dtype == KDA_BF16 ? launch<float, __nv_bfloat16>(p, stream) : launch<float, float>(p, stream);
 }
 
+// Whether the tensor-core kernel takes these operands.
+bool tc_path(int n_seqs, int64_t T, int d_k, int d_v, int dtype)
+{
+    return dtype == KDA_BF16 && d_k <= 128 && d_v <= 128 && T >= 8 * (int64_t)n_seqs;
+}
+
 }  // namespace delta
 
 int launch_delta_prefill(const void *q, const void *k, const void *v, const float *g, int g_per_token,
@@ -193,6 +199,7 @@ int launch_delta_prefill(const void *q, const void *k, const void *v, const floa
     p.init = init;
     p.out = out;
     p.final_state = final_state;
+    if (delta::tc_path(n_seqs, T, d_k, d_v, dtype)) return delta::run_tc_path(p, out_dtype, stream);
     return delta::run_token_path(p, dtype, out_dtype, stream);
 }
 

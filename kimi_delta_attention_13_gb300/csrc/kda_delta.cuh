@@ -61,6 +61,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 }
 
 int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream);
+int run_tc_path(const Args &p, int out_dtype, cudaStream_t stream);   // bf16 operands, d <= 128
 
 }  // namespace delta
 }  // namespace kda

@@ -30,7 +30,7 @@ class CheckpointStore:
     """A pool of `n_slots` states [n_slots, H, d_k, d_v] on `device`, filled round-robin
     (the oldest entry is overwritten when the pool is full), indexed by (key, tokens covered).
     dtype: float32 (as they are), int8 (a quarter of the memory: a value is off by at most 1/254 of its
-    row's largest, rows being key channels, whose scales are `scales`), or bfloat16 (half: at most 2^-9 of
+    row's largest, rows being key channels, whose scales are `scales`), or bfloat16 (half: at most 2^-8 of
     the value)."""
 
     def __init__(self, n_slots: int, heads: int, d_k: int = 128, d_v: int = 128, device=None,

@@ -53,3 +53,64 @@ def inputs(lengths, heads, keys, dk, dv, dtype, seed, per_token=True, init=False
     x["cu"] = ends
     x["init"] = 0.3 * normal(len(lengths), heads, dk, dv) if init else None
     return {n: y if y is None else y.to(device) for n, y in x.items()}
+
+
+def chunked_bounds(q, k, v, g, beta, lengths, init=None, scale=1.0, chunk=64):
+    """(out, state, state bound, out bound) as of recurrence(), for the evaluation in chunks on tensor cores:
+        A_ij = beta_i w_ij (k_i . k_j),  T = (I + A)^-1,  R = beta v - beta e^G S^T k,  U = T R
+    with w = exp of a difference x of sums of log decays.  What it may leave of U, given the chunk's start state:
+      - R and T in three bf16 parts (8 bits each, all of fp32's), of whose nine products the three smallest, each at
+        most 2^-24 |T| |R|, are left out
+      - w off by 2^-22 (1 + |x|) of itself, A by that and its sums' roundings, T by |T| dA |T| and by the block
+        inverse's roundings, 3 x 64 eps |T| (I + |A|) |T|
+      - sums in fp32 of 3 d_k, or 6 x 64, terms, each rounding twice eps (the accumulator may cut off)
+    An error of the start state only shrinks (see recurrence), so a chunk adds sum_j e^(G_C - G_j) |du_j| to it, and
+    the roundings of its own sum.  Outputs take one bf16 rounding (2^-8) of the state, of P = w (q . k) and of u each."""
+    t, h, dv = v.shape
+    share, dk = h // q.shape[1], q.shape[2]
+    want = recurrence(q, k, v, g, beta, lengths, init, scale)[:2]
+    gg = (g if g.dim() == 2 else g.expand(t, h)).double()
+    err = torch.zeros(len(lengths), h, dv, dtype=torch.float64, device=v.device)
+    bound = torch.zeros(t, h, dv, dtype=torch.float64, device=v.device)
+    at = 0
+    for s, length in enumerate(lengths):
+        state = None if init is None else init[s:s + 1]
+        for b in range(at, at + length, chunk):
+            e = min(b + chunk, at + length)
+            part = [x[b:e] for x in (q, k, v)] + [gg[b:e], beta[b:e]]
+            start = torch.zeros(1, h, dk, dv, dtype=torch.float64, device=v.device) if state is None else state.double()
+            _, state, _, _ = recurrence(*part, [e - b], start, 1.0)
+            qq, kk = (x.double().repeat_interleave(share, 1).transpose(0, 1) for x in part[:2])     # [h, c, dk]
+            vv, bb = part[2].double().transpose(0, 1), part[4].double().t()                          # [h, c, dv], [h, c]
+            cum = part[3].clamp(min=-128).cumsum(0).t()                                              # [h, c]
+            low = torch.ones(e - b, e - b, dtype=torch.bool, device=v.device).tril()
+            x = torch.where(low, cum[:, :, None] - cum[:, None, :], 0.0)
+            w = torch.where(low, x.exp(), 0.0)
+            dw = w * 2.0 ** -22 * (1 + x.abs())
+            gram = kk @ kk.transpose(1, 2)
+            a = (bb[:, :, None] * w * gram).tril(-1)
+            da = (bb[:, :, None] * (dw + 2 * dk * EPS * w)).tril(-1)                                # |k| <= 1
+            eye = torch.eye(e - b, dtype=torch.float64, device=v.device)
+            inv = torch.linalg.inv(eye + a)
+            ti = inv.abs()
+            dt = ti @ da @ ti + 192 * EPS * ti @ (eye + a.abs()) @ ti
+            gam, dgam = cum.exp()[..., None], (cum.exp() * 2.0 ** -22 * (1 + cum.abs()))[..., None]
+            norm = start[0].norm(dim=-2)[:, None, :]                                                 # [h, 1, dv]
+            r = bb[..., None] * (vv - gam * (kk @ start[0]))
+            dr = bb[..., None] * ((gam * (6 * dk + 16) * EPS + dgam) * norm + 8 * EPS * vv.abs())
+            u = inv @ r
+            tr = ti @ r.abs()
+            du = dt @ r.abs() + ti @ dr + (3 + 800) * EPS * tr
+            late = (cum[:, -1:] - cum)
+            lat, dlat = late.exp()[..., None], (late.exp() * 2.0 ** -22 * (1 + late.abs()))[..., None]
+            total = cum[:, -1].exp()[:, None]
+            dtot = total * 2.0 ** -22 * (1 + cum[:, -1].abs()[:, None])
+            p, dp = w * (qq @ kk.transpose(1, 2)), dw + 2 * dk * EPS * w
+            o = (gam * ((2.0 ** -8 + 8 * dk * EPS) * (qq.abs() @ start[0].abs()) + err[s][:, None, :] + dgam * norm)
+                 + (p.abs() + dp) @ du + dp @ u.abs() + (2 * 2.0 ** -8 + 2.0 ** -14) * (p.abs() @ u.abs()))
+            bound[b:e] = abs(scale) * o.transpose(0, 1)
+            err[s] = (1 + 2.0 ** -20) * total * err[s] + ((lat * du).sum(1) + (dlat * u.abs()).sum(1)
+                                                          + 400 * EPS * (lat * u.abs()).sum(1)
+                                                          + (dtot + 4 * EPS * total) * norm[:, 0] + 4 * EPS * state[0].norm(dim=-2))
+        at += length
+    return *want, err, bound
