@@ -337,11 +337,15 @@ def linear_decode(q, k, v, g, state, *, scale: float = 1.0, out=None, out_dtype=
     return out
 
 
-def _on_device(device: torch.device):
-    """A context in which `device` is the current one: where a call's kernels are launched."""
-    import contextlib
-
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _call(name, fn, device: torch.device, *args):
+    """A C call whose kernels are launched on `device`, whichever is the current one."""
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc:
+        _lib.check(rc, name)
 
 
 def _delta_inputs(q, k, v, g, beta):
@@ -387,19 +391,22 @@ def delta_prefill(q, k, v, g, beta, cu_seqlens=None, init_state=None, *, scale: 
     shape = (n, H, dk, dv)
     if init_state is not None:
         _require(init_state, "init_state", dev, torch.float32, shape)
-    with _on_stream(dev, stream):   # new outputs come from the pool of the stream that writes them
-        out = _out(out, out_dtype or (dtype if out is None else out.dtype), dev, (T, H, dv))
+    if final_state is not None and not isinstance(final_state, bool):
+        _require(final_state, "final_state", dev, torch.float32, shape)
+    out_dtype = out_dtype or (dtype if out is None else out.dtype)
+    if stream is None:
+        out = _out(out, out_dtype, dev, (T, H, dv))
         if final_state is True:
             final_state = torch.empty(shape, device=dev, dtype=torch.float32)
-        elif final_state is False or final_state is None:
-            final_state = None
-        else:
-            _require(final_state, "final_state", dev, torch.float32, shape)
-    with _on_device(dev):
-        rc = lib.kda_delta_prefill(*head, cu, n, T, H, Hk, dk, dv, scale, _DTYPES[dtype], _DTYPES[out.dtype],
-                                   _ptr(init_state), out.data_ptr(), _ptr(final_state), _stream(dev, stream))
-    if rc:
-        _lib.check(rc, "kda_delta_prefill")
+    else:   # new outputs come from the pool of the stream that writes them
+        with _on_stream(dev, stream):
+            out = _out(out, out_dtype, dev, (T, H, dv))
+            if final_state is True:
+                final_state = torch.empty(shape, device=dev, dtype=torch.float32)
+    if final_state is False:
+        final_state = None
+    _call("kda_delta_prefill", lib.kda_delta_prefill, dev, *head, cu, n, T, H, Hk, dk, dv, scale, _DTYPES[dtype],
+          _DTYPES[out.dtype], _ptr(init_state), out.data_ptr(), _ptr(final_state), _stream(dev, stream))
     return out, final_state
 
 
@@ -411,13 +418,14 @@ def delta_decode(q, k, v, g, beta, state, *, scale: float = 1.0, out=None, out_d
     head, N, H, Hk, dk, dv = _delta_inputs(q, k, v, g, beta)
     dev, dtype = q.device, q.dtype
     _require(state, "state", dev, torch.float32, (N, H, dk, dv))
-    with _on_stream(dev, stream):
-        out = _out(out, out_dtype or (dtype if out is None else out.dtype), dev, (N, H, dv))
-    with _on_device(dev):
-        rc = lib.kda_delta_decode(*head, state.data_ptr(), out.data_ptr(), N, H, Hk, dk, dv, scale, _DTYPES[dtype],
-                                  _DTYPES[out.dtype], _stream(dev, stream))
-    if rc:
-        _lib.check(rc, "kda_delta_decode")
+    out_dtype = out_dtype or (dtype if out is None else out.dtype)
+    if stream is None:
+        out = _out(out, out_dtype, dev, (N, H, dv))
+    else:
+        with _on_stream(dev, stream):
+            out = _out(out, out_dtype, dev, (N, H, dv))
+    _call("kda_delta_decode", lib.kda_delta_decode, dev, *head, state.data_ptr(), out.data_ptr(), N, H, Hk, dk, dv, scale,
+          _DTYPES[dtype], _DTYPES[out.dtype], _stream(dev, stream))
     return out
 
 
@@ -624,11 +632,8 @@ def state_pack(dst, src, dst_idx=None, src_idx=None, *, scales=None, n: Optional
     those of dst all different.  Returns dst."""
     lib = _lib.load()
     dev, n, H, dk, dv = _pack_inputs(dst, scales, dst_idx, src, src_idx, n)
-    with _on_device(dev):
-        rc = lib.kda_state_pack(dst.data_ptr(), _ptr(scales), _FORMATS[dst.dtype], _ptr(dst_idx), dst.shape[0],
-                                src.data_ptr(), _ptr(src_idx), src.shape[0], n, H, dk, dv, _stream(dev, stream))
-    if rc:
-        _lib.check(rc, "kda_state_pack")
+    _call("kda_state_pack", lib.kda_state_pack, dev, dst.data_ptr(), _ptr(scales), _FORMATS[dst.dtype], _ptr(dst_idx),
+          dst.shape[0], src.data_ptr(), _ptr(src_idx), src.shape[0], n, H, dk, dv, _stream(dev, stream))
     return dst
 
 
@@ -637,12 +642,8 @@ def state_unpack(dst, src, dst_idx=None, src_idx=None, *, scales=None, n: Option
     back, dst fp32 and src the pool with its scales.  Returns dst."""
     lib = _lib.load()
     dev, n, H, dk, dv = _pack_inputs(src, scales, src_idx, dst, dst_idx, n)
-    with _on_device(dev):
-        rc = lib.kda_state_unpack(dst.data_ptr(), _ptr(dst_idx), dst.shape[0], src.data_ptr(), _ptr(scales),
-                                  _FORMATS[src.dtype], _ptr(src_idx), src.shape[0], n, H, dk, dv,
-                                  _stream(dev, stream))
-    if rc:
-        _lib.check(rc, "kda_state_unpack")
+    _call("kda_state_unpack", lib.kda_state_unpack, dev, dst.data_ptr(), _ptr(dst_idx), dst.shape[0], src.data_ptr(),
+          _ptr(scales), _FORMATS[src.dtype], _ptr(src_idx), src.shape[0], n, H, dk, dv, _stream(dev, stream))
     return dst
 
 

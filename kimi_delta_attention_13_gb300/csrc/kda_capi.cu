@@ -610,6 +610,10 @@ int kda_device_status(int32_t *status, void *stream)
     rc = read_and_clear_status_delta((cudaStream_t)stream, &dt);
     if (rc != KDA_OK) return rc;
     if (c == KDA_OK) c = dt;
+    int32_t dd = 0;
+    rc = read_and_clear_status_delta_decode((cudaStream_t)stream, &dd);
+    if (rc != KDA_OK) return rc;
+    if (c == KDA_OK) c = dd;
     int32_t pk = 0;
     rc = read_and_clear_status_state_pack((cudaStream_t)stream, &pk);
     if (rc != KDA_OK) return rc;

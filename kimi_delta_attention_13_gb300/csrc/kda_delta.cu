@@ -1,164 +1,278 @@
-// kda_delta.cu -- the gated delta rule with one decay per head, token by token on CUDA cores.
+// kda_delta.cu -- the gated delta rule with one decay per head on CUDA cores: fp32 inputs and head sizes that the
+// tensor-core kernel does not take.
 //
 //     S' = exp(g_t) S_(t-1),   S_t = S' + beta_t k_t (v_t - S'^T k_t)^T,   o_t = scale S_t^T q_t
 //
-// The columns of a state (value channels) do not meet, so a warp keeps all key channels of NC columns in
-// registers, R rows a lane, and needs no other warp: the sums over key channels stay inside it.  A sum of
-// NC columns over 32 lanes is folded so that every step halves the columns a lane still carries, and a lane
-// ends with one column's sum (NC = 8: 9 shuffles in place of 40).
+// A block owns 64 value columns of one (sequence, head), or 32: a thread holds 8 key channels x 2 columns (or 1) of
+// the state in registers, warp w the channels [8 w, 8 w + 8).  Eight tokens (i, j) are taken at a time (four where d_k is
+// over 128).  With w_ij = exp(g_(j+1) + .. + g_i), G_i = g_1 + .. + g_i and S the state before them,
+//     u_i = beta_i (v_i - e^(G_i) S^T k_i - sum_(j < i) w_ij (k_i . k_j) u_j)
+//     o_i = scale (e^(G_i) S^T q_i + sum_(j <= i) w_ij (q_i . k_j) u_j)
+//     S  <- e^(G_8) S + sum_j k_j (e^(G_8 - G_j) u_j)^T
+// so that the sums over all key channels, which have to cross the warps, are taken for eight tokens at once, and
+// what follows token after token is a small substitution.  Products of decays are exponentials of their own sums
+// of log decays; the state's is taken as 1 + expm1 where it is near 1: rounded to fp32 itself, a decay that stays
+// the same would be off the same way block after block (over 256 tokens of memory 1e-6 of the state).
+// Bound by latency: a block of tokens is five steps with a barrier after each (staging, scores and the products with
+// the state, sums, substitution, outputs and update), some 3700 cycles for 64 x 32 of a state and 130 of FMA a
+// scheduler for the update.  2560 tokens in two sequences, 16 heads of 64 x 128: 0.50 ms (token by token, with
+// the sums folded inside a warp, 0.88; 64 columns a block 0.55).
 #include "kda_delta.cuh"
 
 namespace kda {
 namespace delta {
 namespace {
 
-constexpr int kWarps = 4;      // warps of a block, each on its own columns
-constexpr int kAhead = 4;      // tokens whose loads are in flight
+constexpr int kRows = 8;     // key channels of a warp
 
-template <int R>
-__device__ __forceinline__ void load_row(const float *p, float (&x)[R])
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ uint2 load4(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
+__device__ __forceinline__ float4 widen(float4 x) { return x; }
+__device__ __forceinline__ float4 widen(uint2 x)
 {
-#pragma unroll
-    for (int i = 0; i < R; i += 2) {
-        const float2 f = *reinterpret_cast<const float2 *>(p + i);
-        x[i] = f.x;
-        x[i + 1] = f.y;
-    }
-}
-template <int R>
-__device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float (&x)[R])
-{
-#pragma unroll
-    for (int i = 0; i < R; i += 2) {
-        const uint32_t u = *reinterpret_cast<const uint32_t *>(p + i);
-        x[i] = __uint_as_float(u << 16);
-        x[i + 1] = __uint_as_float(u & 0xffff0000u);
-    }
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xffff0000u));
 }
 
-// Sums s[c] over the lanes, for NC columns; lane l ends with that of column l / (32 / NC).
-template <int NC>
-__device__ __forceinline__ float fold(float (&s)[NC], int lane)
-{
-    int o = 16;
-#pragma unroll
-    for (int n = NC / 2; n >= 1; n /= 2, o /= 2) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int c = 0; c < n; ++c) {
-            const float send = up ? s[c] : s[c + n];
-            const float keep = up ? s[c + n] : s[c];
-            s[c] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
-    }
-    float x = s[0];
-#pragma unroll
-    for (; o >= 1; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
+// tokens at a time
+template <int WARPS>
+constexpr int kTokens = WARPS <= 16 ? 8 : 4;
 
-template <typename T, typename TO, int R, int NC>
-__global__ void __launch_bounds__(32 * kWarps) delta_token_kernel(const Args p)
+template <typename T, typename TO, int WARPS, int CPL>
+__global__ void __launch_bounds__(32 * WARPS) delta_token_kernel(const Args p)
 {
-    constexpr int SUB = 32 / NC;   // lanes that end with the same column
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int THREADS = 32 * WARPS, DK = kRows * WARPS, TB = kTokens<WARPS>, kCols = 32 * CPL;
+    constexpr int KUNITS = TB * DK / 4, VUNITS = TB * kCols / 4;
+    constexpr int KU = (KUNITS + THREADS - 1) / THREADS;
+    constexpr int DP = DK + 4;                        // padded rows: the score threads walk several at once
+    constexpr int SUB = THREADS / (TB * TB) < 32 ? THREADS / (TB * TB) : 32;   // threads of a score
+    using Four = decltype(load4((const T *)nullptr));
+    extern __shared__ __align__(16) float parts[];    // [2][TB][WARPS][kCols]: S^T k, S^T q of a warp's channels
+    __shared__ __align__(16) float sk[TB][DP], sq[TB][DP];
+    __shared__ __align__(16) float sv[TB][kCols], su[TB][kCols];
+    struct Decays {
+        float g[TB], beta[TB], pre[TB], suf[TB];      // log decays, beta, e^G, e^(G_last - G)
+        float all, one;                               // the whole block's decay (see above)
+    };
+    __shared__ Decays sd[2];                          // this block's and the next one's
+    __shared__ float sa[TB][TB + 1], sp[TB][TB + 1];  // beta w (k . k), w (q . k)
+    constexpr int DEC = 2;                            // the warp that makes the decays, while others substitute
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / p.group, Hk = p.H / p.group;
-    const int c0 = (blockIdx.y * kWarps + warp) * NC;
-    if (c0 >= p.dv) return;
+    const int cb = blockIdx.y * kCols, col = cb + lane;
+    auto part = [&](int which, int t, int w) { return parts + ((which * TB + t) * WARPS + w) * kCols; };
     long long b, e;
     bounds(p, seq, b, e);
-    const int row = lane * R, col = c0 + lane / SUB;
-    const bool row_ok = row < p.dk, col_ok = col < p.dv;   // (d_k is a multiple of 8, so of R)
-    const long long own = (((long long)seq * p.H + h) * p.dk + row) * p.dv + c0;
-    float2 st[R][NC / 2];
+    const long long own = ((long long)seq * p.H + h) * p.dk * p.dv;
+    float st[kRows][CPL];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < kRows; ++r)
 #pragma unroll
-        for (int c = 0; c < NC; c += 4) {
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p.init && row_ok && c0 + c < p.dv) s = *reinterpret_cast<const float4 *>(p.init + own + (long long)r * p.dv + c);
-            st[r][c / 2] = make_float2(s.x, s.y);
-            st[r][c / 2 + 1] = make_float2(s.z, s.w);
+        for (int c = 0; c < CPL; ++c) {
+            const int i = warp * kRows + r;
+            st[r][c] = p.init && col + 32 * c < p.dv && i < p.dk ? p.init[own + (long long)i * p.dv + col + 32 * c] : 0.f;
         }
-    const T *q = static_cast<const T *>(p.q) + hk * p.dk + row, *k = static_cast<const T *>(p.k) + hk * p.dk + row;
-    const T *v = static_cast<const T *>(p.v) + (long long)h * p.dv + col;
-    const long long qk_step = (long long)Hk * p.dk, v_step = (long long)p.H * p.dv;
-    float nk[kAhead][R], nq[kAhead][R], nv[kAhead], ng[kAhead], nb[kAhead];
-    auto fetch = [&](long long t, int i) {
+    const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
+    Four nk[KU], nq[KU], nv;
+    float ng = 0.f, nb = 0.f;
+    auto fetch = [&](long long tb) {
+        const Four zero = {};
 #pragma unroll
-        for (int r = 0; r < R; ++r) nk[i][r] = nq[i][r] = 0.f;
-        nv[i] = ng[i] = nb[i] = 0.f;
-        if (t < e) {
-            if (row_ok) {
-                load_row<R>(k + t * qk_step, nk[i]);
-                load_row<R>(q + t * qk_step, nq[i]);
-            }
-            if (col_ok) nv[i] = to_f32(v[t * v_step]);
-            ng[i] = p.g[p.g_per_token ? t * p.H + h : h];
-            nb[i] = p.beta[t * p.H + h];
+        for (int u = 0; u < KU; ++u) {
+            const int x = tid + u * THREADS, t = x / (DK / 4), i = x % (DK / 4) * 4;
+            const bool ok = x < KUNITS && tb + t < e && i < p.dk;
+            nk[u] = ok ? load4(k + ((tb + t) * Hk + hk) * p.dk + i) : zero;
+            nq[u] = ok ? load4(q + ((tb + t) * Hk + hk) * p.dk + i) : zero;
+        }
+        {
+            const int t = tid / (kCols / 4), c = cb + tid % (kCols / 4) * 4;
+            nv = tid < VUNITS && tb + t < e && c < p.dv ? load4(v + ((tb + t) * p.H + h) * p.dv + c) : zero;
+        }
+        if (warp == DEC && lane < TB) {   // (tokens past the end neither decay nor write)
+            const bool ok = tb + lane < e;
+            ng = ok ? p.g[p.g_per_token ? (tb + lane) * p.H + h : h] : 0.f;
+            nb = ok ? p.beta[(tb + lane) * p.H + h] : 0.f;
         }
     };
+    auto decays = [&](Decays &to) {   // (lanes from TB on hold 0, the sums that reach past the block stay in it)
+        float after = ng, before = ng;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(b + i, i);
-    for (long long t0 = b; t0 < e; t0 += kAhead) {
+        for (int o = 1; o < TB; o <<= 1) {
+            after += __shfl_down_sync(0xffffffffu, after, o);
+            const float x = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += x;
+        }
+        const float rest = __shfl_down_sync(0xffffffffu, after, 1);
+        if (lane < TB) {
+            to.g[lane] = ng;
+            to.beta[lane] = nb;
+            to.pre[lane] = expf(before);
+            to.suf[lane] = expf(rest);   // (of the last: of nothing)
+        }
+        if (lane == 0) {
+            const bool near = after > -0.25f;
+            to.all = near ? expm1f(after) : expf(after);
+            to.one = near ? 1.f : 0.f;
+        }
+    };
+    int cur = 0;
+    if (b < e) {
+        fetch(b);
+        if (warp == DEC) decays(sd[0]);
+    }
+    for (long long tb = b; tb < e; tb += TB, cur ^= 1) {
+        const int n = (int)min((long long)TB, e - tb);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const long long t = t0 + i;
-            if (t >= e) break;
-            const float a = expf(ng[i]);
-            float2 acc[NC / 2] = {};
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int c = 0; c < NC / 2; ++c) acc[c] = fma2(st[r][c], make_float2(nk[i][r], nk[i][r]), acc[c]);
-            float s[NC];
-#pragma unroll
-            for (int c = 0; c < NC / 2; ++c) {
-                s[2 * c] = acc[c].x;
-                s[2 * c + 1] = acc[c].y;
+        for (int u = 0; u < KU; ++u) {
+            const int x = tid + u * THREADS;
+            if (x < KUNITS) {
+                *reinterpret_cast<float4 *>(&sk[x / (DK / 4)][x % (DK / 4) * 4]) = widen(nk[u]);
+                *reinterpret_cast<float4 *>(&sq[x / (DK / 4)][x % (DK / 4) * 4]) = widen(nq[u]);
             }
-            const float u = nb[i] * fmaf(-a, fold<NC>(s, lane), nv[i]);
-            float2 o[NC / 2] = {};
+        }
+        if (tid < VUNITS) *reinterpret_cast<float4 *>(&sv[0][0] + 4 * tid) = widen(nv);
+        const Decays &d = sd[cur];
+        __syncthreads();
+        if (tb + TB < e) fetch(tb + TB);
+        if (tid < TB * TB * SUB) {   // scores
+            const int i = tid / SUB / TB, j = tid / SUB % TB;
+            float kk = 0.f, qk = 0.f;
+#pragma unroll 4
+            for (int x = tid % SUB * 4; x < DK; x += 4 * SUB) {
+                const float4 a = *reinterpret_cast<const float4 *>(&sk[j][x]);
+                const float4 c = *reinterpret_cast<const float4 *>(&sk[i][x]);
+                const float4 f = *reinterpret_cast<const float4 *>(&sq[i][x]);
+                kk += a.x * c.x + a.y * c.y + a.z * c.z + a.w * c.w;
+                qk += a.x * f.x + a.y * f.y + a.z * f.z + a.w * f.w;
+            }
 #pragma unroll
-            for (int c = 0; c < NC / 2; ++c) {
-                const float2 uc = make_float2(__shfl_sync(0xffffffffu, u, 2 * c * SUB), __shfl_sync(0xffffffffu, u, (2 * c + 1) * SUB));
+            for (int o = SUB / 2; o > 0; o >>= 1) {
+                kk += __shfl_xor_sync(0xffffffffu, kk, o);
+                qk += __shfl_xor_sync(0xffffffffu, qk, o);
+            }
+            float w = 0.f;
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    st[r][c] = fma2(make_float2(nk[i][r], nk[i][r]), uc, mul2(st[r][c], make_float2(a, a)));
-                    o[c] = fma2(st[r][c], make_float2(nq[i][r], nq[i][r]), o[c]);
+            for (int l = 1; l < TB; ++l) w += l > j && l <= i ? d.g[l] : 0.f;
+            w = expf(w);
+            if (tid % SUB == 0) {
+                sa[i][j] = d.beta[i] * w * kk;
+                sp[i][j] = w * qk;
+            }
+        }
+#pragma unroll 4
+        for (int t = 0; t < TB; ++t) {   // S^T k, S^T q over the warp's channels
+            float ak[CPL] = {}, aq[CPL] = {};
+#pragma unroll
+            for (int r = 0; r < kRows; r += 4) {
+                const float4 kr = *reinterpret_cast<const float4 *>(&sk[t][warp * kRows + r]);
+                const float4 qr = *reinterpret_cast<const float4 *>(&sq[t][warp * kRows + r]);
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    ak[c] = fmaf(st[r + 3][c], kr.w, fmaf(st[r + 2][c], kr.z, fmaf(st[r + 1][c], kr.y, fmaf(st[r][c], kr.x, ak[c]))));
+                    aq[c] = fmaf(st[r + 3][c], qr.w, fmaf(st[r + 2][c], qr.z, fmaf(st[r + 1][c], qr.y, fmaf(st[r][c], qr.x, aq[c]))));
                 }
             }
 #pragma unroll
-            for (int c = 0; c < NC / 2; ++c) {
-                s[2 * c] = o[c].x;
-                s[2 * c + 1] = o[c].y;
+            for (int c = 0; c < CPL; ++c) {
+                part(0, t, warp)[lane + 32 * c] = ak[c];
+                part(1, t, warp)[lane + 32 * c] = aq[c];
             }
-            const float sum = fold<NC>(s, lane);
-            if (lane % SUB == 0 && col_ok)
-                store_as(static_cast<TO *>(p.out) + (t * p.H + h) * p.dv + col, sum * p.scale);
-            fetch(t + kAhead, i);
         }
-    }
-    if (p.final_state && row_ok) {
+        __syncthreads();
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int x0 = 0; x0 < 2 * TB * kCols; x0 += THREADS) {   // over all of them: R, and what outputs take from S
+            const int x = x0 + tid, t = x / kCols % TB, c = x % kCols, which = x / (TB * kCols);
+            if (x >= 2 * TB * kCols) break;
+            float *from = part(which, t, 0) + c, sum = 0.f;
 #pragma unroll
-            for (int c = 0; c < NC; c += 4)
-                if (c0 + c < p.dv)
-                    *reinterpret_cast<float4 *>(p.final_state + own + (long long)r * p.dv + c) =
-                        make_float4(st[r][c / 2].x, st[r][c / 2].y, st[r][c / 2 + 1].x, st[r][c / 2 + 1].y);
+            for (int w = 0; w < WARPS; ++w) sum += from[w * kCols];
+            from[0] = which ? d.pre[t] * sum : d.beta[t] * fmaf(-d.pre[t], sum, sv[t][c]);
+        }
+        __syncthreads();
+        if (tid < kCols) {   // a column's substitution
+            float u[TB];
+#pragma unroll
+            for (int i = 0; i < TB; ++i) u[i] = part(0, i, 0)[tid];
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+#pragma unroll
+                for (int i = j + 1; i < TB; ++i) u[i] = fmaf(-sa[i][j], u[j], u[i]);
+#pragma unroll
+            for (int i = 0; i < TB; ++i) su[i][tid] = u[i];
+        }
+        if (warp == DEC && tb + TB < e) decays(sd[cur ^ 1]);
+        __syncthreads();
+        for (int x = tid; x < n * kCols; x += THREADS) {
+            const int i = x / kCols, c = x % kCols;
+            float o = part(1, i, 0)[c];
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+                if (j <= i) o = fmaf(sp[i][j], su[j][c], o);
+            if (cb + c < p.dv) store_as(static_cast<TO *>(p.out) + ((tb + i) * p.H + h) * p.dv + cb + c, o * p.scale);
+        }
+        const float all = d.all, one = d.one;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) st[r][c] = fmaf(st[r][c], all, st[r][c] * one);
+#pragma unroll 4
+        for (int t = 0; t < TB; ++t) {
+            const float f = d.suf[t];
+            float u[CPL];
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) u[c] = f * su[t][lane + 32 * c];
+#pragma unroll
+            for (int r = 0; r < kRows; r += 4) {
+                const float4 kr = *reinterpret_cast<const float4 *>(&sk[t][warp * kRows + r]);
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    st[r][c] = fmaf(kr.x, u[c], st[r][c]);
+                    st[r + 1][c] = fmaf(kr.y, u[c], st[r + 1][c]);
+                    st[r + 2][c] = fmaf(kr.z, u[c], st[r + 2][c]);
+                    st[r + 3][c] = fmaf(kr.w, u[c], st[r + 3][c]);
+                }
+            }
+        }
+        __syncthreads();
     }
+    if (p.final_state) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                const int i = warp * kRows + r;
+                if (i < p.dk && col + 32 * c < p.dv) p.final_state[own + (long long)i * p.dv + col + 32 * c] = st[r][c];
+            }
+    }
+}
+
+template <typename T, typename TO, int WARPS, int CPL>
+int launch_cols(const Args &p, cudaStream_t stream)
+{
+    constexpr int bytes = 2 * kTokens<WARPS> * WARPS * 32 * CPL * 4;
+    // a function attribute belongs to the current device: set it on every launch
+    if (cudaFuncSetAttribute(delta_token_kernel<T, TO, WARPS, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+        return KDA_ERR_CUDA;
+    const dim3 grid((unsigned)(p.n_seqs * p.H), (unsigned)ceil_div(p.dv, 32 * CPL));
+    delta_token_kernel<T, TO, WARPS, CPL><<<grid, 32 * WARPS, bytes, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <typename T, typename TO, int WARPS>
+int launch_warps(const Args &p, cudaStream_t stream)
+{
+    // 32 columns a block where 64 would leave SMs idle
+    if ((long long)p.n_seqs * p.H * ceil_div(p.dv, 64) < 152) return launch_cols<T, TO, WARPS, 1>(p, stream);
+    return launch_cols<T, TO, WARPS, 2>(p, stream);
 }
 
 template <typename T, typename TO>
 int launch(const Args &p, cudaStream_t stream)
 {
-    constexpr int NC = 8;
-    const dim3 grid((unsigned)(p.n_seqs * p.H), (unsigned)ceil_div(p.dv, NC * kWarps));
-    if (p.dk <= 64) delta_token_kernel<T, TO, 2, NC><<<grid, 32 * kWarps, 0, stream>>>(p);
-    else if (p.dk <= 128) delta_token_kernel<T, TO, 4, NC><<<grid, 32 * kWarps, 0, stream>>>(p);
-    else delta_token_kernel<T, TO, 8, NC><<<grid, 32 * kWarps, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    if (p.dk <= 64) return launch_warps<T, TO, 8>(p, stream);
+    if (p.dk <= 128) return launch_warps<T, TO, 16>(p, stream);
+    return launch_warps<T, TO, 32>(p, stream);
 }
 
 }  // namespace

@@ -64,6 +64,7 @@ int read_and_clear_status_cp(cudaStream_t s, int32_t *status);
 int read_and_clear_status_linear(cudaStream_t s, int32_t *status);
 int read_and_clear_status_state_pack(cudaStream_t s, int32_t *status);
 int read_and_clear_status_delta(cudaStream_t s, int32_t *status);
+int read_and_clear_status_delta_decode(cudaStream_t s, int32_t *status);
 // Launch the one-CTA probe whose bounded device wait expires after `cycles` SM cycles.
 int launch_wait_timeout_probe(long long cycles, cudaStream_t stream);
 // The same with the waits of the linear-attention and of the gated-delta-rule prefill.

@@ -39,13 +39,38 @@ __device__ __forceinline__ bool slots(const Move &m, int64_t i, int64_t &held, i
     return false;
 }
 
-__device__ __forceinline__ uint32_t code8(float x, float s, float inv)
+constexpr float kMagic = 12582912.f;  // 1.5 x 2^23: a sum with it is rounded to a whole number, in its low bits
+
+// The codes of four values, as bytes.  A code is that of the exact quotient x / s, ties to even: what x / s rounds
+// to may be the wrong one of two neighbours, which the exact remainder x - code s shows.
+__device__ __forceinline__ uint32_t codes(float4 f, float s, float inv)
 {
-    float r = rintf(inv > 0.f ? x * inv : x / s);
-    const float left = fmaf(-r, s, x);               // exact: at most about s / 2, in units of the smaller ulp
-    const float twice = 2.f * fabsf(left);
-    if (twice > s || (twice == s && ((int)r & 1))) r += copysignf(1.f, left);
-    return (uint32_t)(int)fminf(fmaxf(r, -127.f), 127.f) & 0xffu;
+    const float x[4] = {f.x, f.y, f.z, f.w};
+    float m[4], far = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        m[e] = fmaf(x[e], inv, kMagic);
+        far = fmaxf(far, fabsf(fmaf(kMagic - m[e], s, x[e])));
+    }
+    if (!(2.f * far < s) || inv == 0.f) {   // a remainder of half a step or more, or no reciprocal
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float r = inv > 0.f ? m[e] - kMagic : rintf(x[e] / s);
+            const float left = fmaf(-r, s, x[e]), twice = 2.f * fabsf(left);
+            if (twice > s || (twice == s && ((int)r & 1))) r += copysignf(1.f, left);
+            m[e] = fminf(fmaxf(r, -127.f), 127.f) + kMagic;
+        }
+    }
+    return __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040),
+                       __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040), 0x5410);
+}
+
+// max / 127 correctly rounded: a quotient by the rounded reciprocal, corrected once by its remainder (Markstein)
+__device__ __forceinline__ float scale_of(float top)
+{
+    if (top < 1e-30f) return __fdiv_rn(top, 127.f);   // (its remainder would underflow)
+    const float q = top * (1.f / 127.f);
+    return fmaf(fmaf(-q, 127.f, top), 1.f / 127.f, q);
 }
 
 // LANES lanes a row of at most 4 LANES V columns
@@ -79,11 +104,15 @@ __global__ void __launch_bounds__(kThreads) state_pack8_kernel(const Move m)
                 for (int c = 0; c < V; ++c)
                     top = max(top, max(max(__float_as_uint(x[u][c].x) & 0x7fffffffu, __float_as_uint(x[u][c].y) & 0x7fffffffu),
                                        max(__float_as_uint(x[u][c].z) & 0x7fffffffu, __float_as_uint(x[u][c].w) & 0x7fffffffu)));
+                if constexpr (LANES == 32) {
+                    top = __reduce_max_sync(0xffffffffu, top);
+                } else {
 #pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float s = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(top), 127.f);
+                    for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                }
+                const float s = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : scale_of(__uint_as_float(top));
                 // (the reciprocal of a scale that is all but 0 would overflow)
-                const float inv = s >= 1e-30f ? 1.f / s : 0.f;
+                const float inv = s >= 1e-30f ? __frcp_rn(s) : 0.f;
                 const int64_t row = r0 + u * SIDE + side;
                 if (row >= m.rows) continue;
                 if (lane == 0) scales[row] = s;
@@ -94,8 +123,7 @@ __global__ void __launch_bounds__(kThreads) state_pack8_kernel(const Move m)
                     if (col >= m.dv) continue;
                     const float4 f = x[u][c];
                     uint32_t w = 0;
-                    if (any)
-                        w = code8(f.x, s, inv) | code8(f.y, s, inv) << 8 | code8(f.z, s, inv) << 16 | code8(f.w, s, inv) << 24;
+                    if (any) w = codes(f, s, inv);
                     *reinterpret_cast<uint32_t *>(to + row * m.dv + col) = w;
                 }
             }

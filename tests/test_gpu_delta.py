@@ -57,12 +57,43 @@ def test_decode(dtype, out_dtype, shape, n):
     check(out, state, x, [1] * n, dk ** -0.5)
 
 
-def test_decode_many_states():
-    """Past the sizes at which blocks take all columns of a state."""
-    x = inputs([1] * 40, 96, 48, 128, 128, BF16, seed=3, init=True)
+@pytest.mark.parametrize("n,shape", [(40, (96, 48, 128, 128)), (130, (4, 2, 120, 104)), (260, (2, 2, 256, 64)),
+                                     (128, (4, 1, 64, 256)), (171, (3, 3, 72, 120)), (520, (1, 1, 128, 72))])
+def test_decode_many_states(n, shape):
+    """Sizes at which states go through shared memory whole."""
+    h, hk, dk, dv = shape
+    x = inputs([1] * n, h, hk, dk, dv, BF16, seed=3, init=True)
     state = x["init"].clone()
     out = kda.delta_decode(x["q"], x["k"], x["v"], x["g"], x["beta"], state, out_dtype=F32)
-    check(out, state, x, [1] * 40, 1.0)
+    check(out, state, x, [1] * n, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_decode_of_a_constant_slow_decay(dtype):
+    """2000 tokens of one decay near 1: its rounding must not add up."""
+    x = inputs([1], 2, 2, 64, 64, F32, seed=21, init=True, per_token=False)
+    x["g"].fill_(-1 / 300)
+    x["beta"].fill_(0.0)                 # nothing is written, all that is left is the decay
+    state = x["init"].clone()
+    args = [x[n].to(dtype) if n in "qkv" else x[n] for n in ("q", "k", "v", "g", "beta")]
+    for _ in range(2000):
+        kda.delta_decode(*args, state)
+    want = x["init"].double() * torch.exp(2000 * x["g"].double())[0]
+    # a step rounds once, half an eps at most, as often up as down (5 deviations of the sum), and its decay is off by
+    # eps / 300 or so
+    off = ((state.double() - want) / want).abs().max()
+    assert float(off) <= 2.0 ** -24 * (5 * 2000 ** 0.5 + 2 * 2000 / 300)
+
+
+def test_prefill_of_a_constant_slow_decay():
+    x = inputs([2000], 2, 2, 64, 64, F32, seed=22, init=True, per_token=False)
+    x["g"].fill_(-1 / 300)
+    x["beta"].fill_(0.0)
+    _, state = kda.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], None, x["init"])
+    want = x["init"].double() * torch.exp(2000 * x["g"].double())[0]
+    # 250 blocks of eight tokens round once each, and their decays are off by 2 eps of the block's sum (8 / 300)
+    off = ((state.double() - want) / want).abs().max()
+    assert float(off) <= 2.0 ** -24 * (5 * 250 ** 0.5 + 4 * 2000 / 300)
 
 
 @pytest.mark.parametrize("call", ["prefill", "decode"])
