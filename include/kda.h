@@ -424,7 +424,7 @@ int kda_linear_decode(const void *q, const void *k, const void *v, const float *
  * is fp32 throughout, rounded once at the end.
  * The tensor-core kernel's waits are bounded (2e9 SM cycles, about 1 s): one that gave up shows as
  * KDA_ERR_DEVICE_TIMEOUT in kda_device_status.  A NaN or infinity in an input of a sequence leaves the other
- * sequences as they are; within its own it may also reach outputs up to 15 tokens before it.
+ * sequences as they are; within its own it may also reach outputs up to 63 tokens before it.
  * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_MISALIGNED, KDA_ERR_CUDA.
  */
 int kda_delta_prefill(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,

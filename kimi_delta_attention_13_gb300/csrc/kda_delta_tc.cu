@@ -27,7 +27,7 @@ using namespace ptx;
 constexpr int C = 64;                           // tokens of a chunk
 constexpr int kThreads = 6 * 128;
 // Registers a thread of each warpgroup, 80 at launch.
-constexpr int kRegsChain = 128, kRegsOut = 56, kRegsPrep = 64, kRegsIssue = 40;
+constexpr int kRegsChain = 128, kRegsOut = 48, kRegsPrep = 72, kRegsIssue = 32;
 static_assert(2 * kRegsChain + kRegsOut + 2 * kRegsPrep + kRegsIssue <= 6 * 80, "registers of the block");
 template <int N>
 __device__ __forceinline__ void set_regs()
@@ -46,14 +46,11 @@ constexpr int STAGES = 3;                       // chunks of k and q
 constexpr uint32_t REGION = 128 * 128;          // 64 channels of 64 k rows, then of 64 q rows (odd chunks: q first)
 constexpr uint32_t TILE = 64 * 128;             // 64 x 64 bf16
 constexpr int PITCH = 68;                       // of the solver's fp32 matrices
-// Shared memory: k and q, v, three parts of T (twice; A comes to stand there first), P (three times), T in fp32
-// (twice)
+// Shared memory: k and q, v, three parts of T (twice), P (three times), A and then T in fp32 (twice)
 constexpr int P_TILES = 3;
 constexpr uint32_t SQUARE = C * PITCH * 4;
 constexpr uint32_t SM_KQ = 0, SM_V = SM_KQ + STAGES * 2 * REGION, SM_T = SM_V + 2 * TILE, SM_P = SM_T + 6 * TILE,
                    SM_TF = SM_P + P_TILES * TILE, SM_SHARED = SM_TF + 2 * SQUARE;
-static_assert(SQUARE <= 3 * TILE, "A in the place of T's parts");
-
 // Tensor memory, lanes = value channels (Gram: tokens).  The state's parts lie 16 key channels at a time, hi and
 // mid side by side, where the update that they make room for comes (a thread overwrites only what it has
 // read); R over X (its lo over the state's), U's parts over U and over R.
@@ -77,7 +74,7 @@ enum Bar {
     B_KQ_FULL, B_K_READY = B_KQ_FULL + STAGES, B_K_FREE = B_K_READY + STAGES, B_V_FULL = B_K_FREE + STAGES, B_V_READY, B_V_FREE,
     B_DEC_READY, B_GRAM_DONE = B_DEC_READY + DECS, B_GRAM_FREE = B_GRAM_DONE + 2, B_P_READY, B_P_FREE = B_P_READY + P_TILES,
     B_T_READY = B_P_FREE + P_TILES, B_T_FREE = B_T_READY + 2, B_S_READY = B_T_FREE + 2, B_X_DONE = B_S_READY + 4, B_R_READY,
-    B_U_DONE = B_R_READY + 2, B_UP_READY, B_KU_DONE = B_UP_READY + 2, B_O1_DONE, B_O1_READY, B_O2_DONE, B_O2_FREE,
+    B_U_DONE = B_R_READY + 2, B_UP_READY, B_KU_DONE = B_UP_READY + 2, B_O1_DONE = B_KU_DONE + 2, B_O1_READY, B_O2_DONE, B_O2_FREE,
     B_DRAIN, B_COUNT = B_DRAIN + 2
 };
 
@@ -91,7 +88,9 @@ struct Shared {
 constexpr uint32_t SM_BYTES = SM_SHARED + sizeof(Shared);
 static_assert(SM_BYTES <= 232448, "shared memory per block");
 
-// Products.  Issuing is on the chain (some 80 a chunk), so all but an operand's place in shared memory is known
+// Products.  Two of them are in order only where they accumulate into the same place in the same shape; what else
+// one has to find read or written by another waits for its completion.  (So T's and P's zeros above the diagonal are
+// multiplied too: products of fewer rows would be another shape.)  Issuing is on the chain, so all but an operand's place in shared memory is known
 // when the kernel is compiled: tensor memory is taken whole, so that it starts at 0, and only the lower half
 // of a descriptor varies.
 constexpr uint32_t NEG_A = 1u << 13, NEG_B = 1u << 14;          // of an instruction descriptor
@@ -149,18 +148,18 @@ __device__ __forceinline__ void rest(uint32_t h, float2 &x)   // x = h - x
         : "+f"(x.x), "+f"(x.y) : "r"(h));
 }
 
-// stage by stage, since a pair's own operations wait for one another
+// stage by stage, since a pair's own operations wait for one another; `two`: the hi parts, then the mid parts
 template <int N>
-__device__ __forceinline__ void split3(float2 (&y)[N], uint32_t (&hi)[N], uint32_t (&mid)[N], uint32_t (&lo)[N])
+__device__ __forceinline__ void split3(float2 (&y)[N], uint32_t (&two)[2 * N], uint32_t (&lo)[N])
 {
 #pragma unroll
-    for (int e = 0; e < N; ++e) hi[e] = pack_bf16x2(y[e].x, y[e].y);
+    for (int e = 0; e < N; ++e) two[e] = pack_bf16x2(y[e].x, y[e].y);
 #pragma unroll
-    for (int e = 0; e < N; ++e) rest(hi[e], y[e]);
+    for (int e = 0; e < N; ++e) rest(two[e], y[e]);
 #pragma unroll
-    for (int e = 0; e < N; ++e) mid[e] = pack_bf16x2(y[e].x, y[e].y);
+    for (int e = 0; e < N; ++e) two[N + e] = pack_bf16x2(y[e].x, y[e].y);
 #pragma unroll
-    for (int e = 0; e < N; ++e) rest(mid[e], y[e]);
+    for (int e = 0; e < N; ++e) rest(two[N + e], y[e]);
 #pragma unroll
     for (int e = 0; e < N; ++e) lo[e] = pack_bf16x2(y[e].x, y[e].y);
 }
@@ -200,18 +199,28 @@ __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CU
         }
         __syncwarp();
     };
+    auto ahead = [&](const CUtensorMap *m, int head, int boxes, int c) {   // into L2
+        if (c < nch && elect_one())
+            for (int r = 0; r < boxes; ++r) tma_prefetch_l2_3d(m, 64 * r, head, (int)(t0 + (long long)c * C));
+        __syncwarp();
+    };
     int nk = 0, nv = 0;   // tiles issued
     for (; nk < nch && nk < STAGES; ++nk) kq(nk);
+    ahead(mk, hk, regions, nk);
+    ahead(mq, hk, regions, nk);
     bool ok = true;
     for (; ok && nv < nch; ++nv) {
         if (nv > 0 && !(ok = wait_warp(sh, B_V_FREE, nv - 1))) break;
         value(nv);
+        ahead(mv, h, 2, nv + 1);
         if (nv > 0 && nk < nch) {   // the stage was chunk nv - 1's
             if (!(ok = wait_warp(sh, B_K_FREE + nk % STAGES, nk / STAGES - 1))) {
                 ++nv;
                 break;
             }
             kq(nk++);
+            ahead(mk, hk, regions, nk);   // (a tile's work begins with its load and has to end in two chunks' time)
+            ahead(mq, hk, regions, nk);
         }
     }
     if (!ok) {   // no copy in flight when the CTA leaves
@@ -273,18 +282,42 @@ __device__ void gram_mma_role(uint32_t sb, Shared *sh, int nch)
     if (!ok) drain(sh, 0);
 }
 
+// Key channels come in steps of 16.  A thread of the chain has GROUPS of them, half of each half of the channels, since
+// the update comes by halves: group g of the first four warps (w = 0) or the others is step
+template <int GROUPS>
+__host__ __device__ constexpr int step_of(int w, int g) { return GROUPS * (g / (GROUPS / 2)) + GROUPS / 2 * w + g % (GROUPS / 2); }
+
 template <int REGIONS>
 __device__ void chain_mma_role(uint32_t sb, Shared *sh, int nch)
 {
     constexpr int STEPS = 4 * REGIONS, GROUPS = STEPS / 2;   // 16 key channels each; those of four warps
-    constexpr uint32_t I64 = idesc_bf16(128, 64, 0, 0), I_KU = idesc_bf16(128, 16 * STEPS, 0, 1);
-    bool ok = true;
-    for (int c = 0; c < nch; ++c) {
+    constexpr uint32_t I64 = idesc_bf16(128, 64, 0, 0), I_KU = idesc_bf16(128, 64, 0, 1);
+    // U = T V, where nothing waits for the pipe: while the state before is worked on
+    auto values = [&](int c) {
+        const int half = c & 1;
+        const uint32_t t = desc_lo(sb + SM_T + half * 3 * TILE), v = desc_lo(sb + SM_V, TILE);
+        if (!wait_warp(sh, B_T_READY + half, c >> 1) || !wait_warp(sh, B_V_FULL, c) || !wait_warp(sh, B_V_READY, c)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+            each<4>([&](auto s_) {
+                constexpr int s = decltype(s_)::value;
+                constexpr uint32_t I = idesc_bf16(128, 64, 1, 0);
+                const uint32_t a = v + (s * 2048 >> 4), hi = t + (s * 32 >> 4);
+                mma_smem<TM_U, I, (s > 0)>(a, hi + 2 * (TILE >> 4));
+                mma_smem<TM_U, I | NEG_B, true>(a, hi + (TILE >> 4));
+                mma_smem<TM_U, I, true>(a, hi);
+            });
+            mma_commit(&sh->bars[B_V_FREE]);
+        }
+        __syncwarp();
+        return true;
+    };
+    bool ok = nch == 0 || values(0);
+    for (int c = 0; ok && c < nch; ++c) {
         const int st = c % STAGES, half = c & 1;
         const uint32_t tile = sb + SM_KQ + st * 2 * REGION;
-        const uint32_t k = desc_lo(tile + half * TILE), kn = desc_lo(tile + half * TILE, REGION),
-                       q = desc_lo(tile + (half ^ 1) * TILE), t = desc_lo(sb + SM_T + half * 3 * TILE),
-                       p = desc_lo(sb + SM_P + c % P_TILES * TILE), v = desc_lo(sb + SM_V, TILE);
+        const uint32_t k = desc_lo(tile + half * TILE), q = desc_lo(tile + (half ^ 1) * TILE), t = desc_lo(sb + SM_T + half * 3 * TILE),
+                       p = desc_lo(sb + SM_P + c % P_TILES * TILE);
         // X = S^T K^T, as the state's parts come (over what the last chunk's outputs read)
         ok = wait_warp(sh, B_K_READY + st, c / STAGES) && (c == 0 || wait_warp(sh, B_O2_DONE, c - 1));
         each<GROUPS>([&](auto g_) {
@@ -293,7 +326,7 @@ __device__ void chain_mma_role(uint32_t sb, Shared *sh, int nch)
             tc_fence_after();
             if (elect_one()) {
                 each<2>([&](auto w_) {
-                    constexpr int x = GROUPS * decltype(w_)::value + g;
+                    constexpr int x = step_of<GROUPS>(decltype(w_)::value, g);
                     const uint32_t b = k + (((x >> 2) * REGION + (x & 3) * 32) >> 4);
                     mma_tmem<TM_X, TM_S + 16 * x, I64, (x > 0)>(b);
                     mma_tmem<TM_X, TM_S + 16 * x + 8, I64 | NEG_A, true>(b);
@@ -303,7 +336,31 @@ __device__ void chain_mma_role(uint32_t sb, Shared *sh, int nch)
             }
             __syncwarp();
         });
-        // S^T Q^T
+        // U + T R
+        each<2>([&](auto g_) {
+            constexpr int g = decltype(g_)::value;
+            if (!ok || !(ok = wait_warp(sh, B_R_READY + g, c))) return;
+            tc_fence_after();
+            if (elect_one()) {
+                each<2>([&](auto w_) {
+                    constexpr int s = 2 * decltype(w_)::value + g;
+                    constexpr uint32_t a = TM_X + 16 * s;
+                    const uint32_t hi = t + (s * 32 >> 4), mid = hi + (TILE >> 4), lo = mid + (TILE >> 4);
+                    mma_tmem<TM_U, TM_SLO + 8 * s, I64, true>(hi);
+                    mma_tmem<TM_U, a + 8, I64, true>(mid);
+                    mma_tmem<TM_U, a, I64, true>(lo);
+                    mma_tmem<TM_U, a + 8, I64 | NEG_A, true>(hi);
+                    mma_tmem<TM_U, a, I64 | NEG_B, true>(mid);
+                    mma_tmem<TM_U, a, I64, true>(hi);
+                });
+                if (g == 1) {
+                    mma_commit(&sh->bars[B_U_DONE]);
+                    mma_commit(&sh->bars[B_T_FREE + half]);
+                }
+            }
+            __syncwarp();
+        });
+        // S^T Q^T, while U is worked on (the update writes over the state's parts)
         ok = ok && (c == 0 || wait_warp(sh, B_O2_FREE, c - 1));
         if (!ok) break;
         tc_fence_after();
@@ -317,62 +374,25 @@ __device__ void chain_mma_role(uint32_t sb, Shared *sh, int nch)
             mma_commit(&sh->bars[B_O1_DONE]);
         }
         __syncwarp();
-        // U = T V + T R: of 16 tokens j the rows i from them on
-        ok = wait_warp(sh, B_T_READY + half, c >> 1) && wait_warp(sh, B_V_FULL, c) && wait_warp(sh, B_V_READY, c);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-            each<4>([&](auto s_) {
-                constexpr int s = decltype(s_)::value;
-                constexpr uint32_t I = idesc_bf16(128, 64 - 16 * s, 1, 0), d = TM_U + 16 * s;
-                const uint32_t a = v + (s * 2048 >> 4), hi = t + (s * (2048 + 32) >> 4);
-                mma_smem<d, I, (s > 0)>(a, hi + 2 * (TILE >> 4));
-                mma_smem<d, I | NEG_B, true>(a, hi + (TILE >> 4));
-                mma_smem<d, I, true>(a, hi);
-            });
-            mma_commit(&sh->bars[B_V_FREE]);
-        }
-        __syncwarp();
-        each<2>([&](auto g_) {
-            constexpr int g = decltype(g_)::value;
-            if (!ok || !(ok = wait_warp(sh, B_R_READY + g, c))) return;
-            tc_fence_after();
-            if (elect_one()) {
-                each<2>([&](auto w_) {
-                    constexpr int s = 2 * decltype(w_)::value + g;
-                    constexpr uint32_t I = idesc_bf16(128, 64 - 16 * s, 0, 0), a = TM_X + 16 * s, d = TM_U + 16 * s;
-                    const uint32_t hi = t + (s * (2048 + 32) >> 4), mid = hi + (TILE >> 4), lo = mid + (TILE >> 4);
-                    mma_tmem<d, TM_SLO + 8 * s, I, true>(hi);
-                    mma_tmem<d, a + 8, I, true>(mid);
-                    mma_tmem<d, a, I, true>(lo);
-                    mma_tmem<d, a + 8, I | NEG_A, true>(hi);
-                    mma_tmem<d, a, I | NEG_B, true>(mid);
-                    mma_tmem<d, a, I, true>(hi);
-                });
-                if (g == 1) {
-                    mma_commit(&sh->bars[B_U_DONE]);
-                    mma_commit(&sh->bars[B_T_FREE + half]);
-                }
-            }
-            __syncwarp();
-        });
         // the update, sum over j of k_j u~_j^T
+        ok = wait_warp(sh, B_O1_DONE, c);
         each<2>([&](auto g_) {
             constexpr int g = decltype(g_)::value;
             if (!ok || !(ok = wait_warp(sh, B_UP_READY + g, c))) return;
             tc_fence_after();
             if (elect_one()) {
-                each<2>([&](auto w_) {
-                    constexpr int s = 2 * decltype(w_)::value + g;
-                    const uint32_t b = kn + (s * 2048 >> 4);
-                    mma_tmem<TM_DST, TM_U + 16 * s, I_KU, (s > 0)>(b);
-                    mma_tmem<TM_DST, TM_U + 16 * s + 8, I_KU | NEG_A, true>(b);
-                    mma_tmem<TM_DST, TM_UX + 16 * s, I_KU, true>(b);
+                each<REGIONS>([&](auto r_) {   // 64 key channels at a time, so that the state's work begins with the first
+                    constexpr int r = decltype(r_)::value;
+                    each<2>([&](auto w_) {
+                        constexpr int s = 2 * decltype(w_)::value + g;
+                        const uint32_t b = k + ((r * REGION + s * 2048) >> 4);
+                        mma_tmem<TM_DST + 64 * r, TM_U + 16 * s, I_KU, (s > 0)>(b);
+                        mma_tmem<TM_DST + 64 * r, TM_U + 16 * s + 8, I_KU | NEG_A, true>(b);
+                        mma_tmem<TM_DST + 64 * r, TM_UX + 16 * s, I_KU, true>(b);
+                    });
+                    if (g == 1) mma_commit(&sh->bars[B_KU_DONE + r]);
                 });
-                if (g == 1) {
-                    mma_commit(&sh->bars[B_KU_DONE]);
-                    mma_commit(&sh->bars[B_K_FREE + st]);
-                }
+                if (g == 1) mma_commit(&sh->bars[B_K_FREE + st]);
             }
             __syncwarp();
         });
@@ -383,38 +403,38 @@ __device__ void chain_mma_role(uint32_t sb, Shared *sh, int nch)
         if (elect_one()) {
             each<4>([&](auto s_) {
                 constexpr int s = decltype(s_)::value;
-                constexpr uint32_t I = idesc_bf16(128, 64 - 16 * s, 0, 0);
-                const uint32_t b = p + (s * (2048 + 32) >> 4);
-                mma_tmem<TM_O + 16 * s, TM_X + 8 * s, I | NEG_A, true>(b);
-                mma_tmem<TM_O + 16 * s, TM_UX + 16 * s + 8, I, true>(b);
+                const uint32_t b = p + (s * 32 >> 4);
+                mma_tmem<TM_O, TM_X + 8 * s, I64 | NEG_A, true>(b);
+                mma_tmem<TM_O, TM_UX + 16 * s + 8, I64, true>(b);
             });
             mma_commit(&sh->bars[B_O2_DONE]);
             mma_commit(&sh->bars[B_P_FREE + c % P_TILES]);
         }
         __syncwarp();
+        if (c + 1 < nch) ok = wait_warp(sh, B_KU_DONE + REGIONS - 1, c) && values(c + 1);   // (the update reads where U comes)
     }
     if (!ok) drain(sh, 1);
 }
 
 // ---------------------------------------------------------------------------------------------
-// warps 0-7, the chain: thread = value channel 32 (warp % 4) + lane; warps 0-3 tokens 0-31 and the lower half of
-// the key channels, warps 4-7 the others
+// warps 0-7, the chain: thread = value channel 32 (warp % 4) + lane; warps 0-3 tokens 0-31 and half of the key
+// channels (see step_of), warps 4-7 the others
 
 template <int REGIONS>
 __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, int h, long long len, int nch)
 {
-    constexpr int GROUPS = 2 * REGIONS, N = 16 * GROUPS;   // key channels of a thread, 16 a group
+    constexpr int GROUPS = 2 * REGIONS;   // of 16 key channels
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp >> 2, ch = 32 * (warp & 3) + lane;
     const uint32_t tq = (uint32_t)(32 * (warp & 3)) << 16;
     const bool ch_ok = ch < p.dv;
-    const long long own = (((long long)seq * p.H + h) * p.dk + N * w) * p.dv + ch;
-    const int rows = p.dk - N * w;   // of these that there are, maybe <= 0
-    float2 st[N / 2];
+    const long long own = ((long long)seq * p.H + h) * p.dk * p.dv + ch;
+    float2 st[8 * GROUPS];
 #pragma unroll
-    for (int x = 0; x < N / 2; ++x) {
+    for (int x = 0; x < 8 * GROUPS; ++x) {
+        const int i = 16 * step_of<GROUPS>(w, x / 8) + x % 8 * 2;
         st[x] = make_float2(0.f, 0.f);
-        if (p.init && ch_ok && 2 * x < rows)   // (d_k is even)
-            st[x] = make_float2(p.init[own + (long long)(2 * x) * p.dv], p.init[own + (long long)(2 * x + 1) * p.dv]);
+        if (p.init && ch_ok && i < p.dk)   // (d_k is even)
+            st[x] = make_float2(p.init[own + (long long)i * p.dv], p.init[own + (long long)(i + 1) * p.dv]);
     }
     for (int c = 0;; ++c) {
         if (c < nch) {   // v's rows of other sequences: 0 x NaN must not get into the products
@@ -432,14 +452,17 @@ __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, in
         float total = 0.f;
         if (c > 0) {
             total = sh->dec[(c - 1) % DECS].total;
-            if (!wait_warp(sh, B_KU_DONE, c - 1)) return give_up(sh);
-            tc_fence_after();
         }
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
+            const int x16 = 16 * step_of<GROUPS>(w, g);
             if (c > 0) {
                 uint32_t x[16];
-                tmem_ld16(tq + TM_DST + N * w + 16 * g, x);
+                if (g % 2 == 0) {
+                    if (!wait_warp(sh, B_KU_DONE + g / 2, c - 1)) return give_up(sh);
+                    tc_fence_after();
+                }
+                tmem_ld16(tq + TM_DST + x16, x);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -448,19 +471,18 @@ __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, in
                 }
             }
             if (c == nch) continue;
-            uint32_t hi[8], mid[8], lo[8];
+            uint32_t two[16], lo[8];
             float2 y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = st[8 * g + e];
-            split3(y, hi, mid, lo);
+            split3(y, two, lo);
             if (g > 0) {   // (what was stored before has had the time)
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(sh, B_S_READY + g - 1, lane);
             }
-            tmem_st8(tq + TM_S + N * w + 16 * g, hi);
-            tmem_st8(tq + TM_S + N * w + 16 * g + 8, mid);
-            tmem_st8(tq + TM_SLO + N / 2 * w + 8 * g, lo);
+            tmem_st16(tq + TM_S + x16, two);
+            tmem_st8(tq + TM_SLO + x16 / 2, lo);
         }
         if (c == nch) break;
         tmem_wait_st();
@@ -472,7 +494,7 @@ __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, in
         tc_fence_after();
 #pragma unroll
         for (int g = 0; g < 2; ++g) {   // R = -e^G X, in three parts
-            uint32_t x[16], hi[8], mid[8], lo[8];
+            uint32_t x[16], two[16], lo[8];
             float2 y[8];
             const int t = 32 * w + 16 * g;
             tmem_ld16(tq + TM_X + t, x);
@@ -483,9 +505,8 @@ __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, in
                 y[e] = make_float2(n.x * __uint_as_float(x[2 * e]), n.y * __uint_as_float(x[2 * e + 1]));
                 y[e + 1] = make_float2(n.z * __uint_as_float(x[2 * e + 2]), n.w * __uint_as_float(x[2 * e + 3]));
             }
-            split3(y, hi, mid, lo);
-            tmem_st8(tq + TM_X + t, hi);
-            tmem_st8(tq + TM_X + t + 8, mid);
+            split3(y, two, lo);
+            tmem_st16(tq + TM_X + t, two);
             tmem_st8(tq + TM_SLO + t / 2, lo);
             tmem_wait_st();
             tc_fence_before();
@@ -495,7 +516,7 @@ __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, in
         tc_fence_after();
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {   // u~ = e^(G_C - G) u in three parts, u in two for the outputs
-            uint32_t x[16], hi[8], mid[8], lo[8];
+            uint32_t x[16], two[16], lo[8];
             float2 y[8];
             const int t = 32 * w + 16 * g;
             tmem_ld16(tq + TM_U + t, x);
@@ -506,20 +527,19 @@ __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, in
                 y[e] = make_float2(__uint_as_float(x[2 * e]) * f.x, __uint_as_float(x[2 * e + 1]) * f.y);
                 y[e + 1] = make_float2(__uint_as_float(x[2 * e + 2]) * f.z, __uint_as_float(x[2 * e + 3]) * f.w);
             }
-            split3(y, hi, mid, lo);
-            tmem_st8(tq + TM_U + t, hi);
-            tmem_st8(tq + TM_U + t + 8, mid);
-            tmem_st8(tq + TM_UX + t, lo);
+            split3(y, two, lo);
+            tmem_st16(tq + TM_U + t, two);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                two[e] = lo[e];
                 y[e] = as_pair(x[2 * e], x[2 * e + 1]);
-                hi[e] = pack_bf16x2(y[e].x, y[e].y);
-                rest(hi[e], y[e]);
+                two[8 + e] = pack_bf16x2(y[e].x, y[e].y);
+                rest(two[8 + e], y[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mid[e] = pack_bf16x2(y[e].x, y[e].y);
-            tmem_st8(tq + TM_UX + t + 8, hi);
-            tmem_st8(tq + TM_X + t / 2, mid);
+            for (int e = 0; e < 8; ++e) lo[e] = pack_bf16x2(y[e].x, y[e].y);
+            tmem_st16(tq + TM_UX + t, two);
+            tmem_st8(tq + TM_X + t / 2, lo);
             tmem_wait_st();
             tc_fence_before();
             arrive(sh, B_UP_READY + g, lane);
@@ -527,11 +547,13 @@ __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, in
     }
     if (p.final_state && ch_ok) {
 #pragma unroll
-        for (int x = 0; x < N / 2; ++x)
-            if (2 * x < rows) {
-                p.final_state[own + (long long)(2 * x) * p.dv] = st[x].x;
-                p.final_state[own + (long long)(2 * x + 1) * p.dv] = st[x].y;
+        for (int x = 0; x < 8 * GROUPS; ++x) {
+            const int i = 16 * step_of<GROUPS>(w, x / 8) + x % 8 * 2;
+            if (i < p.dk) {
+                p.final_state[own + (long long)i * p.dv] = st[x].x;
+                p.final_state[own + (long long)(i + 1) * p.dv] = st[x].y;
             }
+        }
     }
 }
 
@@ -611,17 +633,19 @@ __device__ void output_role(const Args &p, Shared *sh, int h, long long t0, long
 // in whole numbers, and a rest below 2^-11, summed in fp32, so that G_i - G_j is good to 2^-30 or
 // so however large G is.  A log decay below -128 is taken as -128: any span over it weighs nothing.
 //
-// T in fp32, by blocks: 16 x 16 by substitution, then twice
+// T in fp32, in A's place, by blocks: 8 x 8 by substitution, then three times
 //     [[P, 0], [B, Q]]^-1 = [[P^-1, 0], [-Q^-1 B P^-1, Q^-1]]
-// The products of the joins run on warp-wide tensor instructions with tf32 operands in two parts each (21 bits; what
-// is left out is below 2^-22 of |a| |b|): an operand read by a few narrow loads, where a product on the FMA pipe was
-// bound by shared memory's path (a 32 x 32 x 32 one took 1200 cycles, this 300).  Both operands stand along
-// k; what stands on the right is kept transposed, in places above the diagonal that nothing else uses.
+// The products of the joins run on warp-wide tensor instructions with tf32 operands in two parts each (what is left
+// out is some 2^-21 of |a| |b|): an operand read by a few narrow loads, where products on the FMA pipe were bound by
+// shared memory's path.  Both operands stand along k; what stands on the right is kept transposed, in places above the
+// diagonal that nothing else uses.
 
+// hi rounded to tf32 (a conversion instruction for it cost 6 % of the whole kernel), lo what is left, whose last bits
+// the product ignores
 __device__ __forceinline__ void tf32_parts(float x, uint32_t &hi, uint32_t &lo)
 {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
@@ -641,7 +665,7 @@ __device__ __forceinline__ void products(const float *a, const float *b, int len
     for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[n][e] = 0.f;
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < len; k += 8) {
         uint32_t ah[4], al[4], bh[2], bl[2];
         tf32_parts(a[at + k], ah[0], al[0]);
@@ -659,6 +683,90 @@ __device__ __forceinline__ void products(const float *a, const float *b, int len
     }
 }
 
+// A warp's two 16 x 16 blocks on the diagonal, of rows o .. o + 31
+template <typename F>
+__device__ __forceinline__ void diagonal(float *A, F turned, int o, int lane)
+{
+    {   // 8 x 8 blocks, a column per lane
+        const int b = lane >> 3, col = lane & 7;
+        float *a = A + (o + 8 * b) * (PITCH + 1), t[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = k == col ? 1.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4)   // what four columns' results take from the rows below
+#pragma unroll
+            for (int k = j + 1; k < 8; ++k) {
+                const float4 r = *reinterpret_cast<const float4 *>(a + k * PITCH + j);
+                t[k] = fmaf(-r.x, t[j], t[k]);
+                if (k > j + 1) t[k] = fmaf(-r.y, t[j + 1], t[k]);
+                if (k > j + 2) t[k] = fmaf(-r.z, t[j + 2], t[k]);
+                if (k > j + 3) t[k] = fmaf(-r.w, t[j + 3], t[k]);
+            }
+        __syncwarp();                    // (every lane has read its block)
+        const float4 x = make_float4(t[0], t[1], t[2], t[3]), y = make_float4(t[4], t[5], t[6], t[7]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k * PITCH + col] = t[k];
+        float4 *to = reinterpret_cast<float4 *>(a + col * PITCH + 8);   // transposed, beside the upper block of a pair
+        if (!(b & 1)) {
+            to[0] = x;
+            to[1] = y;
+        }
+        const int pair = (o >> 4) + (b >> 1);
+        to = reinterpret_cast<float4 *>(turned(pair) + (8 * (b & 1) + col) * PITCH);
+        if (pair < 3) {
+            if (b & 1) to[0] = to[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            to[2 * (b & 1)] = x;
+            to[2 * (b & 1) + 1] = y;
+        }
+        __syncwarp();
+    }
+    // The joins of both pairs in one: the first pair's rows are a product's upper half, the second's its lower; of a
+    // result for the other pair's columns half is of no use.
+    const int r = lane >> 2, t = lane & 3;
+    float *first = A + o * (PITCH + 1), *second = first + 16 * (PITCH + 1);
+    auto product = [&](int left, float (&y0)[4], float (&y1)[4]) {
+        uint32_t ah[4], al[4], bh[2], bl[2];
+        const int a = (8 + r) * PITCH + left + t, b = r * PITCH + 8 + t;
+        tf32_parts(first[a], ah[0], al[0]);
+        tf32_parts(second[a], ah[1], al[1]);
+        tf32_parts(first[a + 4], ah[2], al[2]);
+        tf32_parts(second[a + 4], ah[3], al[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y0[e] = y1[e] = 0.f;
+        tf32_parts(first[b], bh[0], bl[0]);
+        tf32_parts(first[b + 4], bh[1], bl[1]);
+        mma_tf32(y0, al, bh);
+        mma_tf32(y0, ah, bl);
+        mma_tf32(y0, ah, bh);
+        tf32_parts(second[b], bh[0], bl[0]);
+        tf32_parts(second[b + 4], bh[1], bl[1]);
+        mma_tf32(y1, al, bh);
+        mma_tf32(y1, ah, bl);
+        mma_tf32(y1, ah, bh);
+        __syncwarp();                    // (every lane has read its operands)
+    };
+    float y0[4], y1[4];
+    product(0, y0, y1);                  // Y = B P^-1, kept transposed over P^-1
+    const int at = 2 * t * PITCH + 8 + r;
+    first[at] = y0[0];
+    first[at + PITCH] = y0[1];
+    second[at] = y1[2];
+    second[at + PITCH] = y1[3];
+    __syncwarp();
+    product(8, y0, y1);                  // Q^-1 Y
+    *reinterpret_cast<float2 *>(first + (8 + r) * PITCH + 2 * t) = make_float2(-y0[0], -y0[1]);
+    *reinterpret_cast<float2 *>(second + (8 + r) * PITCH + 2 * t) = make_float2(-y1[2], -y1[3]);
+    *reinterpret_cast<float2 *>(first + r * PITCH + 8 + 2 * t) = make_float2(0.f, 0.f);
+    *reinterpret_cast<float2 *>(second + r * PITCH + 8 + 2 * t) = make_float2(0.f, 0.f);
+    const int pair = o >> 4;
+    turned(pair)[at] = -y0[0];
+    turned(pair)[at + PITCH] = -y0[1];
+    if (pair + 1 < 3) {
+        turned(pair + 1)[at] = -y1[2];
+        turned(pair + 1)[at + PITCH] = -y1[3];
+    }
+}
+
 __device__ void prep_role(const Args &p, uint8_t *smem, Shared *sh, int h, int regions, long long t0, long long len,
                           int nch)
 {
@@ -666,7 +774,10 @@ __device__ void prep_role(const Args &p, uint8_t *smem, Shared *sh, int h, int r
     const int par = (threadIdx.x >> 7) - 3, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
     const uint32_t tq = ((uint32_t)(32 * warp) << 16) + TM_GRAM, bar = 1 + par;
     uint8_t *parts = smem + SM_T + par * 3 * TILE;
-    float *A = reinterpret_cast<float *>(parts), *T = reinterpret_cast<float *>(smem + SM_TF + par * SQUARE);
+    float *A = reinterpret_cast<float *>(smem + SM_TF + par * SQUARE);
+    const int r = lane >> 2, q = (lane & 3) * 2;    // this lane's part of a product's result
+    // where a 16 x 16 block's inverse stands transposed (the last one's does not)
+    auto turned = [&](int b) { return A + (b ? 16 : 0) * PITCH + (b == 1 ? 48 : 32); };
     const bool lower = (warp >> 1) == par;          // makes A
     const int dec_warp = 2 - 2 * par;               // makes the decays
     float g0 = 0.f, g1 = 0.f, b0 = 0.f, b1 = 0.f;   // of tokens 2 lane, 2 lane + 1
@@ -738,8 +849,7 @@ __device__ void prep_role(const Args &p, uint8_t *smem, Shared *sh, int h, int r
         }
         if (!bar_and(bar, 128, ok)) break;   // the four warps leave together (and the last T of theirs is read)
         ok = wait_warp(sh, B_GRAM_DONE + par, c >> 1);
-        if (lower) ok = ok && (c < 2 || wait_warp(sh, B_T_FREE + par, (c >> 1) - 1));
-        else ok = ok && (c < P_TILES || wait_warp(sh, B_P_FREE + c % P_TILES, c / P_TILES - 1));
+        if (!lower) ok = ok && (c < P_TILES || wait_warp(sh, B_P_FREE + c % P_TILES, c / P_TILES - 1));
         if (ok) {
             tc_fence_after();
             const int row = 32 * (warp & 1), i = row + lane;
@@ -780,7 +890,7 @@ __device__ void prep_role(const Args &p, uint8_t *smem, Shared *sh, int h, int r
 #pragma unroll
                     for (int e = 0; e < 16; ++e) y[e] = e <= last ? y[e] : 0.f;
                 }
-                if (x >= row + 16 && lane < 16) continue;   // above the diagonal's block: not read
+                if (x >= row + 16 && lane < 16) continue;   // above the diagonal's block
                 if (lower) {
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
@@ -798,50 +908,25 @@ __device__ void prep_role(const Args &p, uint8_t *smem, Shared *sh, int h, int r
             if (!lower) fence_proxy_async_smem();
             arrive(sh, B_GRAM_FREE, lane);
             if (!lower && lane == 0) mbar_arrive(&sh->bars[B_P_READY + c % P_TILES]);
-            if (lower) {   // a column of a diagonal block per lane, two blocks (of the rows just made) a warp
-                const int o = 16 * ((tid & 63) >> 4), col = lane & 15;
-                const float *a = A + o * (PITCH + 1);
-                float t[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) t[k] = k == col ? 1.f : 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; j += 4)   // what four columns' results take from the rows below
-#pragma unroll
-                    for (int k = j + 1; k < 16; ++k) {
-                        const float4 r = *reinterpret_cast<const float4 *>(a + k * PITCH + j);
-                        t[k] = fmaf(-r.x, t[j], t[k]);
-                        if (k > j + 1) t[k] = fmaf(-r.y, t[j + 1], t[k]);
-                        if (k > j + 2) t[k] = fmaf(-r.z, t[j + 2], t[k]);
-                        if (k > j + 3) t[k] = fmaf(-r.w, t[j + 3], t[k]);
-                    }
-#pragma unroll
-                for (int k = 0; k < 16; ++k) T[(o + k) * PITCH + o + col] = t[k];
-                // transposed: of the first two blocks where the 32 x 32 block's goes, of the third beside itself
-                float *to = T + (o + col) * PITCH + (o < 32 ? 32 + o : o + 16);
-                if (o < 48) {
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4 *>(to + k) = make_float4(t[k], t[k + 1], t[k + 2], t[k + 3]);
-                }
-            }
+            if (lower) diagonal(A, turned, 32 * (warp & 1), lane);
         }
         if (!bar_and(bar, 128, ok)) break;
-        const int r = lane >> 2, q = (lane & 3) * 2;   // this lane's part of a product's result
         {   // the 32 x 32 blocks, two warps each: Y = B P^-1, and Q^-1 Y
             const int o = 32 * (warp >> 1), n = 8 * (warp & 1);
             float y[1][4];
-            products(A + (o + 16) * PITCH + o, T + (o + n) * PITCH + (o ? 48 : 32), 16, y);
+            products(A + (o + 16) * PITCH + o, turned(o >> 4) + n * PITCH, 16, y);
             float *to = A + (o + n + q) * PITCH + o + 16 + r;
             to[0] = y[0][0];
             to[PITCH] = y[0][1];
             to[8] = y[0][2];
             to[PITCH + 8] = y[0][3];
             named_bar_sync(bar, 128);
-            products(T + (o + 16) * PITCH + o + 16, A + (o + n) * PITCH + o + 16, 16, y);
-            to = T + (o + 16 + r) * PITCH + o + n + q;
+            products(A + (o + 16) * PITCH + o + 16, A + (o + n) * PITCH + o + 16, 16, y);
+            to = A + (o + 16 + r) * PITCH + o + n + q;
             *reinterpret_cast<float2 *>(to) = make_float2(-y[0][0], -y[0][1]);
             *reinterpret_cast<float2 *>(to + 8 * PITCH) = make_float2(-y[0][2], -y[0][3]);
             if (o == 0) {
-                to = T + (n + q) * PITCH + 48 + r;
+                to = A + (n + q) * PITCH + 48 + r;
                 to[0] = -y[0][0];
                 to[PITCH] = -y[0][1];
                 to[8] = -y[0][2];
@@ -852,7 +937,8 @@ __device__ void prep_role(const Args &p, uint8_t *smem, Shared *sh, int h, int r
         {   // the 64 x 64 block, 16 rows and columns a warp
             const int m = 16 * (warp & 1), n = 16 * (warp >> 1);
             float y[2][4];
-            products(A + (32 + m) * PITCH + n, T + n * PITCH + 32 + n, 32 - n, y);   // (P^-1 is 0 above its diagonal)
+            products(A + (32 + m) * PITCH + n, A + n * PITCH + 32 + n, 32 - n, y);   // (P^-1 is 0 above its diagonal)
+            named_bar_sync(bar, 128);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float *to = A + (n + 8 * x + q) * PITCH + 32 + m + r;
@@ -862,36 +948,30 @@ __device__ void prep_role(const Args &p, uint8_t *smem, Shared *sh, int h, int r
                 to[PITCH + 8] = y[x][3];
             }
             named_bar_sync(bar, 128);
-            products(T + (32 + m) * PITCH + 32, A + n * PITCH + 32, 16 + m, y);      // (nor is Q^-1)
+            products(A + (32 + m) * PITCH + 32, A + n * PITCH + 32, 16 + m, y);      // (nor is Q^-1)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float *to = T + (32 + m + r) * PITCH + n + 8 * x + q;
+                float *to = A + (32 + m + r) * PITCH + n + 8 * x + q;
                 *reinterpret_cast<float2 *>(to) = make_float2(-y[x][0], -y[x][1]);
                 *reinterpret_cast<float2 *>(to + 8 * PITCH) = make_float2(-y[x][2], -y[x][3]);
             }
         }
-        named_bar_sync(bar, 128);
-        // Columns times beta, in three bf16 parts, eight columns at a time: in rows i and 63 - i together nine such units up to the
-        // diagonal's (whose 16 x 16 block has its zeros), and seven above it, all 0.
+        ok = c < 2 || wait_warp(sh, B_T_FREE + par, (c >> 1) - 1);
+        if (!bar_and(bar, 128, ok)) break;
+        // Columns times beta, in three bf16 parts, eight columns at a time up to the diagonal's: nine such units in rows
+        // i and 63 - i together.
 #pragma unroll 1
-        for (int u = warp; u < 16; u += 4) {
-            const int m = (lane >> 3) + 1;
-            const bool mine = u < 9 ? u < m : u - 9 < 8 - m;
-            const int i = mine ? lane : 63 - lane, j = 8 * (u < 9 ? (mine ? u : u - m) : mine ? u - 9 + m : u - 8);
-            float2 y[4] = {};
-            if (u < 9) {
-                const float4 a = *reinterpret_cast<const float4 *>(T + i * PITCH + j), b = *reinterpret_cast<const float4 *>(T + i * PITCH + j + 4);
-                const float4 f = *reinterpret_cast<const float4 *>(&d.beta[j]), g = *reinterpret_cast<const float4 *>(&d.beta[j + 4]);
-                y[0] = mul2(make_float2(a.x, a.y), make_float2(f.x, f.y));
-                y[1] = mul2(make_float2(a.z, a.w), make_float2(f.z, f.w));
-                y[2] = mul2(make_float2(b.x, b.y), make_float2(g.x, g.y));
-                y[3] = mul2(make_float2(b.z, b.w), make_float2(g.z, g.w));
-            }
+        for (int u = warp; u < 9; u += 4) {
+            const int m = (lane >> 3) + 1, i = u < m ? lane : 63 - lane, j = 8 * (u < m ? u : u - m);
+            const float4 a = *reinterpret_cast<const float4 *>(A + i * PITCH + j), b = *reinterpret_cast<const float4 *>(A + i * PITCH + j + 4);
+            const float4 f = *reinterpret_cast<const float4 *>(&d.beta[j]), g = *reinterpret_cast<const float4 *>(&d.beta[j + 4]);
+            float2 y[4] = {make_float2(a.x * f.x, a.y * f.y), make_float2(a.z * f.z, a.w * f.w),
+                           make_float2(b.x * g.x, b.y * g.y), make_float2(b.z * g.z, b.w * g.w)};
+            uint32_t two[8], lo[4];
+            split3(y, two, lo);
             const uint32_t at = sw128(i, 2 * j);
-            uint32_t hi[4], mid[4], lo[4];
-            split3(y, hi, mid, lo);
-            *reinterpret_cast<uint4 *>(parts + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(parts + TILE + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            *reinterpret_cast<uint4 *>(parts + at) = make_uint4(two[0], two[1], two[2], two[3]);
+            *reinterpret_cast<uint4 *>(parts + TILE + at) = make_uint4(two[4], two[5], two[6], two[7]);
             *reinterpret_cast<uint4 *>(parts + 2 * TILE + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async_smem();
@@ -931,6 +1011,10 @@ delta_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         tma_prefetch_desc(&mk);
         tma_prefetch_desc(&mv);
     }
+    // what stands above the diagonals of T's parts and of P stays 0
+    static_assert(SM_P == SM_T + 6 * TILE, "one range");
+    for (int x = threadIdx.x; x < (6 + P_TILES) * (int)TILE / 16; x += kThreads) reinterpret_cast<uint4 *>(smem + SM_T)[x] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
     if (warp == 20) {
         tmem_alloc(&sh->tmem, TM_COLS);
         tmem_relinquish();

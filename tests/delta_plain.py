@@ -62,7 +62,8 @@ def chunked_bounds(q, k, v, g, beta, lengths, init=None, scale=1.0, chunk=64):
       - R and T in three bf16 parts (8 bits each, all of fp32's), of whose nine products the three smallest, each at
         most 2^-24 |T| |R|, are left out
       - w off by 2^-22 (1 + |x|) of itself, A by that and its sums' roundings, T by |T| dA |T| and by the block
-        inverse's roundings, 3 x 64 eps |T| (I + |A|) |T|
+        inverse's: three joins of two products each, whose operands' parts leave out 2^-21 of |a| |b| thrice at most and
+        whose sums of up to 32 terms round twice eps: 6 (24 + 64) eps |T| (I + |A|) |T|
       - sums in fp32 of 3 d_k, or 6 x 64, terms, each rounding twice eps (the accumulator may cut off)
     An error of the start state only shrinks (see recurrence), so a chunk adds sum_j e^(G_C - G_j) |du_j| to it, and
     the roundings of its own sum.  Outputs take one bf16 rounding (2^-8) of the state, of P = w (q . k) and of u each."""
@@ -93,7 +94,7 @@ def chunked_bounds(q, k, v, g, beta, lengths, init=None, scale=1.0, chunk=64):
             eye = torch.eye(e - b, dtype=torch.float64, device=v.device)
             inv = torch.linalg.inv(eye + a)
             ti = inv.abs()
-            dt = ti @ da @ ti + 192 * EPS * ti @ (eye + a.abs()) @ ti
+            dt = ti @ da @ ti + 528 * EPS * ti @ (eye + a.abs()) @ ti
             gam, dgam = cum.exp()[..., None], (cum.exp() * 2.0 ** -22 * (1 + cum.abs()))[..., None]
             norm = start[0].norm(dim=-2)[:, None, :]                                                 # [h, 1, dv]
             r = bb[..., None] * (vv - gam * (kk @ start[0]))

@@ -116,12 +116,12 @@ def test_rows_behind_and_nan():
     assert kda.device_status() == 0
 
 
-def test_a_nan_reaches_back_at_most_15_tokens():
-    x = inputs([128], 1, 1, 128, 128, BF16, seed=10)
+def test_a_nan_reaches_back_to_its_chunk_at_most():
+    x = inputs([192], 1, 1, 128, 128, BF16, seed=10)
     want, _ = call(x)
     x["v"][101] = float("nan")
     out, _ = call(x)
-    assert torch.equal(out[:96], want[:96]) and bool(out[101:].isnan().all())
+    assert torch.equal(out[:64], want[:64]) and bool(out[101:].isnan().all())
 
 
 def test_in_place_graph_streams():
