@@ -7,15 +7,18 @@
 // A row has a scale of its own because a state's key channels differ in magnitude by what was written under
 // them.  The code is that of the exact quotient: the remainder x - code s is exact in one fused
 // multiply-add, and a code that it shows to be the wrong neighbour is moved by one.
-// Bound by HBM: 4 bytes an element on one side, 1 (and 4 a row) or 2 on the other.  LANES lanes take a row,
-// four columns each (a row past 128 columns in two pieces), and a warp has four loads in flight.
+// Bound by HBM: 4 bytes an element on one side, 1 (and 4 a row) or 2 on the other.  LANES lanes take a row in V
+// pieces of four columns each, U rows in flight a thread.  64 slots of 96 heads of 128 x 128, warm, of the measured
+// copy rate: int8 written 88 us (0.85), read back 80 us (0.93); bf16 written 103 us (0.87), read back 92 us (0.96).
+// 64 x 64: 25 us (0.75) and 24 us (0.79).  72 columns, written: 66 us (0.64), one lane in four of the row idle.
+#include <type_traits>
+
 #include "kda_internal.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kDepth = 4;             // rows (or pieces of them) in flight a thread
 
 __device__ int g_state_pack_error;    // sticky device error word of this translation unit
 
@@ -73,12 +76,11 @@ __device__ __forceinline__ float scale_of(float top)
     return fmaf(fmaf(-q, 127.f, top), 1.f / 127.f, q);
 }
 
-// LANES lanes a row of at most 4 LANES V columns
-template <int LANES, int V>
+// LANES lanes a row of at most 4 LANES V columns, U rows in flight a thread
+template <int LANES, int V, int U>
 __global__ void __launch_bounds__(kThreads) state_pack8_kernel(const Move m)
 {
     constexpr int SIDE = kThreads / LANES;           // rows of the block side by side
-    constexpr int U = V == 1 ? kDepth : kDepth / 2;
     const int lane = threadIdx.x % LANES, side = threadIdx.x / LANES;
     for (int64_t i = blockIdx.y; i < m.n; i += gridDim.y) {
         int64_t hs, fs;
@@ -97,45 +99,46 @@ __global__ void __launch_bounds__(kThreads) state_pack8_kernel(const Move m)
                     x[u][c] = row < m.rows && col < m.dv ? __ldcs(reinterpret_cast<const float4 *>(from + row * m.dv + col))
                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
+            uint32_t top[U];                         // magnitudes as bits: infinities and NaN are the largest
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                uint32_t top = 0;                    // magnitudes as bits: infinities and NaN are the largest
+                top[u] = 0;
 #pragma unroll
                 for (int c = 0; c < V; ++c)
-                    top = max(top, max(max(__float_as_uint(x[u][c].x) & 0x7fffffffu, __float_as_uint(x[u][c].y) & 0x7fffffffu),
-                                       max(__float_as_uint(x[u][c].z) & 0x7fffffffu, __float_as_uint(x[u][c].w) & 0x7fffffffu)));
-                if constexpr (LANES == 32) {
-                    top = __reduce_max_sync(0xffffffffu, top);
-                } else {
+                    top[u] = max(top[u], max(max(__float_as_uint(x[u][c].x) & 0x7fffffffu, __float_as_uint(x[u][c].y) & 0x7fffffffu),
+                                             max(__float_as_uint(x[u][c].z) & 0x7fffffffu, __float_as_uint(x[u][c].w) & 0x7fffffffu)));
+            }
 #pragma unroll
-                    for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                }
-                const float s = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : scale_of(__uint_as_float(top));
+            for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int u = 0; u < U; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+            float s[U], inv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u] = top[u] >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : scale_of(__uint_as_float(top[u]));
                 // (the reciprocal of a scale that is all but 0 would overflow)
-                const float inv = s >= 1e-30f ? __frcp_rn(s) : 0.f;
+                inv[u] = s[u] >= 1e-30f ? __frcp_rn(s[u]) : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
                 const int64_t row = r0 + u * SIDE + side;
-                if (row >= m.rows) continue;
-                if (lane == 0) scales[row] = s;
-                const bool any = s > 0.f;            // else a row of zeros, or one not finite: codes 0
+                if (row >= m.rows) break;
+                if (lane == 0) scales[row] = s[u];
 #pragma unroll
                 for (int c = 0; c < V; ++c) {
                     const int col = 4 * (lane + c * LANES);
-                    if (col >= m.dv) continue;
-                    const float4 f = x[u][c];
-                    uint32_t w = 0;
-                    if (any) w = codes(f, s, inv);
-                    *reinterpret_cast<uint32_t *>(to + row * m.dv + col) = w;
+                    // a row of zeros, or one not finite, has codes 0
+                    if (col < m.dv) *reinterpret_cast<uint32_t *>(to + row * m.dv + col) = s[u] > 0.f ? codes(x[u][c], s[u], inv[u]) : 0u;
                 }
             }
         }
     }
 }
 
-template <int LANES, int V>
+template <int LANES, int V, int U>
 __global__ void __launch_bounds__(kThreads) state_unpack8_kernel(const Move m)
 {
     constexpr int SIDE = kThreads / LANES;
-    constexpr int U = 2 * (V == 1 ? kDepth : kDepth / 2);
     const int lane = threadIdx.x % LANES, side = threadIdx.x / LANES;
     for (int64_t i = blockIdx.y; i < m.n; i += gridDim.y) {
         int64_t hs, fs;
@@ -225,17 +228,41 @@ int run(const Move &m, int format, bool pack, cudaStream_t stream)
         if (pack) state_bf16_kernel<true><<<blocks(4 * kThreads), kThreads, 0, stream>>>(m);
         else state_bf16_kernel<false><<<blocks(4 * kThreads), kThreads, 0, stream>>>(m);
     } else {
-        const int depth = m.dv <= 128 ? kDepth : kDepth / 2;
+        auto pack8 = [&](auto lanes, auto v, auto u) {
+            constexpr int L = decltype(lanes)::value, V = decltype(v)::value, U = decltype(u)::value;
+            state_pack8_kernel<L, V, U><<<blocks(kThreads / L * U), kThreads, 0, stream>>>(m);
+        };
+        auto unpack8 = [&](auto lanes, auto v, auto u) {
+            constexpr int L = decltype(lanes)::value, V = decltype(v)::value, U = decltype(u)::value;
+            state_unpack8_kernel<L, V, U><<<blocks(kThreads / L * U), kThreads, 0, stream>>>(m);
+        };
+        using std::integral_constant;
+        using one = integral_constant<int, 1>;
+        using two = integral_constant<int, 2>;
+        using three = integral_constant<int, 3>;
+        using four = integral_constant<int, 4>;
+        using quarter = integral_constant<int, 4>;
+        using eight = integral_constant<int, 8>;
+        using half = integral_constant<int, 16>;
+        using whole = integral_constant<int, 32>;
+        // Packing wants few rows in flight and long pieces of them: a row's maximum crosses its lanes and is divided
+        // by 127 in each, so eight lanes of sixteen values cost less than thirty-two of four.  64 x 96 states of
+        // 128 x 128: 32 lanes and 4 rows 106 us, 8 rows 135; 16 lanes and 4, 2, 1 rows 117, 95, 116; 8 lanes and 1
+        // row 88.  64 wide: 16 lanes 32, 8 lanes 27, 4 lanes 25.  72 wide: 32 lanes of which 14 idle 104, here 66.
+        // 32 states of 32 heads of 256 x 256: 32 lanes and 2 rows 66, 16 lanes 60, 8 lanes 56.
+        // Reading back has nothing across lanes and wants every load in flight that registers hold.
         if (pack) {
-            if (m.dv <= 32) state_pack8_kernel<8, 1><<<blocks(kThreads / 8 * depth), kThreads, 0, stream>>>(m);
-            else if (m.dv <= 64) state_pack8_kernel<16, 1><<<blocks(kThreads / 16 * depth), kThreads, 0, stream>>>(m);
-            else if (m.dv <= 128) state_pack8_kernel<32, 1><<<blocks(kThreads / 32 * depth), kThreads, 0, stream>>>(m);
-            else state_pack8_kernel<32, 2><<<blocks(kThreads / 32 * depth), kThreads, 0, stream>>>(m);
+            if (m.dv <= 32) pack8(quarter{}, two{}, two{});
+            else if (m.dv <= 64) pack8(quarter{}, four{}, one{});
+            else if (m.dv <= 96) pack8(eight{}, three{}, one{});
+            else if (m.dv <= 128) pack8(eight{}, four{}, one{});
+            else pack8(eight{}, eight{}, one{});
         } else {
-            if (m.dv <= 32) state_unpack8_kernel<8, 1><<<blocks(kThreads / 8 * 2 * depth), kThreads, 0, stream>>>(m);
-            else if (m.dv <= 64) state_unpack8_kernel<16, 1><<<blocks(kThreads / 16 * 2 * depth), kThreads, 0, stream>>>(m);
-            else if (m.dv <= 128) state_unpack8_kernel<32, 1><<<blocks(kThreads / 32 * 2 * depth), kThreads, 0, stream>>>(m);
-            else state_unpack8_kernel<32, 2><<<blocks(kThreads / 32 * 2 * depth), kThreads, 0, stream>>>(m);
+            if (m.dv <= 32) unpack8(eight{}, one{}, eight{});
+            else if (m.dv <= 64) unpack8(half{}, one{}, eight{});
+            else if (m.dv <= 96) unpack8(eight{}, three{}, four{});
+            else if (m.dv <= 128) unpack8(whole{}, one{}, eight{});
+            else unpack8(whole{}, two{}, four{});
         }
     }
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
