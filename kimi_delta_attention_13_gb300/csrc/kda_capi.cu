@@ -115,6 +115,18 @@ bool meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
     return a && b && a_bytes > 0 && b_bytes > 0 && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
 
+int64_t bytes_of(int32_t dtype) { return dtype == KDA_BF16 ? 2 : 4; }
+
+// Whether what a kda_delta call writes meets the operands of its `rows` tokens.
+bool delta_overlap(const void *to, int64_t bytes, const void *q, const void *k, const void *v, const float *g,
+                   int32_t g_per_token, const float *beta, int64_t rows, int32_t n_heads, int32_t n_key_heads,
+                   int32_t d_k, int32_t d_v, int32_t dtype)
+{
+    const int64_t keys = rows * n_key_heads * d_k * bytes_of(dtype);
+    return meet(to, bytes, q, keys) || meet(to, bytes, k, keys) || meet(to, bytes, v, rows * n_heads * d_v * bytes_of(dtype)) ||
+           meet(to, bytes, g, (g_per_token ? rows : 1) * n_heads * 4) || meet(to, bytes, beta, rows * n_heads * 4);
+}
+
 // Validation shared by kda_state_pack and kda_state_unpack: the pool (`held`, `scales`) and the states.
 int check_pack(const void *held, const float *scales, int32_t format, const int64_t *held_idx, int64_t n_held,
                const float *full, const int64_t *full_idx, int64_t n_full, int64_t n, int32_t n_heads, int32_t d_k,
@@ -135,6 +147,9 @@ int check_pack(const void *held, const float *scales, int32_t format, const int6
     if (meet(held, held_bytes, full, full_bytes) || meet(scales, scale_bytes, full, full_bytes) ||
         meet(scales, scale_bytes, held, held_bytes))
         return KDA_ERR_INVALID_ARG;
+    for (const int64_t *idx : {held_idx, full_idx})
+        if (meet(idx, 8 * n, held, held_bytes) || meet(idx, 8 * n, full, full_bytes) || meet(idx, 8 * n, scales, scale_bytes))
+            return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
 
@@ -407,8 +422,17 @@ int kda_delta_prefill(const void *q, const void *k, const void *v, const float *
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
     if (!aligned4(g) || !aligned4(beta) || !aligned4(cu_seqlens)) return KDA_ERR_MISALIGNED;
-    if (aliases(out, {q, k, v, g, beta, cu_seqlens, init_state, final_state}) ||
-        aliases(final_state, {q, k, v, g, beta, cu_seqlens}))
+    if ((int64_t)n_seqs * n_heads > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const int64_t states = (int64_t)n_seqs * n_heads * d_k * d_v * 4;
+    if (delta_overlap(out, total_tokens * n_heads * d_v * bytes_of(out_dtype), q, k, v, g, g_per_token, beta,
+                      total_tokens, n_heads, n_key_heads, d_k, d_v, dtype) ||
+        delta_overlap(final_state, states, q, k, v, g, g_per_token, beta, total_tokens, n_heads, n_key_heads, d_k, d_v,
+                      dtype) ||
+        meet(out, total_tokens * n_heads * d_v * bytes_of(out_dtype), init_state, states) ||
+        meet(out, total_tokens * n_heads * d_v * bytes_of(out_dtype), final_state, states) ||
+        meet(out, total_tokens * n_heads * d_v * bytes_of(out_dtype), cu_seqlens, 4 * ((int64_t)n_seqs + 1)) ||
+        meet(final_state, states, cu_seqlens, 4 * ((int64_t)n_seqs + 1)) ||
+        (final_state != init_state && meet(final_state, states, init_state, states)))
         return KDA_ERR_INVALID_ARG;
     return launch_delta_prefill(q, k, v, g, g_per_token != 0, beta, cu_seqlens, n_seqs, total_tokens, n_heads,
                                 n_key_heads, d_k, d_v, scale, dtype, out_dtype, init_state, out, final_state,
@@ -430,7 +454,13 @@ int kda_delta_decode(const void *q, const void *k, const void *v, const float *g
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_MISALIGNED;
     if (!aligned4(g) || !aligned4(beta)) return KDA_ERR_MISALIGNED;
-    if (aliases(out, {q, k, v, g, beta, state}) || aliases(state, {q, k, v, g, beta})) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)n_seqs * n_heads > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED_SHAPE;
+    const int64_t states = (int64_t)n_seqs * n_heads * d_k * d_v * 4;
+    const int64_t outs = (int64_t)n_seqs * n_heads * d_v * bytes_of(out_dtype);
+    if (delta_overlap(out, outs, q, k, v, g, g_per_token, beta, n_seqs, n_heads, n_key_heads, d_k, d_v, dtype) ||
+        delta_overlap(state, states, q, k, v, g, g_per_token, beta, n_seqs, n_heads, n_key_heads, d_k, d_v, dtype) ||
+        meet(out, outs, state, states))
+        return KDA_ERR_INVALID_ARG;
     return launch_delta_decode(q, k, v, g, g_per_token != 0, beta, state, out, n_seqs, n_heads, n_key_heads, d_k,
                                d_v, scale, dtype, out_dtype, (cudaStream_t)stream);
 }

@@ -305,7 +305,7 @@ int launch_delta_prefill(const void *q, const void *k, const void *v, const floa
     p.q = q; p.k = k; p.v = v; p.g = g;
     p.g_per_token = g_per_token;
     p.beta = beta;
-    p.cu = n_seqs == 1 ? nullptr : cu;
+    p.cu = cu;
     p.n_seqs = n_seqs;
     p.T = T;
     p.H = H;

@@ -23,7 +23,7 @@ from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
 
-from . import num_checkpoints, prefill, state_copy, state_pack, state_unpack
+from . import _on_stream, num_checkpoints, prefill, state_copy, state_pack, state_unpack
 
 
 class CheckpointStore:
@@ -97,8 +97,9 @@ class CheckpointStore:
         dst = [self._take_slot(e) for e in entries]
         if entries:
             dev = self.states.device
-            self.write(torch.tensor(dst, device=dev, dtype=torch.int64), ckpts,
-                       torch.tensor(src, device=dev, dtype=torch.int64), stream=stream)
+            with _on_stream(dev, stream):   # what the copy reads belongs to its stream
+                slots, rows = (torch.tensor(x, device=dev, dtype=torch.int64) for x in (dst, src))
+            self.write(slots, ckpts, rows, stream=stream)
         return [(k, n, s) for (k, n), s in zip(entries, dst)]
 
     def lookup(self, key: object, n_tokens: int) -> Tuple[Optional[int], int]:
@@ -122,11 +123,12 @@ def resume_prefill(store: CheckpointStore, slots: Sequence[Optional[int]], q, k,
         raise ValueError("one slot per request")
     _, H, dk, dv = store.states.shape
     dev = store.states.device
-    init = torch.zeros(n, H, dk, dv, device=dev, dtype=torch.float32)
     pairs = [(i, s) for i, s in enumerate(slots) if s is not None]
+    with _on_stream(dev, stream):   # zeros before the restored states, on their stream
+        init = torch.zeros(n, H, dk, dv, device=dev, dtype=torch.float32)
+        to, of = (torch.tensor([p[x] for p in pairs], device=dev, dtype=torch.int64) for x in (0, 1))
     if pairs:
-        store.read(init, torch.tensor([i for i, _ in pairs], device=dev, dtype=torch.int64),
-                   torch.tensor([s for _, s in pairs], device=dev, dtype=torch.int64), stream=stream)
+        store.read(init, to, of, stream=stream)
     o, f, _ = prefill(q, k, v, g, beta, cu_seqlens, init, out=out, final_state=final_state,
                       lengths=lengths, out_dtype=out_dtype, stream=stream)
     return o, f, init

@@ -31,6 +31,34 @@ def test_prefill_rejects(lib, over, code):
     assert prefill(lib, **over) == code
 
 
+# one byte into another's memory, and one behind it: [16, 4 or 2, 128] bf16 is 16 or 8 KB, out 32 KB, the state 256 KB
+@pytest.mark.parametrize("over,code", [
+    (dict(out=A + 8176), 1), (dict(out=3 * A + 16368), 1), (dict(out=4 * A + 240), 1), (dict(out=3 * A - 32752), 1),
+    (dict(out=7 * A + 262128), 1), (dict(out=8 * A, init=7 * A + 16), 1), (dict(fin=2 * A + 8176), 1), (dict(fin=6 * A - 16), 1),
+    (dict(cu=6 * A + 4), 1), (dict(cu=7 * A + 8), 1)])
+def test_prefill_rejects_overlap(lib, over, code):
+    assert prefill(lib, **over) == code
+
+
+@pytest.mark.parametrize("over", [dict(out=3 * A + 3056), dict(out=6 * A + 16), dict(state=5 * A - 16), dict(state=7 * A - 16)])
+def test_decode_rejects_overlap(lib, over):
+    a = dict(q=A, k=2 * A, v=3 * A, g=4 * A, per=0, beta=5 * A, state=6 * A, out=7 * A, n=3, H=4, Hk=2, dk=128, dv=128,
+             scale=1.0, dt=0, odt=0)
+    a.update(over)
+    assert lib.kda_delta_decode(*a.values(), None) == 1
+
+
+@pytest.mark.parametrize("over", [dict(didx=2 * (1 << 40) + 64), dict(sidx=(1 << 40) + 64), dict(didx=1 << 20)])
+def test_pack_rejects_indices_in_its_memory(lib, over):
+    a = dict(dst=1 << 40, scales=1 << 20, fmt=1, didx=None, nd=8, src=2 << 40, sidx=None, ns=8, n=3, H=2, dk=128, dv=128)
+    a.update(over)
+    assert lib.kda_state_pack(*a.values(), None) == 1
+
+
+def test_timeout_probe_rejects(lib):
+    assert lib.kda_diag_delta_timeout(0, None) == 1 and lib.kda_diag_delta_timeout(4000000001, None) == 1
+
+
 def test_nothing_to_do(lib):
     assert prefill(lib, T=0, n=0, q=None, k=None, v=None, g=None, beta=None, out=None, fin=None) == 0
     assert lib.kda_delta_decode(None, None, None, None, 1, None, None, None, 0, 4, 2, 128, 128, 1.0, 0, 1, None) == 0
