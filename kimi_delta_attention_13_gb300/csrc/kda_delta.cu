@@ -18,12 +18,11 @@
 // scheduler for the update.  2560 tokens in two sequences, 16 heads of 64 x 128: 0.50 ms (token by token, with
 // the sums folded inside a warp, 0.88; 64 columns a block 0.55).
 #include "kda_delta.cuh"
+#include "sm100_ptx.cuh"
 
 namespace kda {
 namespace delta {
 namespace {
-
-constexpr int kRows = 8;     // key channels of a warp
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ uint2 load4(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
@@ -34,245 +33,335 @@ __device__ __forceinline__ float4 widen(uint2 x)
                        __uint_as_float(x.y & 0xffff0000u));
 }
 
-// tokens at a time
-template <int WARPS>
-constexpr int kTokens = WARPS <= 16 ? 8 : 4;
+constexpr int TB = 8;        // tokens at a time
+constexpr int kChain = 4;    // warps that hold the state, 16 value columns each
+constexpr int kMakers = 4;   // warps that make what does not depend on it
+constexpr int COLS = 16 * kChain;
 
-template <typename T, typename TO, int WARPS, int CPL>
-__global__ void __launch_bounds__(32 * WARPS) delta_token_kernel(const Args p)
+// what a block of tokens is worked from: staged, scored, solved and used in four periods
+template <int DK, int PARTS>
+struct __align__(16) Stage {
+    uint16_t k[PARTS][TB][DK + 8], q[PARTS][TB][DK + 8];   // bf16 parts (rows padded against bank conflicts)
+    float v[TB][COLS + 4];
+    float a[TB][12], m[TB][12], p[TB][12];     // beta w (k . k);  (I + a)^-1 diag(beta);  w (q . k)
+    float g[TB], beta[TB], pre[TB], suf[TB];   // log decays, beta, e^G, e^(G_last - G)
+    float all, near, unused[2];                // the whole block's decay, less 1 where it is near 1
+};
+template <int DK>
+struct Rows {
+    float k[TB][DK + 4], q[TB][DK + 4];        // for the scores
+};
+
+// x, y as three packed pairs of bf16, which sum to them
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo)
 {
-    constexpr int THREADS = 32 * WARPS, DK = kRows * WARPS, TB = kTokens<WARPS>, kCols = 32 * CPL;
-    constexpr int KUNITS = TB * DK / 4, VUNITS = TB * kCols / 4;
-    constexpr int KU = (KUNITS + THREADS - 1) / THREADS;
-    constexpr int DP = DK + 4;                        // padded rows: the score threads walk several at once
-    constexpr int SUB = THREADS / (TB * TB) < 32 ? THREADS / (TB * TB) : 32;   // threads of a score
+    float2 r = make_float2(x, y);
+    hi = ptx::pack_bf16x2(r.x, r.y);
+    rest(hi, r);
+    mid = ptx::pack_bf16x2(r.x, r.y);
+    rest(mid, r);
+    mid ^= 0x80008000u;
+    lo = ptx::pack_bf16x2(r.x, r.y);
+}
+
+// c [16 x 8] += a [16 x 16] b [16 x 8]; lane l = 4 x + y has of c the rows x, x + 8 and columns 2 y, 2 y + 1; of a the
+// same rows at k = 2 y, + 1, then at k + 8; of b column x at k = 2 y, + 1, then at k + 8
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// four tiles of 8 tokens x 8 channels: element (token x, channels 2 y, + 1), or (tokens 2 y, + 1, channel x)
+__device__ __forceinline__ void tiles(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tiles_trans(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
+// c += x y over 8 tokens, x [16 x 8] and y [8 x 8] in three parts: two parts of x side by side in k
+__device__ __forceinline__ void mma_tokens(float (&c)[4], float (&small)[4], const uint32_t (&x)[3][2], const uint32_t (&y)[3])
+{
+    mma(c, x[0][0], x[0][1], x[1][0], x[1][1], y[0], y[0]);
+    mma(small, x[0][0], x[0][1], x[1][0], x[1][1], y[1], y[1]);
+    mma(small, x[0][0], x[0][1], x[2][0], x[2][1], y[2], y[0]);
+}
+
+template <typename T, typename TO, int DK>
+__global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(const Args p)
+{
+    constexpr int PARTS = sizeof(T) == 4 ? 3 : 1, MT = 32 * kMakers;
+    constexpr int KU = TB * DK / 4 / MT, PITCH = (DK + 8) * 2;
+    constexpr int SUB = MT / (TB * TB);               // threads of a score
+    static_assert(TB * DK / 4 % MT == 0 && TB * COLS / 4 == MT && SUB == 2, "");
     using Four = decltype(load4((const T *)nullptr));
-    extern __shared__ __align__(16) float parts[];    // [2][TB][WARPS][kCols]: S^T k, S^T q of a warp's channels
-    __shared__ __align__(16) float sk[TB][DP], sq[TB][DP];
-    __shared__ __align__(16) float sv[TB][kCols], su[TB][kCols];
-    struct Decays {
-        float g[TB], beta[TB], pre[TB], suf[TB];      // log decays, beta, e^G, e^(G_last - G)
-        float all, one;                               // the whole block's decay (see above)
-    };
-    __shared__ Decays sd[2];                          // this block's and the next one's
-    __shared__ float sa[TB][TB + 1], sp[TB][TB + 1];  // beta w (k . k), w (q . k)
-    constexpr int DEC = 2;                            // the warp that makes the decays, while others substitute
+    extern __shared__ __align__(16) char raw[];
+    Stage<DK, PARTS> *stages = reinterpret_cast<Stage<DK, PARTS> *>(raw);   // [4]
+    Rows<DK> *rows = reinterpret_cast<Rows<DK> *>(stages + 4);              // [2]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / p.group, Hk = p.H / p.group;
-    const int cb = blockIdx.y * kCols, col = cb + lane;
-    auto part = [&](int which, int t, int w) { return parts + ((which * TB + t) * WARPS + w) * kCols; };
+    const int cb = blockIdx.y * COLS;
     long long b, e;
     bounds(p, seq, b, e);
-    const long long own = ((long long)seq * p.H + h) * p.dk * p.dv;
-    float st[kRows][CPL];
+    const int nb = (int)((e - b + TB - 1) / TB), first = nb ? -3 : 0;
+    if (warp >= kChain) {
+        const int mid = tid - 32 * kChain;
+        const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
+        Four nk[KU], nq[KU], nv;
+        float ng = 0.f, nbeta = 0.f;
+        auto fetch = [&](int m) {   // block m into registers (tokens past the end neither decay nor write)
+            const long long tb = b + (long long)m * TB;
+            const Four zero = {};
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+            for (int u = 0; u < KU; ++u) {
+                const int x = mid + u * MT, t = x / (DK / 4), i = x % (DK / 4) * 4;
+                const bool ok = tb + t < e && i < p.dk;
+                nk[u] = ok ? load4(k + ((tb + t) * Hk + hk) * p.dk + i) : zero;
+                nq[u] = ok ? load4(q + ((tb + t) * Hk + hk) * p.dk + i) : zero;
+            }
+            const int t = mid / (COLS / 4), c = cb + mid % (COLS / 4) * 4;
+            nv = tb + t < e && c < p.dv ? load4(v + ((tb + t) * p.H + h) * p.dv + c) : zero;
+            if (warp == kChain + 1 && lane < TB) {
+                const bool ok = tb + lane < e;
+                ng = ok ? p.g[p.g_per_token ? (tb + lane) * p.H + h : h] : 0.f;
+                nbeta = ok ? p.beta[(tb + lane) * p.H + h] : 0.f;
+            }
+        };
+        auto put = [&](uint16_t (&to)[PARTS][TB][DK + 8], float (&wide)[TB][DK + 4], int t, int i, Four x) {
+            const float4 f = widen(x);
+            *reinterpret_cast<float4 *>(&wide[t][i]) = f;
+            if constexpr (PARTS == 3) {
+                uint2 hi, md, lo;
+                split(f.x, f.y, hi.x, md.x, lo.x);
+                split(f.z, f.w, hi.y, md.y, lo.y);
+                *reinterpret_cast<uint2 *>(&to[0][t][i]) = hi;
+                *reinterpret_cast<uint2 *>(&to[1][t][i]) = md;
+                *reinterpret_cast<uint2 *>(&to[2][t][i]) = lo;
+            } else {
+                *reinterpret_cast<uint2 *>(&to[0][t][i]) = x;
+            }
+        };
+        if (nb) fetch(0);
+        for (int it = first; it < nb; ++it) {
+            if (it + 2 >= 0 && it + 2 < nb) {   // score
+                Stage<DK, PARTS> &s = stages[(it + 2) & 3];
+                const Rows<DK> &f = rows[it & 1];
+                const int i = mid / SUB / TB, j = mid / SUB % TB;
+                float w = 0.f;
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            const int i = warp * kRows + r;
-            st[r][c] = p.init && col + 32 * c < p.dv && i < p.dk ? p.init[own + (long long)i * p.dv + col + 32 * c] : 0.f;
-        }
-    const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
-    Four nk[KU], nq[KU], nv;
-    float ng = 0.f, nb = 0.f;
-    auto fetch = [&](long long tb) {
-        const Four zero = {};
+                for (int l = 1; l < TB; ++l) w += l > j && l <= i ? s.g[l] : 0.f;
+                w = expf(w);
+                float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), q4 = k4;
+#pragma unroll 8
+                for (int x = mid % SUB * 4; x < DK; x += 4 * SUB) {
+                    const float4 kj = *reinterpret_cast<const float4 *>(&f.k[j][x]);
+                    const float4 ki = *reinterpret_cast<const float4 *>(&f.k[i][x]);
+                    const float4 qi = *reinterpret_cast<const float4 *>(&f.q[i][x]);
+                    k4.x = fmaf(kj.x, ki.x, k4.x); k4.y = fmaf(kj.y, ki.y, k4.y); k4.z = fmaf(kj.z, ki.z, k4.z); k4.w = fmaf(kj.w, ki.w, k4.w);
+                    q4.x = fmaf(kj.x, qi.x, q4.x); q4.y = fmaf(kj.y, qi.y, q4.y); q4.z = fmaf(kj.z, qi.z, q4.z); q4.w = fmaf(kj.w, qi.w, q4.w);
+                }
+                float kk = (k4.x + k4.y) + (k4.z + k4.w), qk = (q4.x + q4.y) + (q4.z + q4.w);
 #pragma unroll
-        for (int u = 0; u < KU; ++u) {
-            const int x = tid + u * THREADS, t = x / (DK / 4), i = x % (DK / 4) * 4;
-            const bool ok = x < KUNITS && tb + t < e && i < p.dk;
-            nk[u] = ok ? load4(k + ((tb + t) * Hk + hk) * p.dk + i) : zero;
-            nq[u] = ok ? load4(q + ((tb + t) * Hk + hk) * p.dk + i) : zero;
-        }
-        {
-            const int t = tid / (kCols / 4), c = cb + tid % (kCols / 4) * 4;
-            nv = tid < VUNITS && tb + t < e && c < p.dv ? load4(v + ((tb + t) * p.H + h) * p.dv + c) : zero;
-        }
-        if (warp == DEC && lane < TB) {   // (tokens past the end neither decay nor write)
-            const bool ok = tb + lane < e;
-            ng = ok ? p.g[p.g_per_token ? (tb + lane) * p.H + h : h] : 0.f;
-            nb = ok ? p.beta[(tb + lane) * p.H + h] : 0.f;
-        }
-    };
-    auto decays = [&](Decays &to) {   // (lanes from TB on hold 0, the sums that reach past the block stay in it)
-        float after = ng, before = ng;
+                for (int o = SUB / 2; o > 0; o >>= 1) {
+                    kk += __shfl_xor_sync(0xffffffffu, kk, o);
+                    qk += __shfl_xor_sync(0xffffffffu, qk, o);
+                }
+                if (mid % SUB == 0) {
+                    s.a[i][j] = s.beta[i] * w * kk;
+                    s.p[i][j] = j <= i ? w * qk : 0.f;
+                }
+            }
+            if (it + 1 >= 0 && it + 1 < nb && mid < TB) {   // solve: a thread a column
+                Stage<DK, PARTS> &s = stages[(it + 1) & 3];
+                float x[TB];
 #pragma unroll
-        for (int o = 1; o < TB; o <<= 1) {
-            after += __shfl_down_sync(0xffffffffu, after, o);
-            const float x = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += x;
+                for (int i = 0; i < TB; ++i) x[i] = i == mid ? 1.f : 0.f;
+#pragma unroll
+                for (int j = 0; j < TB - 1; ++j)
+#pragma unroll
+                    for (int i = j + 1; i < TB; ++i) {
+                        const float y = fmaf(-s.a[i][j], x[j], x[i]);
+                        x[i] = j >= mid ? y : x[i];   // (a NaN stays behind its token)
+                    }
+                const float beta = s.beta[mid];
+#pragma unroll
+                for (int i = 0; i < TB; ++i) s.m[i][mid] = x[i] * beta;
+            }
+            if (it + 3 < nb) {   // stage
+                Stage<DK, PARTS> &s = stages[(it + 3) & 3];
+                Rows<DK> &f = rows[(it + 1) & 1];
+#pragma unroll
+                for (int u = 0; u < KU; ++u) {
+                    const int x = mid + u * MT, t = x / (DK / 4), i = x % (DK / 4) * 4;
+                    put(s.k, f.k, t, i, nk[u]);
+                    put(s.q, f.q, t, i, nq[u]);
+                }
+                *reinterpret_cast<float4 *>(&s.v[mid / (COLS / 4)][mid % (COLS / 4) * 4]) = widen(nv);
+                if (warp == kChain + 1) {   // (lanes from TB on hold 0, the sums that reach past the block stay in it)
+                    float after = ng, before = ng;
+#pragma unroll
+                    for (int o = 1; o < TB; o <<= 1) {
+                        after += __shfl_down_sync(0xffffffffu, after, o);
+                        const float x = __shfl_up_sync(0xffffffffu, before, o);
+                        if (lane >= o) before += x;
+                    }
+                    const float left = __shfl_down_sync(0xffffffffu, after, 1);
+                    if (lane < TB) {
+                        s.g[lane] = ng;
+                        s.beta[lane] = nbeta;
+                        s.pre[lane] = expf(before);
+                        s.suf[lane] = expf(left);   // (of the last: of nothing)
+                    }
+                    if (lane == 0) {
+                        const bool near = after > -0.25f;
+                        s.all = near ? expm1f(after) : expf(after);
+                        s.near = near ? 1.f : 0.f;
+                    }
+                }
+                if (it + 4 < nb) fetch(it + 4);
+            }
+            __syncthreads();
         }
-        const float rest = __shfl_down_sync(0xffffffffu, after, 1);
-        if (lane < TB) {
-            to.g[lane] = ng;
-            to.beta[lane] = nb;
-            to.pre[lane] = expf(before);
-            to.suf[lane] = expf(rest);   // (of the last: of nothing)
-        }
-        if (lane == 0) {
-            const bool near = after > -0.25f;
-            to.all = near ? expm1f(after) : expf(after);
-            to.one = near ? 1.f : 0.f;
-        }
-    };
-    int cur = 0;
-    if (b < e) {
-        fetch(b);
-        if (warp == DEC) decays(sd[0]);
+        return;
     }
-    for (long long tb = b; tb < e; tb += TB, cur ^= 1) {
-        const int n = (int)min((long long)TB, e - tb);
+    // the chain: the state's transpose as the accumulators of [16 columns x 8 channels] products
+    constexpr int NT = DK / 8;
+    const int x = lane >> 2, y = lane & 3, t0 = 2 * y, wc = 16 * warp, col = cb + wc + x;
+    const bool busy = cb + wc < p.dv;
+    const long long own = ((long long)seq * p.H + h) * p.dk * p.dv;
+    float st[NT][4];
 #pragma unroll
-        for (int u = 0; u < KU; ++u) {
-            const int x = tid + u * THREADS;
-            if (x < KUNITS) {
-                *reinterpret_cast<float4 *>(&sk[x / (DK / 4)][x % (DK / 4) * 4]) = widen(nk[u]);
-                *reinterpret_cast<float4 *>(&sq[x / (DK / 4)][x % (DK / 4) * 4]) = widen(nq[u]);
-            }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ch = 8 * n + t0 + (i & 1), c = col + 8 * (i >> 1);
+            st[n][i] = p.init && ch < p.dk && c < p.dv ? p.init[own + (long long)ch * p.dv + c] : 0.f;
         }
-        if (tid < VUNITS) *reinterpret_cast<float4 *>(&sv[0][0] + 4 * tid) = widen(nv);
-        const Decays &d = sd[cur];
-        __syncthreads();
-        if (tb + TB < e) fetch(tb + TB);
-        if (tid < TB * TB * SUB) {   // scores
-            const int i = tid / SUB / TB, j = tid / SUB % TB;
-            float kk = 0.f, qk = 0.f;
-#pragma unroll 4
-            for (int x = tid % SUB * 4; x < DK; x += 4 * SUB) {
-                const float4 a = *reinterpret_cast<const float4 *>(&sk[j][x]);
-                const float4 c = *reinterpret_cast<const float4 *>(&sk[i][x]);
-                const float4 f = *reinterpret_cast<const float4 *>(&sq[i][x]);
-                kk += a.x * c.x + a.y * c.y + a.z * c.z + a.w * c.w;
-                qk += a.x * f.x + a.y * f.y + a.z * f.z + a.w * f.w;
-            }
+    // a lane's row of the four tiles that it addresses
+    const uint32_t tile = (lane & 7) * PITCH + (lane >> 3) * 16;
+    for (int it = first; it < nb; ++it) {
+        if (it >= 0 && busy) {
+            const Stage<DK, PARTS> &s = stages[it & 3];
+            const long long tb = b + (long long)it * TB;
+            const uint32_t ak = ptx::smem_u32(&s.k[0][0][0]) + tile, aq = ptx::smem_u32(&s.q[0][0][0]) + tile;
+            float xk[3][4] = {}, xq[3][4] = {};       // S^T k, S^T q: the large, the middle and the small products
 #pragma unroll
-            for (int o = SUB / 2; o > 0; o >>= 1) {
-                kk += __shfl_xor_sync(0xffffffffu, kk, o);
-                qk += __shfl_xor_sync(0xffffffffu, qk, o);
-            }
-            float w = 0.f;
+            for (int c = 0; c < DK / 32; ++c) {
+                uint32_t kb[PARTS][4], qb[PARTS][4];
 #pragma unroll
-            for (int l = 1; l < TB; ++l) w += l > j && l <= i ? d.g[l] : 0.f;
-            w = expf(w);
-            if (tid % SUB == 0) {
-                sa[i][j] = d.beta[i] * w * kk;
-                sp[i][j] = w * qk;
-            }
-        }
-#pragma unroll 4
-        for (int t = 0; t < TB; ++t) {   // S^T k, S^T q over the warp's channels
-            float ak[CPL] = {}, aq[CPL] = {};
+                for (int a = 0; a < PARTS; ++a) {
+                    tiles(kb[a], ak + a * TB * PITCH + 64 * c);
+                    tiles(qb[a], aq + a * TB * PITCH + 64 * c);
+                }
 #pragma unroll
-            for (int r = 0; r < kRows; r += 4) {
-                const float4 kr = *reinterpret_cast<const float4 *>(&sk[t][warp * kRows + r]);
-                const float4 qr = *reinterpret_cast<const float4 *>(&sq[t][warp * kRows + r]);
+                for (int o = 0; o < 4; o += 2) {
+                    uint32_t f[3][4];
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) {
-                    ak[c] = fmaf(st[r + 3][c], kr.w, fmaf(st[r + 2][c], kr.z, fmaf(st[r + 1][c], kr.y, fmaf(st[r][c], kr.x, ak[c]))));
-                    aq[c] = fmaf(st[r + 3][c], qr.w, fmaf(st[r + 2][c], qr.z, fmaf(st[r + 1][c], qr.y, fmaf(st[r][c], qr.x, aq[c]))));
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = 4 * c + o + (i >> 1), r = 2 * (i & 1);
+                        split(st[n][r], st[n][r + 1], f[0][i], f[1][i], f[2][i]);
+                    }
+                    auto go = [&](float (&to)[3][4], const uint32_t (&w)[PARTS][4]) {
+                        auto one = [&](float (&d)[4], int a, int z) { mma(d, f[a][0], f[a][1], f[a][2], f[a][3], w[z][o], w[z][o + 1]); };
+                        one(to[0], 0, 0);
+                        one(to[1], 1, 0);
+                        one(to[2], 2, 0);
+                        if constexpr (PARTS == 3) {
+                            one(to[1], 0, 1);
+                            one(to[2], 1, 1);
+                            one(to[2], 0, 2);
+                        }
+                    };
+                    go(xk, kb);
+                    go(xq, qb);
                 }
             }
+            const float pre[2] = {s.pre[t0], s.pre[t0 + 1]}, suf[2] = {s.suf[t0], s.suf[t0 + 1]};
+            float r[4], u[4] = {}, small[4] = {}, out[4], low[4] = {};
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-                part(0, t, warp)[lane + 32 * c] = ak[c];
-                part(1, t, warp)[lane + 32 * c] = aq[c];
+            for (int i = 0; i < 4; ++i) {
+                r[i] = fmaf(-pre[i & 1], xk[0][i] + (xk[1][i] + xk[2][i]), s.v[t0 + (i & 1)][wc + x + 8 * (i >> 1)]);
+                out[i] = pre[i & 1] * (xq[0][i] + (xq[1][i] + xq[2][i]));
             }
-        }
-        __syncthreads();
+            uint32_t f[3][2], w[3];
+            split(s.m[x][t0], s.m[x][t0 + 1], w[0], w[1], w[2]);
 #pragma unroll
-        for (int x0 = 0; x0 < 2 * TB * kCols; x0 += THREADS) {   // over all of them: R, and what outputs take from S
-            const int x = x0 + tid, t = x / kCols % TB, c = x % kCols, which = x / (TB * kCols);
-            if (x >= 2 * TB * kCols) break;
-            float *from = part(which, t, 0) + c, sum = 0.f;
+            for (int i = 0; i < 2; ++i) split(r[2 * i], r[2 * i + 1], f[0][i], f[1][i], f[2][i]);
+            mma_tokens(u, small, f, w);
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) sum += from[w * kCols];
-            from[0] = which ? d.pre[t] * sum : d.beta[t] * fmaf(-d.pre[t], sum, sv[t][c]);
-        }
-        __syncthreads();
-        if (tid < kCols) {   // a column's substitution
-            float u[TB];
+            for (int i = 0; i < 4; ++i) u[i] += small[i];
+            uint32_t d[3][2];                         // the new values as the state takes them
 #pragma unroll
-            for (int i = 0; i < TB; ++i) u[i] = part(0, i, 0)[tid];
+            for (int i = 0; i < 2; ++i) split(suf[0] * u[2 * i], suf[1] * u[2 * i + 1], d[0][i], d[1][i], d[2][i]);
+            const float all = s.all, near = s.near;
 #pragma unroll
-            for (int j = 0; j < TB; ++j)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = j + 1; i < TB; ++i) u[i] = fmaf(-sa[i][j], u[j], u[i]);
+                for (int i = 0; i < 4; ++i) st[n][i] = fmaf(st[n][i], all, st[n][i] * near);
 #pragma unroll
-            for (int i = 0; i < TB; ++i) su[i][tid] = u[i];
-        }
-        if (warp == DEC && tb + TB < e) decays(sd[cur ^ 1]);
-        __syncthreads();
-        for (int x = tid; x < n * kCols; x += THREADS) {
-            const int i = x / kCols, c = x % kCols;
-            float o = part(1, i, 0)[c];
+            for (int c = 0; c < DK / 32; ++c) {
+                uint32_t kb[PARTS][4];
 #pragma unroll
-            for (int j = 0; j < TB; ++j)
-                if (j <= i) o = fmaf(sp[i][j], su[j][c], o);
-            if (cb + c < p.dv) store_as(static_cast<TO *>(p.out) + ((tb + i) * p.H + h) * p.dv + cb + c, o * p.scale);
-        }
-        const float all = d.all, one = d.one;
+                for (int a = 0; a < PARTS; ++a) tiles_trans(kb[a], ak + a * TB * PITCH + 64 * c);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
+                for (int n = 0; n < 4; ++n) mma(st[4 * c + n], d[0][0], d[0][1], d[1][0], d[1][1], kb[0][n], kb[0][n]);
+                if constexpr (PARTS == 3) {
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) st[r][c] = fmaf(st[r][c], all, st[r][c] * one);
-#pragma unroll 4
-        for (int t = 0; t < TB; ++t) {
-            const float f = d.suf[t];
-            float u[CPL];
+                    for (int n = 0; n < 4; ++n) mma(st[4 * c + n], d[0][0], d[0][1], d[1][0], d[1][1], kb[1][n], kb[1][n]);
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) u[c] = f * su[t][lane + 32 * c];
+                    for (int n = 0; n < 4; ++n) mma(st[4 * c + n], d[0][0], d[0][1], d[2][0], d[2][1], kb[2][n], kb[0][n]);
+                } else {
 #pragma unroll
-            for (int r = 0; r < kRows; r += 4) {
-                const float4 kr = *reinterpret_cast<const float4 *>(&sk[t][warp * kRows + r]);
-#pragma unroll
-                for (int c = 0; c < CPL; ++c) {
-                    st[r][c] = fmaf(kr.x, u[c], st[r][c]);
-                    st[r + 1][c] = fmaf(kr.y, u[c], st[r + 1][c]);
-                    st[r + 2][c] = fmaf(kr.z, u[c], st[r + 2][c]);
-                    st[r + 3][c] = fmaf(kr.w, u[c], st[r + 3][c]);
+                    for (int n = 0; n < 4; ++n) mma(st[4 * c + n], d[2][0], d[2][1], 0u, 0u, kb[0][n], 0u);
                 }
+            }
+            split(s.p[x][t0], s.p[x][t0 + 1], w[0], w[1], w[2]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) split(u[2 * i], u[2 * i + 1], f[0][i], f[1][i], f[2][i]);
+            mma_tokens(out, low, f, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long t = tb + t0 + (i & 1);
+                const int c = col + 8 * (i >> 1);
+                if (t < e && c < p.dv) store_as(static_cast<TO *>(p.out) + (t * p.H + h) * p.dv + c, (out[i] + low[i]) * p.scale);
             }
         }
         __syncthreads();
     }
     if (p.final_state) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-                const int i = warp * kRows + r;
-                if (i < p.dk && col + 32 * c < p.dv) p.final_state[own + (long long)i * p.dv + col + 32 * c] = st[r][c];
+            for (int i = 0; i < 4; ++i) {
+                const int ch = 8 * n + t0 + (i & 1), c = col + 8 * (i >> 1);
+                if (ch < p.dk && c < p.dv) p.final_state[own + (long long)ch * p.dv + c] = st[n][i];
             }
     }
 }
 
-template <typename T, typename TO, int WARPS, int CPL>
-int launch_cols(const Args &p, cudaStream_t stream)
+template <typename T, typename TO, int DK>
+int launch_size(const Args &p, cudaStream_t stream)
 {
-    constexpr int bytes = 2 * kTokens<WARPS> * WARPS * 32 * CPL * 4;
+    constexpr int bytes = 4 * sizeof(Stage<DK, sizeof(T) == 4 ? 3 : 1>) + 2 * sizeof(Rows<DK>);
     // a function attribute belongs to the current device: set it on every launch
-    if (cudaFuncSetAttribute(delta_token_kernel<T, TO, WARPS, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(delta_token_kernel<T, TO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return KDA_ERR_CUDA;
-    const dim3 grid((unsigned)(p.n_seqs * p.H), (unsigned)ceil_div(p.dv, 32 * CPL));
-    delta_token_kernel<T, TO, WARPS, CPL><<<grid, 32 * WARPS, bytes, stream>>>(p);
+    const dim3 grid((unsigned)(p.n_seqs * p.H), (unsigned)ceil_div(p.dv, COLS));
+    delta_token_kernel<T, TO, DK><<<grid, 32 * (kChain + kMakers), bytes, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
-}
-
-template <typename T, typename TO, int WARPS>
-int launch_warps(const Args &p, cudaStream_t stream)
-{
-    // 32 columns a block where 64 would leave SMs idle
-    if ((long long)p.n_seqs * p.H * ceil_div(p.dv, 64) < 152) return launch_cols<T, TO, WARPS, 1>(p, stream);
-    return launch_cols<T, TO, WARPS, 2>(p, stream);
 }
 
 template <typename T, typename TO>
 int launch(const Args &p, cudaStream_t stream)
 {
-    if (p.dk <= 64) return launch_warps<T, TO, 8>(p, stream);
-    if (p.dk <= 128) return launch_warps<T, TO, 16>(p, stream);
-    return launch_warps<T, TO, 32>(p, stream);
+    if (p.dk <= 64) return launch_size<T, TO, 64>(p, stream);
+    if (p.dk <= 128) return launch_size<T, TO, 128>(p, stream);
+    return launch_size<T, TO, 256>(p, stream);
 }
 
 }  // namespace

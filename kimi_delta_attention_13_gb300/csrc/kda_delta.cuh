@@ -49,6 +49,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b)
     return v;
 }
 
+// Values in three bf16 parts, x = hi - mid + lo, all 24 bits: what a rounding leaves is its result less the value,
+// which takes a half of a packed pair as it is (unpacked, a part of a pair cost four instructions on the ALU,
+// which was the chain's busiest pipe, in place of one).
+__device__ __forceinline__ void rest(uint32_t h, float2 &x)   // x = h - x
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tsub.rn.f32.bf16 %0, a, %0;\n\tsub.rn.f32.bf16 %1, b, %1;\n\t}"
+        : "+f"(x.x), "+f"(x.y) : "r"(h));
+}
+
 int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream);
 int run_tc_path(const Args &p, int out_dtype, cudaStream_t stream);   // bf16 operands, d <= 128
 

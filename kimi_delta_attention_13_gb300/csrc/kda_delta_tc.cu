@@ -139,15 +139,6 @@ __device__ __forceinline__ void arrive(Shared *sh, int bar, int lane)
     if (lane == 0) mbar_arrive(&sh->bars[bar]);
 }
 
-// Values in three bf16 parts, x = hi - mid + lo, all 24 bits: what a rounding leaves is its result less the value,
-// which takes a half of a packed pair as it is (unpacked, a part of a pair cost four instructions on the ALU,
-// which was the chain's busiest pipe, in place of one).
-__device__ __forceinline__ void rest(uint32_t h, float2 &x)   // x = h - x
-{
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tsub.rn.f32.bf16 %0, a, %0;\n\tsub.rn.f32.bf16 %1, b, %1;\n\t}"
-        : "+f"(x.x), "+f"(x.y) : "r"(h));
-}
-
 // stage by stage, since a pair's own operations wait for one another; `two`: the hi parts, then the mid parts
 template <int N>
 __device__ __forceinline__ void split3(float2 (&y)[N], uint32_t (&two)[2 * N], uint32_t (&lo)[N])
