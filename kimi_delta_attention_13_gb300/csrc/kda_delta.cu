@@ -37,6 +37,18 @@ constexpr int TB = 8;        // tokens at a time
 constexpr int kChain = 4;    // warps that hold the state, 16 value columns each
 constexpr int kMakers = 4;   // warps that make what does not depend on it
 constexpr int COLS = 16 * kChain;
+constexpr int kThreads = 32 * (kChain + kMakers + 4);   // and a warpgroup of which one warp works: decays and solves
+
+// Registers a thread: at launch, then of each warpgroup (their sum may not pass the block's)
+template <int DK>
+constexpr int kRegs[4] = {DK == 64 ? 80 : 168, DK == 64 ? 144 : 240, DK == 64 ? 56 : 160, DK == 64 ? 40 : 104};
+static_assert(kRegs<64>[1] + kRegs<64>[2] + kRegs<64>[3] <= 3 * kRegs<64>[0] && kRegs<128>[1] + kRegs<128>[2] + kRegs<128>[3] <= 3 * kRegs<128>[0], "");
+template <int LAUNCH, int N>
+__device__ __forceinline__ void set_regs()
+{
+    if constexpr (N > LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // what a block of tokens is worked from: staged, scored, solved and used in four periods
 template <int DK, int PARTS>
@@ -44,7 +56,8 @@ struct __align__(16) Stage {
     uint16_t k[PARTS][TB][DK + 8], q[PARTS][TB][DK + 8];   // bf16 parts (rows padded against bank conflicts)
     float v[TB][COLS + 4];
     float a[TB][12], m[TB][12], p[TB][12];     // beta w (k . k);  (I + a)^-1 diag(beta);  w (q . k)
-    float g[TB], beta[TB], pre[TB], suf[TB];   // log decays, beta, e^G, e^(G_last - G)
+    float w[TB][TB];                           // for j <= i
+    float beta[TB], pre[TB], suf[TB];          // beta, e^G, e^(G_last - G)
     float all, near, unused[2];                // the whole block's decay, less 1 where it is near 1
 };
 template <int DK>
@@ -93,7 +106,7 @@ __device__ __forceinline__ void mma_tokens(float (&c)[4], float (&small)[4], con
 }
 
 template <typename T, typename TO, int DK>
-__global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(const Args p)
+__global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel(const Args p)
 {
     constexpr int PARTS = sizeof(T) == 4 ? 3 : 1, MT = 32 * kMakers;
     constexpr int KU = TB * DK / 4 / MT, PITCH = (DK + 8) * 2;
@@ -108,29 +121,30 @@ __global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(co
     const int cb = blockIdx.y * COLS;
     long long b, e;
     bounds(p, seq, b, e);
-    const int nb = (int)((e - b + TB - 1) / TB), first = nb ? -3 : 0;
-    if (warp >= kChain) {
+    const int len = (int)(e - b), nb = len / TB + (len % TB != 0), first = nb ? -3 : 0;
+    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * (kChain + kMakers + 2)) : "memory"); };
+    if (warp >= kChain && warp < kChain + kMakers) {
+        set_regs<kRegs<DK>[0], kRegs<DK>[2]>();
         const int mid = tid - 32 * kChain;
         const T *q = static_cast<const T *>(p.q), *k = static_cast<const T *>(p.k), *v = static_cast<const T *>(p.v);
         Four nk[KU], nq[KU], nv;
-        float ng = 0.f, nbeta = 0.f;
-        auto fetch = [&](int m) {   // block m into registers (tokens past the end neither decay nor write)
-            const long long tb = b + (long long)m * TB;
+        // a thread's places: units of four channels of k and q, STEP tokens apart, and one of v
+        constexpr int STEP = MT / (DK / 4);
+        const int kt = mid / (DK / 4), ki = mid % (DK / 4) * 4, vt = mid / (COLS / 4), vi = mid % (COLS / 4) * 4;
+        const bool kin = ki < p.dk, vin = cb + vi < p.dv;
+        const long long krow = (long long)Hk * p.dk, vrow = (long long)p.H * p.dv;
+        long long ko = (b + kt) * krow + (long long)hk * p.dk + ki, vo = (b + vt) * vrow + (long long)h * p.dv + cb + vi;
+        auto fetch = [&](int left) {   // the next block into registers; `left` tokens are
             const Four zero = {};
 #pragma unroll
             for (int u = 0; u < KU; ++u) {
-                const int x = mid + u * MT, t = x / (DK / 4), i = x % (DK / 4) * 4;
-                const bool ok = tb + t < e && i < p.dk;
-                nk[u] = ok ? load4(k + ((tb + t) * Hk + hk) * p.dk + i) : zero;
-                nq[u] = ok ? load4(q + ((tb + t) * Hk + hk) * p.dk + i) : zero;
+                const bool ok = kin && kt + u * STEP < left;
+                nk[u] = ok ? load4(k + ko + u * STEP * krow) : zero;
+                nq[u] = ok ? load4(q + ko + u * STEP * krow) : zero;
             }
-            const int t = mid / (COLS / 4), c = cb + mid % (COLS / 4) * 4;
-            nv = tb + t < e && c < p.dv ? load4(v + ((tb + t) * p.H + h) * p.dv + c) : zero;
-            if (warp == kChain + 1 && lane < TB) {
-                const bool ok = tb + lane < e;
-                ng = ok ? p.g[p.g_per_token ? (tb + lane) * p.H + h : h] : 0.f;
-                nbeta = ok ? p.beta[(tb + lane) * p.H + h] : 0.f;
-            }
+            nv = vin && vt < left ? load4(v + vo) : zero;
+            ko += TB * krow;
+            vo += TB * vrow;
         };
         auto put = [&](uint16_t (&to)[PARTS][TB][DK + 8], float (&wide)[TB][DK + 4], int t, int i, Four x) {
             const float4 f = widen(x);
@@ -146,16 +160,13 @@ __global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(co
                 *reinterpret_cast<uint2 *>(&to[0][t][i]) = x;
             }
         };
-        if (nb) fetch(0);
+        const int si = mid / SUB / TB, sj = mid / SUB % TB;
+        if (nb) fetch(len);
         for (int it = first; it < nb; ++it) {
             if (it + 2 >= 0 && it + 2 < nb) {   // score
                 Stage<DK, PARTS> &s = stages[(it + 2) & 3];
                 const Rows<DK> &f = rows[it & 1];
-                const int i = mid / SUB / TB, j = mid / SUB % TB;
-                float w = 0.f;
-#pragma unroll
-                for (int l = 1; l < TB; ++l) w += l > j && l <= i ? s.g[l] : 0.f;
-                w = expf(w);
+                const int i = si, j = sj;
                 float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), q4 = k4;
 #pragma unroll 8
                 for (int x = mid % SUB * 4; x < DK; x += 4 * SUB) {
@@ -172,63 +183,103 @@ __global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(co
                     qk += __shfl_xor_sync(0xffffffffu, qk, o);
                 }
                 if (mid % SUB == 0) {
+                    const float w = s.w[i][j];
                     s.a[i][j] = s.beta[i] * w * kk;
                     s.p[i][j] = j <= i ? w * qk : 0.f;
                 }
-            }
-            if (it + 1 >= 0 && it + 1 < nb && mid < TB) {   // solve: a thread a column
-                Stage<DK, PARTS> &s = stages[(it + 1) & 3];
-                float x[TB];
-#pragma unroll
-                for (int i = 0; i < TB; ++i) x[i] = i == mid ? 1.f : 0.f;
-#pragma unroll
-                for (int j = 0; j < TB - 1; ++j)
-#pragma unroll
-                    for (int i = j + 1; i < TB; ++i) {
-                        const float y = fmaf(-s.a[i][j], x[j], x[i]);
-                        x[i] = j >= mid ? y : x[i];   // (a NaN stays behind its token)
-                    }
-                const float beta = s.beta[mid];
-#pragma unroll
-                for (int i = 0; i < TB; ++i) s.m[i][mid] = x[i] * beta;
             }
             if (it + 3 < nb) {   // stage
                 Stage<DK, PARTS> &s = stages[(it + 3) & 3];
                 Rows<DK> &f = rows[(it + 1) & 1];
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
-                    const int x = mid + u * MT, t = x / (DK / 4), i = x % (DK / 4) * 4;
-                    put(s.k, f.k, t, i, nk[u]);
-                    put(s.q, f.q, t, i, nq[u]);
+                    put(s.k, f.k, kt + u * STEP, ki, nk[u]);
+                    put(s.q, f.q, kt + u * STEP, ki, nq[u]);
                 }
-                *reinterpret_cast<float4 *>(&s.v[mid / (COLS / 4)][mid % (COLS / 4) * 4]) = widen(nv);
-                if (warp == kChain + 1) {   // (lanes from TB on hold 0, the sums that reach past the block stay in it)
-                    float after = ng, before = ng;
-#pragma unroll
-                    for (int o = 1; o < TB; o <<= 1) {
-                        after += __shfl_down_sync(0xffffffffu, after, o);
-                        const float x = __shfl_up_sync(0xffffffffu, before, o);
-                        if (lane >= o) before += x;
-                    }
-                    const float left = __shfl_down_sync(0xffffffffu, after, 1);
-                    if (lane < TB) {
-                        s.g[lane] = ng;
-                        s.beta[lane] = nbeta;
-                        s.pre[lane] = expf(before);
-                        s.suf[lane] = expf(left);   // (of the last: of nothing)
-                    }
-                    if (lane == 0) {
-                        const bool near = after > -0.25f;
-                        s.all = near ? expm1f(after) : expf(after);
-                        s.near = near ? 1.f : 0.f;
-                    }
-                }
-                if (it + 4 < nb) fetch(it + 4);
+                *reinterpret_cast<float4 *>(&s.v[vt][vi]) = widen(nv);
+                if (it + 4 < nb) fetch(len - (it + 4) * TB);
             }
-            __syncthreads();
+            meet();
         }
         return;
     }
+    if (warp >= kChain) {                             // decays and solves
+        set_regs<kRegs<DK>[0], kRegs<DK>[3]>();
+        if (warp > kChain + kMakers + 1) return;
+        if (warp == kChain + kMakers) {
+            for (int it = first; it < nb; ++it) {
+                if (it + 1 >= 0 && it + 1 < nb && lane < TB) {   // solve: a thread a column
+                    Stage<DK, PARTS> &s = stages[(it + 1) & 3];
+                    float x[TB];
+#pragma unroll
+                    for (int i = 0; i < TB; ++i) x[i] = i == lane ? 1.f : 0.f;
+#pragma unroll
+                    for (int j = 0; j < TB - 1; ++j)
+#pragma unroll
+                        for (int i = j + 1; i < TB; ++i) {
+                            const float y = fmaf(-s.a[i][j], x[j], x[i]);
+                            x[i] = j >= lane ? y : x[i];   // (a NaN stays behind its token)
+                        }
+                    const float beta = s.beta[lane];
+#pragma unroll
+                    for (int i = 0; i < TB; ++i) s.m[i][lane] = x[i] * beta;
+                }
+                meet();
+            }
+            return;
+        }
+        float ng = 0.f, nbeta = 0.f;                  // of tokens past the end: they neither decay nor write
+        long long at = (b + lane) * p.H + h;
+        int pi = 1, pj = lane;                        // a lane's pair of tokens, the later first
+#pragma unroll
+        for (int i = 1; i < TB; ++i)
+            if (pj >= pi) {
+                pj -= pi;
+                ++pi;
+            }
+        auto fetch = [&](int left) {
+            const bool ok = lane < TB && lane < left;
+            ng = ok ? p.g[p.g_per_token ? at : h] : 0.f;
+            nbeta = ok ? p.beta[at] : 0.f;
+            at += (long long)TB * p.H;
+        };
+        if (nb) fetch(len);
+        for (int it = first; it < nb; ++it) {
+            if (it + 3 < nb) {   // (lanes from TB on hold 0, the sums that reach past the block stay in it)
+                Stage<DK, PARTS> &s = stages[(it + 3) & 3];
+                float after = ng, before = ng;
+#pragma unroll
+                for (int o = 1; o < TB; o <<= 1) {
+                    after += __shfl_down_sync(0xffffffffu, after, o);
+                    const float x = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o) before += x;
+                }
+                const float left = __shfl_down_sync(0xffffffffu, after, 1);
+                if (lane < TB) {
+                    s.beta[lane] = nbeta;
+                    s.pre[lane] = expf(before);
+                    s.suf[lane] = expf(left);   // (of the last: of nothing)
+                }
+                if (lane < TB) s.w[lane][lane] = 1.f;
+                float sum = 0.f;                      // of the log decays between a pair's tokens
+#pragma unroll
+                for (int l = 1; l < TB; ++l) {
+                    const float gl = __shfl_sync(0xffffffffu, ng, l);
+                    sum += l > pj && l <= pi ? gl : 0.f;
+                }
+                if (lane < TB * (TB - 1) / 2) s.w[pi][pj] = expf(sum);
+                if (lane == 0) {
+                    const bool near = after > -0.25f;
+                    s.all = near ? expm1f(after) : expf(after);
+                    s.near = near ? 1.f : 0.f;
+                }
+                if (it + 4 < nb) fetch(len - (it + 4) * TB);
+            }
+            meet();
+        }
+        return;
+    }
+    set_regs<kRegs<DK>[0], kRegs<DK>[1]>();
     // the chain: the state's transpose as the accumulators of [16 columns x 8 channels] products
     constexpr int NT = DK / 8;
     const int x = lane >> 2, y = lane & 3, t0 = 2 * y, wc = 16 * warp, col = cb + wc + x;
@@ -242,12 +293,14 @@ __global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(co
             const int ch = 8 * n + t0 + (i & 1), c = col + 8 * (i >> 1);
             st[n][i] = p.init && ch < p.dk && c < p.dv ? p.init[own + (long long)ch * p.dv + c] : 0.f;
         }
+    const long long orow = (long long)p.H * p.dv;
+    long long oo = (b + t0) * orow + (long long)h * p.dv + col;
     // a lane's row of the four tiles that it addresses
     const uint32_t tile = (lane & 7) * PITCH + (lane >> 3) * 16;
     for (int it = first; it < nb; ++it) {
         if (it >= 0 && busy) {
             const Stage<DK, PARTS> &s = stages[it & 3];
-            const long long tb = b + (long long)it * TB;
+            const int left = len - it * TB;
             const uint32_t ak = ptx::smem_u32(&s.k[0][0][0]) + tile, aq = ptx::smem_u32(&s.q[0][0][0]) + tile;
             float xk[3][4] = {}, xq[3][4] = {};       // S^T k, S^T q: the large, the middle and the small products
 #pragma unroll
@@ -266,19 +319,19 @@ __global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(co
                         const int n = 4 * c + o + (i >> 1), r = 2 * (i & 1);
                         split(st[n][r], st[n][r + 1], f[0][i], f[1][i], f[2][i]);
                     }
-                    auto go = [&](float (&to)[3][4], const uint32_t (&w)[PARTS][4]) {
-                        auto one = [&](float (&d)[4], int a, int z) { mma(d, f[a][0], f[a][1], f[a][2], f[a][3], w[z][o], w[z][o + 1]); };
-                        one(to[0], 0, 0);
-                        one(to[1], 1, 0);
-                        one(to[2], 2, 0);
-                        if constexpr (PARTS == 3) {
-                            one(to[1], 0, 1);
-                            one(to[2], 1, 1);
-                            one(to[2], 0, 2);
-                        }
+                    // (k's and q's in turn, so that a sum's next product is six away)
+                    auto both = [&](int to, int a, int z) {
+                        mma(xk[to], f[a][0], f[a][1], f[a][2], f[a][3], kb[z][o], kb[z][o + 1]);
+                        mma(xq[to], f[a][0], f[a][1], f[a][2], f[a][3], qb[z][o], qb[z][o + 1]);
                     };
-                    go(xk, kb);
-                    go(xq, qb);
+                    both(0, 0, 0);
+                    both(1, 1, 0);
+                    both(2, 2, 0);
+                    if constexpr (PARTS == 3) {
+                        both(1, 0, 1);
+                        both(2, 1, 1);
+                        both(0, 0, 2);
+                    }
                 }
             }
             const float pre[2] = {s.pre[t0], s.pre[t0 + 1]}, suf[2] = {s.suf[t0], s.suf[t0 + 1]};
@@ -298,11 +351,18 @@ __global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(co
             uint32_t d[3][2];                         // the new values as the state takes them
 #pragma unroll
             for (int i = 0; i < 2; ++i) split(suf[0] * u[2 * i], suf[1] * u[2 * i + 1], d[0][i], d[1][i], d[2][i]);
-            const float all = s.all, near = s.near;
+            const float all = s.all;
+            if (s.near != 0.f) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) st[n][i] = fmaf(st[n][i], all, st[n][i] * near);
+                    for (int i = 0; i < 4; ++i) st[n][i] = fmaf(st[n][i], all, st[n][i]);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) st[n][i] *= all;
+            }
 #pragma unroll
             for (int c = 0; c < DK / 32; ++c) {
                 uint32_t kb[PARTS][4];
@@ -325,13 +385,12 @@ __global__ void __launch_bounds__(32 * (kChain + kMakers)) delta_token_kernel(co
             for (int i = 0; i < 2; ++i) split(u[2 * i], u[2 * i + 1], f[0][i], f[1][i], f[2][i]);
             mma_tokens(out, low, f, w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const long long t = tb + t0 + (i & 1);
-                const int c = col + 8 * (i >> 1);
-                if (t < e && c < p.dv) store_as(static_cast<TO *>(p.out) + (t * p.H + h) * p.dv + c, (out[i] + low[i]) * p.scale);
-            }
+            for (int i = 0; i < 4; ++i)
+                if (t0 + (i & 1) < left && col + 8 * (i >> 1) < p.dv)
+                    store_as(static_cast<TO *>(p.out) + oo + (i & 1) * orow + 8 * (i >> 1), (out[i] + low[i]) * p.scale);
+            oo += TB * orow;
         }
-        __syncthreads();
+        meet();
     }
     if (p.final_state) {
 #pragma unroll
@@ -352,7 +411,7 @@ int launch_size(const Args &p, cudaStream_t stream)
     if (cudaFuncSetAttribute(delta_token_kernel<T, TO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return KDA_ERR_CUDA;
     const dim3 grid((unsigned)(p.n_seqs * p.H), (unsigned)ceil_div(p.dv, COLS));
-    delta_token_kernel<T, TO, DK><<<grid, 32 * (kChain + kMakers), bytes, stream>>>(p);
+    delta_token_kernel<T, TO, DK><<<grid, kThreads, bytes, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
