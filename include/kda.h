@@ -417,12 +417,12 @@ int kda_linear_decode(const void *q, const void *k, const void *v, const float *
  *   out               [total_tokens, H, d_v] `out_dtype`.  out and final_state (but for init_state) must
  *                     not alias an input or each other.
  * Head sizes: multiples of 8 from 8 to 256.
- * States, sums and decays are fp32.  bf16 inputs with head sizes up to 128 take the tensor-core kernel
- * (but for batches of a few tokens a sequence): chunks of 64 tokens, whose new values are good to fp32 (operands
+ * States, sums and decays are fp32.  bf16 inputs with head sizes up to 128 take the tcgen05 kernel
+ * (but for batches of short sequences): chunks of 64 tokens, whose new values are good to fp32 (operands
  * in three bf16 parts), and with them the states; what outputs sum is rounded once to bf16 where it is a
  * weighted score (each output is within 2^-8 of the sum of its terms' magnitudes, fp32 outputs too).  All else
- * is fp32 throughout, rounded once at the end.
- * The tensor-core kernel's waits are bounded (2e9 SM cycles, about 1 s): one that gave up shows as
+ * is good to fp32 throughout, rounded once at the end.
+ * The tcgen05 kernel's waits are bounded (2e9 SM cycles, about 1 s): one that gave up shows as
  * KDA_ERR_DEVICE_TIMEOUT in kda_device_status.  A NaN or infinity in an input of a sequence leaves the other
  * sequences as they are; within its own it may also reach outputs up to 63 tokens before it.
  * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED_SHAPE, KDA_ERR_MISALIGNED, KDA_ERR_CUDA.

@@ -1,22 +1,33 @@
-// kda_delta.cu -- the gated delta rule with one decay per head on CUDA cores: fp32 inputs and head sizes that the
-// tensor-core kernel does not take.
+// kda_delta.cu -- the gated delta rule with one decay per head for fp32 inputs, head sizes that kda_delta_tc.cu does
+// not take, and short sequences.
 //
 //     S' = exp(g_t) S_(t-1),   S_t = S' + beta_t k_t (v_t - S'^T k_t)^T,   o_t = scale S_t^T q_t
 //
-// A block owns 64 value columns of one (sequence, head), or 32: a thread holds 8 key channels x 2 columns (or 1) of
-// the state in registers, warp w the channels [8 w, 8 w + 8).  Eight tokens (i, j) are taken at a time (four where d_k is
-// over 128).  With w_ij = exp(g_(j+1) + .. + g_i), G_i = g_1 + .. + g_i and S the state before them,
-//     u_i = beta_i (v_i - e^(G_i) S^T k_i - sum_(j < i) w_ij (k_i . k_j) u_j)
+// Eight tokens (i, j) are taken at a time.  With w_ij = exp(g_(j+1) + .. + g_i), G_i = g_1 + .. + g_i, S the state before
+// them, A_ij = beta_i w_ij (k_i . k_j) for j < i and M = (I + A)^-1 diag(beta),
+//     U  = M R,   r_i = v_i - e^(G_i) S^T k_i
 //     o_i = scale (e^(G_i) S^T q_i + sum_(j <= i) w_ij (q_i . k_j) u_j)
 //     S  <- e^(G_8) S + sum_j k_j (e^(G_8 - G_j) u_j)^T
-// so that the sums over all key channels, which have to cross the warps, are taken for eight tokens at once, and
-// what follows token after token is a small substitution.  Products of decays are exponentials of their own sums
-// of log decays; the state's is taken as 1 + expm1 where it is near 1: rounded to fp32 itself, a decay that stays
-// the same would be off the same way block after block (over 256 tokens of memory 1e-6 of the state).
-// Bound by latency: a block of tokens is five steps with a barrier after each (staging, scores and the products with
-// the state, sums, substitution, outputs and update), some 3700 cycles for 64 x 32 of a state and 130 of FMA a
-// scheduler for the update.  2560 tokens in two sequences, 16 heads of 64 x 128: 0.50 ms (token by token, with
-// the sums folded inside a warp, 0.88; 64 columns a block 0.55).
+// Products of decays are exponentials of their own sums of log decays; the state's is taken as 1 + expm1 where it is near
+// 1: rounded to fp32 itself, a decay that stays the same would be off the same way block after block (over 256 tokens of
+// memory 1e-6 of the state).
+//
+// A block owns 64 value columns of one (sequence, head).  Four warps are the chain: a warp holds S^T for 16 columns in
+// registers, as the accumulators of [16 columns x 8 channels] products of mma.sync, whose layout is also that of
+// the operands which S^T k, S^T q, M R and the update take, so that nothing crosses lanes.  A factor is three bf16 parts
+// (two side by side along k where that is only eight tokens long); of the nine products of two factors the three smallest,
+// 2^-24 of the whole, are left out; a bf16 input is one part.  A warp's CUDA cores would take 768 cycles of FMA for
+// eight tokens of 16 columns x 64 channels, and each of their operands from shared memory: the 78 products take 640.
+// Four warps load three blocks ahead, make the parts and, two ahead, the scores; one warp makes the decays, and one M,
+// a thread a column, one block ahead.  A barrier of these ten warps ends a block.  Registers are moved to the chain.
+// (tcgen05's 64-token chunks, kda_delta_tc.cu, would need k and q in three parts in shared memory as well.)
+//
+// Bound by the chain's latency, one warp a scheduler: some 1,400 cycles of the 1,800 that a block of tokens takes, the
+// other warps' instructions between them.  2560 tokens in two sequences, 16 heads of 64 x 128, fp32: 233 us.  Before, on
+// CUDA cores with a barrier between the steps: 454; sums over lanes in place of shared memory: 372, bound by shared
+// memory's 128 bytes a cycle; all makers' work in four warps: 285; decays and M in one warp: 250; q's products behind the
+// new values, or outputs a block later: no gain.  2048 tokens of 96 heads of 128 x 128 0.80 ms (1.58 before), of 16 heads of
+// 256 x 256 in bf16 0.56 (1.20).
 #include "kda_delta.cuh"
 #include "sm100_ptx.cuh"
 
@@ -37,7 +48,7 @@ constexpr int TB = 8;        // tokens at a time
 constexpr int kChain = 4;    // warps that hold the state, 16 value columns each
 constexpr int kMakers = 4;   // warps that make what does not depend on it
 constexpr int COLS = 16 * kChain;
-constexpr int kThreads = 32 * (kChain + kMakers + 4);   // and a warpgroup of which one warp works: decays and solves
+constexpr int kThreads = 32 * (kChain + kMakers + 4);   // and a warpgroup of which two warps work: solves, decays
 
 // Registers a thread: at launch, then of each warpgroup (their sum may not pass the block's)
 template <int DK>
@@ -203,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel
         }
         return;
     }
-    if (warp >= kChain) {                             // decays and solves
+    if (warp >= kChain) {                             // solves, decays
         set_regs<kRegs<DK>[0], kRegs<DK>[3]>();
         if (warp > kChain + kMakers + 1) return;
         if (warp == kChain + kMakers) {
@@ -432,12 +443,13 @@ int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream)
     return out_dtype == KDA_BF16 ? launch<float, __nv_bfloat16>(p, stream) : launch<float, float>(p, stream);
 }
 
-// Whether the tensor-core kernel takes these operands: from a mean length on at which it is the faster (us, here and
-// there, with initial states: 32 heads of 128 x 128, one sequence of 16 tokens 7.6, 14.0, of 32 12.5, 13.6, of 64 22.6,
-// 12.8; 16 sequences of 8 36, 55, of 16 59, 55; 16 heads of 64 x 64, one of 64 16.2, 10.7, 16 of 32 15.8, 23.0).
+// Whether the kernel of kda_delta_tc.cu takes these operands: from a mean length on at which it is the faster (us, here
+// and there, with initial states.  128 x 128: 32 heads, one sequence of 32 tokens 9.1, 13.8, of 64 13.6, 13.0, 16 of 16 38,
+// 55, of 32 57, 55, of 64 91, 54; 96 heads, one of 32 16, 14, 16 of 32 176, 151.  64 x 64: 16 heads, one of 64 9.7, 11.1,
+// of 128 15.6, 14.4, 16 of 64 14, 22, of 128 23, 29; 64 heads, 64 sequences of 64 176, 289, 16 of 128 84, 100).
 bool tc_path(int n_seqs, int64_t T, int d_k, int d_v, int dtype)
 {
-    return dtype == KDA_BF16 && d_k <= 128 && d_v <= 128 && T >= (d_k <= 64 ? 48 : 16) * (int64_t)n_seqs;
+    return dtype == KDA_BF16 && d_k <= 128 && d_v <= 128 && T >= (d_k <= 64 ? 128 : 32) * (int64_t)n_seqs;
 }
 
 }  // namespace delta

@@ -4,6 +4,7 @@ import torch
 
 import kimi_delta_attention_13_gb300 as kda
 from delta_plain import chunked_bounds, inputs, recurrence
+from test_gpu_delta_tc import check as chunk_check
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -114,3 +115,35 @@ def test_resume_on_another_stream():
     torch.cuda.synchronize()
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dk,dv", [(8, 8), (16, 128), (24, 40), (64, 64), (64, 96), (40, 120)])
+@pytest.mark.parametrize("lengths", [[150, 130], [260, 1, 0, 300]])
+def test_small_heads_in_chunks(dk, dv, lengths):
+    """Head sizes up to 64 with sequences long enough for chunks of 64 tokens."""
+    x = inputs(lengths, 2, 1, dk, dv, BF16, seed=dk + dv, init=True, per_token=dv != 40)
+    out, state = kda.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], x["cu"], x["init"], scale=0.5)
+    chunk_check(out, state, x, lengths, 0.5)
+
+
+@pytest.mark.parametrize("dtype,shape", [(F32, (3, 1, 128, 128)), (BF16, (4, 2, 64, 72)), (BF16, (2, 2, 128, 128)),
+                                         (BF16, (2, 1, 248, 200))])
+@pytest.mark.parametrize("lengths", [[9], [16, 1, 7, 0, 8], [25, 24, 23]])
+def test_blocks_of_eight_tokens(dtype, shape, lengths):
+    """Sequences that end within a block of eight tokens, at one and behind one."""
+    h, hk, dk, dv = shape
+    x = inputs(lengths, h, hk, dk, dv, dtype, seed=sum(lengths) + dk, init=True)
+    out, state = kda.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], x["cu"], x["init"], out_dtype=F32)
+    want, final, err, bound = recurrence(x["q"], x["k"], x["v"], x["g"], x["beta"], lengths, x["init"])
+    assert bool(((out.double() - want).abs() <= bound + 2.0 ** -24 * (want.abs() + bound)).all())
+    assert bool(((state.double() - final).norm(dim=-2) <= err).all())
+    assert kda.device_status() == 0
+
+
+@pytest.mark.parametrize("power", [-60, 60])
+def test_magnitudes_of_fp32_values(power):
+    """Values and states times a power of two: the same results times it, bit for bit."""
+    x = inputs([50, 21], 2, 2, 64, 64, F32, seed=23, init=True)
+    out, state = kda.delta_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], x["cu"], x["init"])
+    y, z = kda.delta_prefill(x["q"], x["k"], x["v"] * 2.0 ** power, x["g"], x["beta"], x["cu"], x["init"] * 2.0 ** power)
+    assert torch.equal(y, out * 2.0 ** power) and torch.equal(z, state * 2.0 ** power)
