@@ -1,5 +1,5 @@
 // kda_delta_tc.cu -- the gated delta rule with one decay per head for bf16 operands: chunks of 64 tokens
-// on the tensor cores.
+// on the tensor cores (tcgen05).
 //
 //     S' = exp(g_t) S_(t-1),   S_t = S' + beta_t k_t (v_t - S'^T k_t)^T,   o_t = scale S_t^T q_t
 //
@@ -10,6 +10,27 @@
 //     S   <- e^(G_C) S + sum_j e^(G_C - G_j) k_j u_j^T
 // T, T V and the weighted q . k do not depend on the state, so they are made ahead of the chain
 // S -> X = S^T K^T -> R -> U -> S, which is all that is serial.
+//
+// One CTA a (sequence, head), all of an SM's tensor memory.  Everything is held transposed, value channels as lanes, so
+// that the state, R and U are A operands from tensor memory as the warps write them and k, q, v, T and the scores are B
+// operands from shared memory.  Two warpgroups are the chain (a thread has half of a lane's columns), one makes outputs,
+// two take the chunks in turn and make T and the scores (8 x 8 substitutions, then three joins of halves by mma.sync), and
+// three warps issue loads, the Gram products and the chain's products.  Registers are moved to the chain.
+// Precision: states shall be good to 1e-6, which bf16 operands (4e-3) miss and tf32's miss too.  S, R, U and T are therefore
+// three bf16 parts each (24 bits), six products where both sides have parts and three where one is an input; outputs
+// take two parts of S and of U and one of the scores.  fp16 parts would do with two, but k and v are bf16 of any size.
+// The products of one chunk: 3 x 8 for X, 6 x 4 for T R, 3 x 8 for the update, 3 x 4 for T V, 2 x 8 for S^T q, 2 x 4 for
+// the scores with U, 8 for the Gram, of [128 x 64 x 16] each at 43 cycles: some 5,000 cycles.
+//
+// Bound by that chain: a chunk takes some 7,600 cycles alone (8 heads), 8,700 with 96 SMs at work, the tensor pipe busy for
+// two thirds of them, issue slots for half, DRAM for a seventh.  Products that a chain needs (X, T R, update: 3,100) and the
+// passes between them (R, U and S out of tensor memory, into parts and back) follow one another; the rest runs beside
+// them, in the gaps.  Left out, to time the rest: preparation 15 % less, the splits 8 %, T V, Gram and S^T q 7 %, all but
+// the bare chain 33 %.  T = 8192: 96 heads of 128 x 128 0.585 ms, 32 heads 0.502, 8 heads 0.494, 96 of 64 x 64 0.493,
+// 152 heads 0.725.  The token-by-token kernel before it took 7.2 ms, the first version of this one 0.86.
+// Tried without gain: the chain's loads 32 columns at a time or ahead (spills), tf32 rounding by cvt.rna (6 % slower),
+// a wait without a first look before it sleeps (8 % slower).  T folded into k, so that
+// the chain would lose a pass, needs a second operand of three parts a chunk, 48 KB more than shared memory has.
 #include <cudaTypedefs.h>
 
 #include <mutex>
