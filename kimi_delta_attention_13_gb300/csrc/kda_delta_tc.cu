@@ -22,15 +22,19 @@
 // The products of one chunk: 3 x 8 for X, 6 x 4 for T R, 3 x 8 for the update, 3 x 4 for T V, 2 x 8 for S^T q, 2 x 4 for
 // the scores with U, 8 for the Gram, of [128 x 64 x 16] each at 43 cycles: some 5,000 cycles.
 //
-// Bound by that chain: a chunk takes some 7,600 cycles alone (8 heads), 8,700 with 96 SMs at work, the tensor pipe busy for
-// two thirds of them, issue slots for half, DRAM for a seventh.  Products that a chain needs (X, T R, update: 3,100) and the
-// passes between them (R, U and S out of tensor memory, into parts and back) follow one another; the rest runs beside
-// them, in the gaps.  Left out, to time the rest: preparation 15 % less, the splits 8 %, T V, Gram and S^T q 7 %, all but
-// the bare chain 33 %.  T = 8192: 96 heads of 128 x 128 0.585 ms, 32 heads 0.502, 8 heads 0.494, 96 of 64 x 64 0.493,
-// 152 heads 0.725.  The token-by-token kernel before it took 7.2 ms, the first version of this one 0.86.
-// Tried without gain: the chain's loads 32 columns at a time or ahead (spills), tf32 rounding by cvt.rna (6 % slower),
-// a wait without a first look before it sleeps (8 % slower).  T folded into k, so that
-// the chain would lose a pass, needs a second operand of three parts a chunk, 48 KB more than shared memory has.
+// Bound by that chain, and by instruction fetch: a chunk takes some 7,400 cycles alone (8 heads).  Products that a chain needs
+// (X, T R, update: 3,100) and the passes between them (R, U and S out of tensor memory, into parts and back) follow one
+// another; the rest runs beside them, in the gaps.  Left out, to time the rest: preparation 15 % less, the splits 8 %, T V,
+// Gram and S^T q 7 %, all but the bare chain 33 %.  The loops' 80 KB of code, a product being 220 bytes of it, do not stay in
+// an SM's instruction cache, and what SMs share behind it slows them down together: warps without an instruction, per one
+// issued, 0.35 with 8 SMs at work, 0.7 with 96, 3.7 with 152.  T = 8192: 8 heads of 128 x 128 0.484 ms, 96 heads 0.510 (on
+// other GPUs up to 0.56), 152 heads 0.681, 96 of 64 x 64 0.438.  The token-by-token kernel before it took 7.2 ms, the first
+// version of this one 0.86.
+// Tried: all products in loops 0.636, 0.646 and 0.659 ms for 8, 96 and 152 heads (their issue is on the chain), those beside
+// the chain in loops 0.532, 0.574, 0.689, by a warp of their own 0.503, 0.576, 0.704; waits without a first look 0.571,
+// 0.576, 0.660; before T V stood once and the joins' and R's loops were rolled 0.492, 0.528, 0.720.  Without gain: the
+// chain's loads 32 columns at a time or ahead (spills), tf32 rounding by cvt.rna (6 % slower).  T folded into k, so
+// that the chain would lose a pass, needs a second operand of three parts a chunk, 48 KB more than shared memory has.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -191,48 +195,51 @@ __device__ __forceinline__ float exp2_fast(float x)
 __device__ void load_role(const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv, uint8_t *smem, Shared *sh,
                           int h, int hk, int regions, long long t0, int nch)
 {
+    // a tile's loads, and the next one's into L2 (its work begins with its load and has to end in two chunks' time)
     auto kq = [&](int c) {
         if (elect_one()) {
             uint64_t *bar = &sh->bars[B_KQ_FULL + c % STAGES];
             uint8_t *to = smem + SM_KQ + c % STAGES * 2 * REGION;
+            const int t = (int)(t0 + (long long)c * C);
             mbar_arrive_expect_tx(bar, regions * REGION);
+#pragma unroll 1
             for (int r = 0; r < regions; ++r) {
-                tma_load_3d(to + r * REGION + (c & 1) * TILE, mk, bar, 64 * r, hk, (int)(t0 + (long long)c * C));
-                tma_load_3d(to + r * REGION + (~c & 1) * TILE, mq, bar, 64 * r, hk, (int)(t0 + (long long)c * C));
+                tma_load_3d(to + r * REGION + (c & 1) * TILE, mk, bar, 64 * r, hk, t);
+                tma_load_3d(to + r * REGION + (~c & 1) * TILE, mq, bar, 64 * r, hk, t);
+                if (c + 1 < nch) {
+                    tma_prefetch_l2_3d(mk, 64 * r, hk, t + C);
+                    tma_prefetch_l2_3d(mq, 64 * r, hk, t + C);
+                }
             }
         }
         __syncwarp();
     };
     auto value = [&](int c) {
         if (elect_one()) {
+            const int t = (int)(t0 + (long long)c * C);
             mbar_arrive_expect_tx(&sh->bars[B_V_FULL], 2 * TILE);
-            for (int r = 0; r < 2; ++r)
-                tma_load_3d(smem + SM_V + r * TILE, mv, &sh->bars[B_V_FULL], 64 * r, h, (int)(t0 + (long long)c * C));
+#pragma unroll 1
+            for (int r = 0; r < 2; ++r) {
+                tma_load_3d(smem + SM_V + r * TILE, mv, &sh->bars[B_V_FULL], 64 * r, h, t);
+                if (c + 1 < nch) tma_prefetch_l2_3d(mv, 64 * r, h, t + C);
+            }
         }
         __syncwarp();
     };
-    auto ahead = [&](const CUtensorMap *m, int head, int boxes, int c) {   // into L2
-        if (c < nch && elect_one())
-            for (int r = 0; r < boxes; ++r) tma_prefetch_l2_3d(m, 64 * r, head, (int)(t0 + (long long)c * C));
-        __syncwarp();
-    };
     int nk = 0, nv = 0;   // tiles issued
+#pragma unroll 1
     for (; nk < nch && nk < STAGES; ++nk) kq(nk);
-    ahead(mk, hk, regions, nk);
-    ahead(mq, hk, regions, nk);
     bool ok = true;
+#pragma unroll 1
     for (; ok && nv < nch; ++nv) {
         if (nv > 0 && !(ok = wait_warp(sh, B_V_FREE, nv - 1))) break;
         value(nv);
-        ahead(mv, h, 2, nv + 1);
         if (nv > 0 && nk < nch) {   // the stage was chunk nv - 1's
             if (!(ok = wait_warp(sh, B_K_FREE + nk % STAGES, nk / STAGES - 1))) {
                 ++nv;
                 break;
             }
             kq(nk++);
-            ahead(mk, hk, regions, nk);   // (a tile's work begins with its load and has to end in two chunks' time)
-            ahead(mq, hk, regions, nk);
         }
     }
     if (!ok) {   // no copy in flight when the CTA leaves
@@ -304,11 +311,16 @@ __device__ void chain_mma_role(uint32_t sb, Shared *sh, int nch)
 {
     constexpr int STEPS = 4 * REGIONS, GROUPS = STEPS / 2;   // 16 key channels each; those of four warps
     constexpr uint32_t I64 = idesc_bf16(128, 64, 0, 0), I_KU = idesc_bf16(128, 64, 0, 1);
-    // U = T V, where nothing waits for the pipe: while the state before is worked on
-    auto values = [&](int c) {
-        const int half = c & 1;
-        const uint32_t t = desc_lo(sb + SM_T + half * 3 * TILE), v = desc_lo(sb + SM_V, TILE);
-        if (!wait_warp(sh, B_T_READY + half, c >> 1) || !wait_warp(sh, B_V_FULL, c) || !wait_warp(sh, B_V_READY, c)) return false;
+    bool ok = true;
+    for (int c = 0; ok && c < nch; ++c) {
+        const int st = c % STAGES, half = c & 1;
+        const uint32_t tile = sb + SM_KQ + st * 2 * REGION;
+        const uint32_t k = desc_lo(tile + half * TILE), q = desc_lo(tile + (half ^ 1) * TILE), t = desc_lo(sb + SM_T + half * 3 * TILE),
+                       v = desc_lo(sb + SM_V, TILE), p = desc_lo(sb + SM_P + c % P_TILES * TILE);
+        // U = T V, where nothing waits for the pipe: while the state before is worked on (the update reads where U comes)
+        ok = (c == 0 || wait_warp(sh, B_KU_DONE + REGIONS - 1, c - 1)) && wait_warp(sh, B_T_READY + half, c >> 1) &&
+             wait_warp(sh, B_V_FULL, c) && wait_warp(sh, B_V_READY, c);
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
             each<4>([&](auto s_) {
@@ -322,14 +334,6 @@ __device__ void chain_mma_role(uint32_t sb, Shared *sh, int nch)
             mma_commit(&sh->bars[B_V_FREE]);
         }
         __syncwarp();
-        return true;
-    };
-    bool ok = nch == 0 || values(0);
-    for (int c = 0; ok && c < nch; ++c) {
-        const int st = c % STAGES, half = c & 1;
-        const uint32_t tile = sb + SM_KQ + st * 2 * REGION;
-        const uint32_t k = desc_lo(tile + half * TILE), q = desc_lo(tile + (half ^ 1) * TILE), t = desc_lo(sb + SM_T + half * 3 * TILE),
-                       p = desc_lo(sb + SM_P + c % P_TILES * TILE);
         // X = S^T K^T, as the state's parts come (over what the last chunk's outputs read)
         ok = wait_warp(sh, B_K_READY + st, c / STAGES) && (c == 0 || wait_warp(sh, B_O2_DONE, c - 1));
         each<GROUPS>([&](auto g_) {
@@ -423,7 +427,6 @@ __device__ void chain_mma_role(uint32_t sb, Shared *sh, int nch)
             mma_commit(&sh->bars[B_P_FREE + c % P_TILES]);
         }
         __syncwarp();
-        if (c + 1 < nch) ok = wait_warp(sh, B_KU_DONE + REGIONS - 1, c) && values(c + 1);   // (the update reads where U comes)
     }
     if (!ok) drain(sh, 1);
 }
@@ -504,7 +507,7 @@ __device__ void chain_role(const Args &p, uint8_t *smem, Shared *sh, int seq, in
         if (!wait_warp(sh, B_DEC_READY + c % DECS, c / DECS)) return give_up(sh);
         if (!wait_warp(sh, B_X_DONE, c)) return give_up(sh);
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int g = 0; g < 2; ++g) {   // R = -e^G X, in three parts
             uint32_t x[16], two[16], lo[8];
             float2 y[8];
@@ -677,7 +680,7 @@ __device__ __forceinline__ void products(const float *a, const float *b, int len
     for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[n][e] = 0.f;
-#pragma unroll
+#pragma unroll 2
     for (int k = 0; k < len; k += 8) {
         uint32_t ah[4], al[4], bh[2], bl[2];
         tf32_parts(a[at + k], ah[0], al[0]);
