@@ -18,16 +18,18 @@
 // (two side by side along k where that is only eight tokens long); of the nine products of two factors the three smallest,
 // 2^-24 of the whole, are left out; a bf16 input is one part.  A warp's CUDA cores would take 768 cycles of FMA for
 // eight tokens of 16 columns x 64 channels, and each of their operands from shared memory: the 78 products take 640.
-// Four warps load three blocks ahead, make the parts and, two ahead, the scores; one warp makes the decays, and one M,
-// a thread a column, one block ahead.  A barrier of these ten warps ends a block.  Registers are moved to the chain.
-// (tcgen05's 64-token chunks, kda_delta_tc.cu, would need k and q in three parts in shared memory as well.)
+// Four warps load four blocks ahead, make the parts and, three ahead, the scores, each for a quarter of the channels; a
+// warp each makes the decays, the scores' sums and weights, and M, a thread a column, one block ahead.  A barrier of these
+// eleven warps ends a block.  Registers are moved to the chain.  (tcgen05's 64-token chunks, kda_delta_tc.cu, would need k
+// and q in three parts in shared memory as well.)
 //
-// Bound by the chain's latency, one warp a scheduler: some 1,400 cycles of the 1,800 that a block of tokens takes, the
-// other warps' instructions between them.  2560 tokens in two sequences, 16 heads of 64 x 128, fp32: 233 us.  Before, on
+// Bound by the chain's latency, one warp a scheduler: some 1,400 cycles of the 1,650 that a block of tokens takes, the
+// other warps' instructions between them.  2560 tokens in two sequences, 16 heads of 64 x 128, fp32: 215 us.  Before, on
 // CUDA cores with a barrier between the steps: 454; sums over lanes in place of shared memory: 372, bound by shared
-// memory's 128 bytes a cycle; all makers' work in four warps: 285; decays and M in one warp: 250; q's products behind the
-// new values, or outputs a block later: no gain.  2048 tokens of 96 heads of 128 x 128 0.80 ms (1.58 before), of 16 heads of
-// 256 x 256 in bf16 0.56 (1.20).
+// memory's 128 bytes a cycle; all but the chain in four warps: 285; decays and M in one warp: 250; scores by fp32 FMA: 233;
+// q's products behind the new values, outputs a block later or before the update, the state's decay earlier, a block
+// an SM with more registers: no gain.  2048 tokens of 96 heads of 128 x 128 0.67 ms (1.58 before), of 16 heads of 256 x 256 in
+// bf16 0.45 (1.20).
 #include "kda_delta.cuh"
 #include "sm100_ptx.cuh"
 
@@ -48,7 +50,7 @@ constexpr int TB = 8;        // tokens at a time
 constexpr int kChain = 4;    // warps that hold the state, 16 value columns each
 constexpr int kMakers = 4;   // warps that make what does not depend on it
 constexpr int COLS = 16 * kChain;
-constexpr int kThreads = 32 * (kChain + kMakers + 4);   // and a warpgroup of which two warps work: solves, decays
+constexpr int kThreads = 32 * (kChain + kMakers + 4);   // and a warpgroup of which three warps work
 
 // Registers a thread: at launch, then of each warpgroup (their sum may not pass the block's)
 template <int DK>
@@ -61,7 +63,7 @@ __device__ __forceinline__ void set_regs()
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// what a block of tokens is worked from: staged, scored, solved and used in four periods
+// what a block of tokens is worked from: staged, scored, weighted, solved and used in five periods
 template <int DK, int PARTS>
 struct __align__(16) Stage {
     uint16_t k[PARTS][TB][DK + 8], q[PARTS][TB][DK + 8];   // bf16 parts (rows padded against bank conflicts)
@@ -71,9 +73,9 @@ struct __align__(16) Stage {
     float beta[TB], pre[TB], suf[TB];          // beta, e^G, e^(G_last - G)
     float all, near, unused[2];                // the whole block's decay, less 1 where it is near 1
 };
-template <int DK>
-struct Rows {
-    float k[TB][DK + 4], q[TB][DK + 4];        // for the scores
+constexpr int kStages = 5;
+struct Scores {
+    float sum[kMakers][2 * TB][TB];            // a maker's channels' part of k . k, then of q . k
 };
 
 // x, y as three packed pairs of bf16, which sum to them
@@ -121,19 +123,19 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel
 {
     constexpr int PARTS = sizeof(T) == 4 ? 3 : 1, MT = 32 * kMakers;
     constexpr int KU = TB * DK / 4 / MT, PITCH = (DK + 8) * 2;
-    constexpr int SUB = MT / (TB * TB);               // threads of a score
-    static_assert(TB * DK / 4 % MT == 0 && TB * COLS / 4 == MT && SUB == 2, "");
+    static_assert(TB * DK / 4 % MT == 0 && TB * COLS / 4 == MT && DK / 16 % kMakers == 0, "");
     using Four = decltype(load4((const T *)nullptr));
     extern __shared__ __align__(16) char raw[];
-    Stage<DK, PARTS> *stages = reinterpret_cast<Stage<DK, PARTS> *>(raw);   // [4]
-    Rows<DK> *rows = reinterpret_cast<Rows<DK> *>(stages + 4);              // [2]
+    Stage<DK, PARTS> *stages = reinterpret_cast<Stage<DK, PARTS> *>(raw);
+    Scores *scores = reinterpret_cast<Scores *>(stages + kStages);          // [2]
+    auto stage_of = [&](int m) -> Stage<DK, PARTS> & { return stages[(unsigned)m % kStages]; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / p.group, Hk = p.H / p.group;
     const int cb = blockIdx.y * COLS;
     long long b, e;
     bounds(p, seq, b, e);
-    const int len = (int)(e - b), nb = len / TB + (len % TB != 0), first = nb ? -3 : 0;
-    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * (kChain + kMakers + 2)) : "memory"); };
+    const int len = (int)(e - b), nb = len / TB + (len % TB != 0), first = nb ? -4 : 0;
+    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * (kChain + kMakers + 3)) : "memory"); };
     if (warp >= kChain && warp < kChain + kMakers) {
         set_regs<kRegs<DK>[0], kRegs<DK>[2]>();
         const int mid = tid - 32 * kChain;
@@ -157,10 +159,9 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel
             ko += TB * krow;
             vo += TB * vrow;
         };
-        auto put = [&](uint16_t (&to)[PARTS][TB][DK + 8], float (&wide)[TB][DK + 4], int t, int i, Four x) {
-            const float4 f = widen(x);
-            *reinterpret_cast<float4 *>(&wide[t][i]) = f;
+        auto put = [&](uint16_t (&to)[PARTS][TB][DK + 8], int t, int i, Four x) {
             if constexpr (PARTS == 3) {
+                const float4 f = widen(x);
                 uint2 hi, md, lo;
                 split(f.x, f.y, hi.x, md.x, lo.x);
                 split(f.z, f.w, hi.y, md.y, lo.y);
@@ -171,56 +172,79 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel
                 *reinterpret_cast<uint2 *>(&to[0][t][i]) = x;
             }
         };
-        const int si = mid / SUB / TB, sj = mid / SUB % TB;
+        // scores, of DK / kMakers channels: rows k and then q of eight tokens by columns k; the four tiles of an operand
+        const int who = warp - kChain, x = lane >> 2, y = lane & 3;
+        const uint32_t tile = (lane & 7) * PITCH + (lane >> 4) * 16 + who * (DK / kMakers) * 2 + (lane >> 3 & 1) * (uint32_t)sizeof(Stage<DK, PARTS>::k);
         if (nb) fetch(len);
         for (int it = first; it < nb; ++it) {
-            if (it + 2 >= 0 && it + 2 < nb) {   // score
-                Stage<DK, PARTS> &s = stages[(it + 2) & 3];
-                const Rows<DK> &f = rows[it & 1];
-                const int i = si, j = sj;
-                float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), q4 = k4;
-#pragma unroll 8
-                for (int x = mid % SUB * 4; x < DK; x += 4 * SUB) {
-                    const float4 kj = *reinterpret_cast<const float4 *>(&f.k[j][x]);
-                    const float4 ki = *reinterpret_cast<const float4 *>(&f.k[i][x]);
-                    const float4 qi = *reinterpret_cast<const float4 *>(&f.q[i][x]);
-                    k4.x = fmaf(kj.x, ki.x, k4.x); k4.y = fmaf(kj.y, ki.y, k4.y); k4.z = fmaf(kj.z, ki.z, k4.z); k4.w = fmaf(kj.w, ki.w, k4.w);
-                    q4.x = fmaf(kj.x, qi.x, q4.x); q4.y = fmaf(kj.y, qi.y, q4.y); q4.z = fmaf(kj.z, qi.z, q4.z); q4.w = fmaf(kj.w, qi.w, q4.w);
-                }
-                float kk = (k4.x + k4.y) + (k4.z + k4.w), qk = (q4.x + q4.y) + (q4.z + q4.w);
+            if (it + 3 >= 0 && it + 3 < nb) {   // score
+                const uint32_t at = ptx::smem_u32(&stage_of(it + 3).k[0][0][0]) + tile;
+                float c[3][4] = {};
 #pragma unroll
-                for (int o = SUB / 2; o > 0; o >>= 1) {
-                    kk += __shfl_xor_sync(0xffffffffu, kk, o);
-                    qk += __shfl_xor_sync(0xffffffffu, qk, o);
+                for (int n = 0; n < DK / 16 / kMakers; ++n) {
+                    uint32_t f[PARTS][4];
+#pragma unroll
+                    for (int a = 0; a < PARTS; ++a) tiles(f[a], at + a * TB * PITCH + 32 * n);
+                    auto one = [&](int to, int a, int z) { mma(c[to], f[a][0], f[a][1], f[a][2], f[a][3], f[z][0], f[z][2]); };
+                    one(0, 0, 0);
+                    if constexpr (PARTS == 3) {
+                        one(1, 0, 1);
+                        one(2, 1, 1);
+                        one(1, 1, 0);
+                        one(2, 0, 2);
+                        one(2, 2, 0);
+                    }
                 }
-                if (mid % SUB == 0) {
-                    const float w = s.w[i][j];
-                    s.a[i][j] = s.beta[i] * w * kk;
-                    s.p[i][j] = j <= i ? w * qk : 0.f;
-                }
+                float (&to)[2 * TB][TB] = scores[it & 1].sum[who];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<float2 *>(&to[x + TB * i][2 * y]) =
+                        make_float2(c[0][2 * i] + (c[1][2 * i] + c[2][2 * i]), c[0][2 * i + 1] + (c[1][2 * i + 1] + c[2][2 * i + 1]));
             }
-            if (it + 3 < nb) {   // stage
-                Stage<DK, PARTS> &s = stages[(it + 3) & 3];
-                Rows<DK> &f = rows[(it + 1) & 1];
+            if (it + 4 < nb) {   // stage
+                Stage<DK, PARTS> &s = stage_of(it + 4);
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
-                    put(s.k, f.k, kt + u * STEP, ki, nk[u]);
-                    put(s.q, f.q, kt + u * STEP, ki, nq[u]);
+                    put(s.k, kt + u * STEP, ki, nk[u]);
+                    put(s.q, kt + u * STEP, ki, nq[u]);
                 }
                 *reinterpret_cast<float4 *>(&s.v[vt][vi]) = widen(nv);
-                if (it + 4 < nb) fetch(len - (it + 4) * TB);
+                if (it + 5 < nb) fetch(len - (it + 5) * TB);
             }
             meet();
         }
         return;
     }
-    if (warp >= kChain) {                             // solves, decays
+    if (warp >= kChain) {                             // solves, decays, weights
         set_regs<kRegs<DK>[0], kRegs<DK>[3]>();
-        if (warp > kChain + kMakers + 1) return;
+        if (warp > kChain + kMakers + 2) return;
+        if (warp == kChain + kMakers + 2) {           // weights
+            for (int it = first; it < nb; ++it) {
+                if (it + 2 >= 0 && it + 2 < nb) {
+                    Stage<DK, PARTS> &s = stage_of(it + 2);
+                    const Scores &f = scores[(it + 1) & 1];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int i = (lane >> 3) + 4 * n, j = lane & 7;
+                        float kk = 0.f, qk = 0.f;
+#pragma unroll
+                        for (int a = 0; a < kMakers; ++a) {
+                            kk += f.sum[a][i][j];
+                            qk += f.sum[a][TB + i][j];
+                        }
+                        const float w = s.w[i][j];
+                        s.a[i][j] = s.beta[i] * w * kk;
+                        s.p[i][j] = j <= i ? w * qk : 0.f;
+                    }
+                }
+                meet();
+            }
+            return;
+        }
         if (warp == kChain + kMakers) {
             for (int it = first; it < nb; ++it) {
                 if (it + 1 >= 0 && it + 1 < nb && lane < TB) {   // solve: a thread a column
-                    Stage<DK, PARTS> &s = stages[(it + 1) & 3];
+                    Stage<DK, PARTS> &s = stage_of(it + 1);
                     float x[TB];
 #pragma unroll
                     for (int i = 0; i < TB; ++i) x[i] = i == lane ? 1.f : 0.f;
@@ -256,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel
         };
         if (nb) fetch(len);
         for (int it = first; it < nb; ++it) {
-            if (it + 3 < nb) {   // (lanes from TB on hold 0, the sums that reach past the block stay in it)
-                Stage<DK, PARTS> &s = stages[(it + 3) & 3];
+            if (it + 4 < nb) {   // (lanes from TB on hold 0, the sums that reach past the block stay in it)
+                Stage<DK, PARTS> &s = stage_of(it + 4);
                 float after = ng, before = ng;
 #pragma unroll
                 for (int o = 1; o < TB; o <<= 1) {
@@ -284,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel
                     s.all = near ? expm1f(after) : expf(after);
                     s.near = near ? 1.f : 0.f;
                 }
-                if (it + 4 < nb) fetch(len - (it + 4) * TB);
+                if (it + 5 < nb) fetch(len - (it + 5) * TB);
             }
             meet();
         }
@@ -310,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel
     const uint32_t tile = (lane & 7) * PITCH + (lane >> 3) * 16;
     for (int it = first; it < nb; ++it) {
         if (it >= 0 && busy) {
-            const Stage<DK, PARTS> &s = stages[it & 3];
+            const Stage<DK, PARTS> &s = stage_of(it);
             const int left = len - it * TB;
             const uint32_t ak = ptx::smem_u32(&s.k[0][0][0]) + tile, aq = ptx::smem_u32(&s.q[0][0][0]) + tile;
             float xk[3][4] = {}, xq[3][4] = {};       // S^T k, S^T q: the large, the middle and the small products
@@ -417,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, DK == 64 ? 2 : 1) delta_token_kernel
 template <typename T, typename TO, int DK>
 int launch_size(const Args &p, cudaStream_t stream)
 {
-    constexpr int bytes = 4 * sizeof(Stage<DK, sizeof(T) == 4 ? 3 : 1>) + 2 * sizeof(Rows<DK>);
+    constexpr int bytes = kStages * sizeof(Stage<DK, sizeof(T) == 4 ? 3 : 1>) + 2 * sizeof(Scores);
     // a function attribute belongs to the current device: set it on every launch
     if (cudaFuncSetAttribute(delta_token_kernel<T, TO, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return KDA_ERR_CUDA;
@@ -444,9 +468,9 @@ int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream)
 }
 
 // Whether the kernel of kda_delta_tc.cu takes these operands: from a mean length on at which it is the faster (us, here
-// and there, with initial states.  128 x 128: 32 heads, one sequence of 32 tokens 9.1, 13.8, of 64 13.6, 13.0, 16 of 16 38,
-// 55, of 32 57, 55, of 64 91, 54; 96 heads, one of 32 16, 14, 16 of 32 176, 151.  64 x 64: 16 heads, one of 64 9.7, 11.1,
-// of 128 15.6, 14.4, 16 of 64 14, 22, of 128 23, 29; 64 heads, 64 sequences of 64 176, 289, 16 of 128 84, 100).
+// and there, with initial states.  128 x 128: 32 heads, one sequence of 32 tokens 8.5, 13.9, of 64 12.1, 12.9, 16 of 16 34,
+// 54, of 32 53, 55, of 64 82, 53; 96 heads, one of 32 15, 14, 16 of 32 176, 149.  64 x 64: 16 heads, one of 64 9.1, 11.1,
+// of 128 14.2, 14.2, 16 of 64 13, 22, of 128 21, 29; 64 heads, 64 sequences of 64 167, 288, 16 of 128 80, 100).
 bool tc_path(int n_seqs, int64_t T, int d_k, int d_v, int dtype)
 {
     return dtype == KDA_BF16 && d_k <= 128 && d_v <= 128 && T >= (d_k <= 64 ? 128 : 32) * (int64_t)n_seqs;
