@@ -94,12 +94,14 @@ class CheckpointStore:
                 pos += 1
         if len(entries) > self.n_slots:
             raise ValueError(f"{len(entries)} checkpoints do not fit {self.n_slots} slots")
-        dst = [self._take_slot(e) for e in entries]
+        dst = [(self._next + i) % self.n_slots for i in range(len(entries))]
         if entries:
             dev = self.states.device
             with _on_stream(dev, stream):   # what the copy reads belongs to its stream
                 slots, rows = (torch.tensor(x, device=dev, dtype=torch.int64) for x in (dst, src))
             self.write(slots, ckpts, rows, stream=stream)
+        for e in entries:                   # indexed once they are written: a refused copy leaves the store as it was
+            self._take_slot(e)
         return [(k, n, s) for (k, n), s in zip(entries, dst)]
 
     def lookup(self, key: object, n_tokens: int) -> Tuple[Optional[int], int]:
