@@ -31,7 +31,7 @@ class CheckpointStore:
     (the oldest entry is overwritten when the pool is full), indexed by (key, tokens covered).
     dtype: float32 (as they are), int8 (a quarter of the memory: a value is off by at most 1/254 of its
     row's largest, rows being key channels, whose scales are `scales`), or bfloat16 (half: at most 2^-8 of
-    the value)."""
+    the value); packed ones have d_v a multiple of 4, d_k and d_v up to 256."""
 
     def __init__(self, n_slots: int, heads: int, d_k: int = 128, d_v: int = 128, device=None,
                  dtype: torch.dtype = torch.float32):
@@ -39,6 +39,8 @@ class CheckpointStore:
             raise ValueError("n_slots must be positive")
         if dtype not in (torch.float32, torch.bfloat16, torch.int8):
             raise ValueError("a store holds float32, bfloat16 or int8 states")
+        if dtype is not torch.float32 and (d_v % 4 != 0 or d_v > 256 or d_k > 256):   # kda_state_pack's
+            raise ValueError(f"states of {d_k} x {d_v} cannot be packed: d_v a multiple of 4, both up to 256")
         self.states = torch.empty(n_slots, heads, d_k, d_v, device=device, dtype=dtype)
         self.scales = torch.empty(n_slots, heads, d_k, device=device) if dtype is torch.int8 else None
         self._index: Dict[Tuple[object, int], int] = {}

@@ -23,3 +23,13 @@ def test_a_refused_write_leaves_the_index(monkeypatch, dtype):
             m.setattr(prefix_cache, name, lambda *a, **kw: None)
         assert store.add_checkpoints(["b"], torch.zeros(2, 1, 4, 4), 32, [64]) == [("b", 32, 2), ("b", 64, 0)]
     assert store.lookup("a", 40) == (None, 0) and store.lookup("a", 100) == (1, 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8])
+@pytest.mark.parametrize("d_k,d_v", [(8, 6), (8, 258), (8, 260), (264, 8), (257, 256)])
+def test_head_sizes_that_cannot_be_packed(dtype, d_k, d_v):
+    with pytest.raises(ValueError):
+        CheckpointStore(2, 1, d_k, d_v, device="cpu", dtype=dtype)
+    CheckpointStore(2, 1, d_k, d_v, device="cpu")        # as they are
+    CheckpointStore(2, 1, 256, 256, device="cpu", dtype=dtype)
+    CheckpointStore(2, 1, 9, 4, device="cpu", dtype=dtype)
