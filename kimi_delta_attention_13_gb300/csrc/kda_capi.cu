@@ -617,39 +617,7 @@ int kda_diag_bounds_check(int32_t run_probe, int32_t *site, void *stream)
 int kda_device_status(int32_t *status, void *stream)
 {
     if (!status) return KDA_ERR_INVALID_ARG;
-    int32_t a = 0, b = 0, c = 0;
-    int rc = read_and_clear_status_state_copy((cudaStream_t)stream, &a);
-    if (rc != KDA_OK) return rc;
-    rc = read_and_clear_status_prefill_tc((cudaStream_t)stream, &b);
-    if (rc != KDA_OK) return rc;
-    int32_t bp = 0;
-    rc = read_and_clear_status_prefill_tc_precise((cudaStream_t)stream, &bp);
-    if (rc != KDA_OK) return rc;
-    if (b == KDA_OK) b = bp;
-    rc = read_and_clear_status_decode((cudaStream_t)stream, &c);
-    if (rc != KDA_OK) return rc;
-    int32_t cp = 0;
-    rc = read_and_clear_status_cp((cudaStream_t)stream, &cp);
-    if (rc != KDA_OK) return rc;
-    if (c == KDA_OK) c = cp;
-    int32_t lt = 0;
-    rc = read_and_clear_status_linear((cudaStream_t)stream, &lt);
-    if (rc != KDA_OK) return rc;
-    if (c == KDA_OK) c = lt;
-    int32_t dt = 0;
-    rc = read_and_clear_status_delta((cudaStream_t)stream, &dt);
-    if (rc != KDA_OK) return rc;
-    if (c == KDA_OK) c = dt;
-    int32_t dd = 0;
-    rc = read_and_clear_status_delta_decode((cudaStream_t)stream, &dd);
-    if (rc != KDA_OK) return rc;
-    if (c == KDA_OK) c = dd;
-    int32_t pk = 0;
-    rc = read_and_clear_status_state_pack((cudaStream_t)stream, &pk);
-    if (rc != KDA_OK) return rc;
-    if (a == KDA_OK) a = pk;
-    *status = b != KDA_OK ? b : (c != KDA_OK ? c : a);
-    return KDA_OK;
+    return read_and_clear_status((cudaStream_t)stream, status);
 }
 
 }  // extern "C"

@@ -365,15 +365,10 @@ int launch_cp_correct(const float *u, const float *s_start, const int32_t *cu_se
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-int read_and_clear_status_cp(cudaStream_t s, int32_t *status)
+int *status_word_cp()
 {
-    int host = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_cp_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_cp_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    *status = host;
-    return KDA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_cp_error) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 }  // namespace kda

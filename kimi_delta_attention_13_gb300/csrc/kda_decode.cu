@@ -239,17 +239,10 @@ decode_bulk_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
 
 }  // namespace
 
-int read_and_clear_status_decode(cudaStream_t s, int32_t *status)
+int *status_word_decode()
 {
-    int host = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_decode_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
-            cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_decode_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
-            cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    *status = host;
-    return KDA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_decode_error) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 int launch_decode(const void *q, const void *k, const void *v, const void *g, const void *beta,

@@ -1165,15 +1165,10 @@ int launch_delta_timeout_probe(uint32_t cycles, cudaStream_t stream)
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-int read_and_clear_status_delta(cudaStream_t s, int32_t *status)
+int *status_word_delta()
 {
-    int host = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, delta::g_delta_tc_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(delta::g_delta_tc_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    *status = host;
-    return KDA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, delta::g_delta_tc_error) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 }  // namespace kda

@@ -55,16 +55,18 @@ __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / 
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Per-translation-unit readers of the sticky device error words (see kda_device_status).
-int read_and_clear_status_state_copy(cudaStream_t s, int32_t *status);
-int read_and_clear_status_prefill_tc(cudaStream_t s, int32_t *status);
-int read_and_clear_status_prefill_tc_precise(cudaStream_t s, int32_t *status);
-int read_and_clear_status_decode(cudaStream_t s, int32_t *status);
-int read_and_clear_status_cp(cudaStream_t s, int32_t *status);
-int read_and_clear_status_linear(cudaStream_t s, int32_t *status);
-int read_and_clear_status_state_pack(cudaStream_t s, int32_t *status);
-int read_and_clear_status_delta(cudaStream_t s, int32_t *status);
-int read_and_clear_status_delta_decode(cudaStream_t s, int32_t *status);
+// Each translation unit's sticky error word on the current device, or null (a CUDA error); and their reader (see
+// kda_device_status), which finds the first that is set in this order and clears all.
+int *status_word_prefill_tc();
+int *status_word_prefill_tc_precise();
+int *status_word_decode();
+int *status_word_cp();
+int *status_word_linear();
+int *status_word_delta();
+int *status_word_delta_decode();
+int *status_word_state_copy();
+int *status_word_state_pack();
+int read_and_clear_status(cudaStream_t s, int32_t *status);
 // Launch the one-CTA probe whose bounded device wait expires after `cycles` SM cycles.
 int launch_wait_timeout_probe(long long cycles, cudaStream_t stream);
 // The same with the waits of the linear-attention and of the gated-delta-rule prefill.

@@ -1362,18 +1362,10 @@ int KDA_TC_EXPORT(read_and_clear_debug_site)(cudaStream_t s, int32_t *site)
     return KDA_OK;
 }
 
-int KDA_TC_EXPORT(read_and_clear_status_prefill_tc)(cudaStream_t s, int32_t *status)
+int *KDA_TC_EXPORT(status_word_prefill_tc)()
 {
-    int host = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_prefill_tc_error, sizeof(int), 0,
-                                  cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaMemcpyToSymbolAsync(g_prefill_tc_error, &zero, sizeof(int), 0,
-                                cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
-    *status = host;
-    return KDA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_prefill_tc_error) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 int KDA_TC_EXPORT(launch_prefill_tc)(const void *q, const void *k, const void *v, const void *g,

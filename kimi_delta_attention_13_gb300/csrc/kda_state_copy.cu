@@ -86,18 +86,10 @@ state_copy_bulk_kernel(char *__restrict__ dst, const int64_t *__restrict__ dst_i
 
 }  // namespace
 
-int read_and_clear_status_state_copy(cudaStream_t s, int32_t *status)
+int *status_word_state_copy()
 {
-    int host = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_state_copy_error, sizeof(int), 0,
-                                  cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaMemcpyToSymbolAsync(g_state_copy_error, &zero, sizeof(int), 0,
-                                cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
-    *status = host;
-    return KDA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_state_copy_error) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 int launch_state_copy(float *dst, const int64_t *dst_idx, int64_t n_dst, const float *src,

@@ -285,15 +285,10 @@ int launch_state_unpack(float *dst, const int64_t *dst_idx, int64_t n_dst, const
     return run(m, format, false, stream);
 }
 
-int read_and_clear_status_state_pack(cudaStream_t s, int32_t *status)
+int *status_word_state_pack()
 {
-    int host = 0, zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&host, g_state_pack_error, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_state_pack_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    *status = host;
-    return KDA_OK;
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_state_pack_error) == cudaSuccess ? static_cast<int *>(p) : nullptr;
 }
 
 }  // namespace kda
