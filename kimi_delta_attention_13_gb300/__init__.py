@@ -654,7 +654,7 @@ def device_status(stream=None, device=None) -> int:
     lib = _lib.load()
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     st = ctypes.c_int32(0)
-    _lib.check(lib.kda_device_status(ctypes.byref(st), _stream(dev, stream)), "kda_device_status")
+    _call("kda_device_status", lib.kda_device_status, dev, ctypes.byref(st), _stream(dev, stream))
     return int(st.value)
 
 
@@ -664,21 +664,18 @@ def diag_device_timeout(timeout_cycles: int = 2_000_000, stream=None, device=Non
     by device_status()."""
     lib = _lib.load()
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    _lib.check(lib.kda_diag_device_timeout(int(timeout_cycles), _stream(dev, stream)),
-               "kda_diag_device_timeout")
+    _call("kda_diag_device_timeout", lib.kda_diag_device_timeout, dev, int(timeout_cycles), _stream(dev, stream))
 
 
 def diag_linear_timeout(timeout_cycles: int = 2_000_000, stream=None, device=None) -> None:
     """diag_device_timeout's check of the wait that linear_prefill's tensor-core kernel uses."""
     lib = _lib.load()
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    _lib.check(lib.kda_diag_linear_timeout(int(timeout_cycles), _stream(dev, stream)),
-               "kda_diag_linear_timeout")
+    _call("kda_diag_linear_timeout", lib.kda_diag_linear_timeout, dev, int(timeout_cycles), _stream(dev, stream))
 
 
 def diag_delta_timeout(timeout_cycles: int = 2_000_000, stream=None, device=None) -> None:
     """diag_device_timeout's check of the wait that delta_prefill's tensor-core kernel uses."""
     lib = _lib.load()
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    _lib.check(lib.kda_diag_delta_timeout(int(timeout_cycles), _stream(dev, stream)),
-               "kda_diag_delta_timeout")
+    _call("kda_diag_delta_timeout", lib.kda_diag_delta_timeout, dev, int(timeout_cycles), _stream(dev, stream))
