@@ -10,6 +10,7 @@ import os
 import platform
 import shutil
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -74,10 +75,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, debug: b
 
     with ThreadPoolExecutor(max_workers=min(8, len(sources()))) as ex:
         results = list(ex.map(compile_one, sources()))
-    if verbose:
-        for _, log in results:
-            if log:
-                print(log)
+    for _, log in results:   # all that the compiler says, or its warnings (spills among them)
+        log = log if verbose else "\n".join(line for line in log.splitlines() if "warning" in line and not line.startswith("Remark"))
+        if log:
+            print(log, file=sys.stdout if verbose else sys.stderr)
     tmp = lib_path + f".tmp{os.getpid()}"
     # -ldl: the NVTX ranges of the C ABI look up a profiler's injection library at run time
     cmd = [cc, "-shared", "-o", tmp] + [o for o, _ in results] + ARCH_FLAGS + ["-ldl"]
@@ -89,6 +90,4 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, debug: b
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))

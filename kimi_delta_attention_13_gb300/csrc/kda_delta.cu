@@ -29,7 +29,8 @@
 // memory's 128 bytes a cycle; all but the chain in four warps: 285; decays and M in one warp: 250; scores by fp32 FMA: 233;
 // q's products behind the new values, outputs a block later or before the update, the state's decay earlier, a block
 // an SM with more registers: no gain.  2048 tokens of 96 heads of 128 x 128 0.67 ms (1.58 before), of 16 heads of 256 x 256 in
-// bf16 0.45 (1.20).
+// bf16 0.45 (1.20).  Above 128 channels the chain spills: 128 accumulators a thread and the parts of products leave 324 (bf16
+// operands) to 360 bytes (fp32) of a thread's values in local memory.
 #include "kda_delta.cuh"
 #include "sm100_ptx.cuh"
 
