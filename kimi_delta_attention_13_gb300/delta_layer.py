@@ -10,7 +10,10 @@ output projection behind), with the delta rule as its mixer and queries and keys
     y        = (norm_gate(o, z)) W_o               head norm and gate, output projection
 
 The states are [N, H, d_k, d_v] fp32, as the KDA layers' own, so that `prefix_cache.CheckpointStore`
-holds them too, as they are or in fewer bits.
+holds them too, as they are or in fewer bits.  `delta_prefill` emits no checkpoints on its way: what can be stored is
+the state at a call's end, sequence i's by `store.add_checkpoints([key], state[i:i + 1], n, [n])` at its length n (or by
+`store.write`); a prompt that continues it takes `store.read`'s states as `prefill`'s `state` (`resume_prefill` is for
+the KDA layers).
 """
 from __future__ import annotations
 
