@@ -30,7 +30,7 @@
  *     (fp32, the accumulation precision, or bf16).  States and checkpoints are always fp32 and
  *     all accumulation is fp32.  Rounding outputs to bf16 costs up to 2^-9 of the largest |o|,
  *     which on the synthetic workloads is ~3.5e-2 of RMS(o): fp32 outputs are the precise form.
- *   - Every pointer passed must be 16-byte aligned (fp32 g and beta of the kda_delta calls: 4-byte).
+ *   - Every pointer passed must be 16-byte aligned (g, beta and cu_seqlens of the kda_delta calls: 4-byte).
  *   - Return value: KDA_OK (0) or a kda_status code; nothing is enqueued on error.  Checks that
  *     need device data (monotone cu_seqlens, finite inputs) are not made.  A bounded device
  *     wait that expires, or a state index out of range, sets a sticky per-device error word
@@ -419,9 +419,14 @@ int kda_linear_decode(const void *q, const void *k, const void *v, const float *
  * Head sizes: multiples of 8 from 8 to 256.
  * States, sums and decays are fp32.  bf16 inputs with head sizes up to 128 take the tcgen05 kernel
  * (but for batches of short sequences): chunks of 64 tokens, whose new values are good to fp32 (operands
- * in three bf16 parts), and with them the states; what outputs sum is rounded once to bf16 where it is a
+ * in three bf16 parts), and with them the states (a 2-norm error of some 1e-6 where 65536 tokens are remembered; it
+ * grows as the root of the chunks); what outputs sum is rounded once to bf16 where it is a
  * weighted score (each output is within 2^-8 of the sum of its terms' magnitudes, fp32 outputs too).  All else
  * is good to fp32 throughout, rounded once at the end.
+ * Which kernel a call takes goes by its mean length, total_tokens / n_seqs, empty sequences and rows of no
+ * sequence counted: the tcgen05 kernel from 32 tokens on, or 128 where d_k <= 64.  So a sequence's results vary, within
+ * these bounds, with the batch that it is in, and a long prompt that shares a call with many single tokens or
+ * empty entries takes the other kernel, which is several times slower for it: give it a call of its own.
  * The tcgen05 kernel's waits are bounded (2e9 SM cycles, about 1 s): one that gave up shows as
  * KDA_ERR_DEVICE_TIMEOUT in kda_device_status.  A NaN or infinity in an input of a sequence leaves the other
  * sequences as they are; within its own it may also reach outputs up to 63 tokens before it.
@@ -460,7 +465,8 @@ typedef enum {
  *   KDA_STATE_INT8    dst int8 of that shape, dst_scales fp32 [n_dst_slots, H, d_k]: a row's scale
  *                     s = max |x| / 127 (rounded to fp32) over its d_v values, its codes x / s rounded to
  *                     the nearest whole number (the exact quotient, ties to even).  A row with a NaN
- *                     or an infinity gets a NaN scale: it reads back as NaN throughout.
+ *                     or an infinity gets a NaN scale: it reads back as NaN throughout.  A row whose largest
+ *                     is below 1e-36 has a subnormal scale, of few bits or 0: codes stop at +-127 there.
  *   dst_idx, src_idx  device int64 [n] or NULL (identity).  An index outside its slot range skips that
  *                     pair and shows as KDA_ERR_INDEX_RANGE in kda_device_status.  Two entries of dst_idx
  *                     must not be the same.

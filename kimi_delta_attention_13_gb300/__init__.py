@@ -378,7 +378,9 @@ def delta_prefill(q, k, v, g, beta, cu_seqlens=None, init_state=None, *, scale: 
     log decays <= 0 (-inf forgets), [T, H] per token or [H] constant; beta: fp32 [T, H]; cu_seqlens: int32
     [N+1] on the device or None for one sequence; init_state: fp32 [N, H, d_k, d_v] or None (zeros).
     final_state: True to allocate, a tensor to fill (init_state itself for an in-place resume), or
-    None/False.  out_dtype defaults to out's, else q's.  Returns (out, final_state)."""
+    None/False.  out_dtype defaults to out's, else q's; fp32 outputs of bf16 operands hold scores of one bf16
+    rounding (2^-8 of their terms).  Which kernel runs goes by the mean length: give a long prompt a call of its own
+    rather than one with many single tokens or empty entries.  Returns (out, final_state)."""
     lib = _lib.load()
     head, T, H, Hk, dk, dv = _delta_inputs(q, k, v, g, beta)
     dev, dtype = q.device, q.dtype

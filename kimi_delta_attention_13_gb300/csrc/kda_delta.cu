@@ -472,6 +472,9 @@ int run_token_path(const Args &p, int dtype, int out_dtype, cudaStream_t stream)
 // and there, with initial states.  128 x 128: 32 heads, one sequence of 32 tokens 8.5, 13.9, of 64 12.1, 12.9, 16 of 16 34,
 // 54, of 32 53, 55, of 64 82, 53; 96 heads, one of 32 15, 14, 16 of 32 176, 149.  64 x 64: 16 heads, one of 64 9.1, 11.1,
 // of 128 14.2, 14.2, 16 of 64 13, 22, of 128 21, 29; 64 heads, 64 sequences of 64 167, 288, 16 of 128 80, 100).
+// The lengths themselves are on the device, so the rule does not see a long prompt among many short sequences: 4096 tokens and
+// 200 single ones, 128 x 128, 681 for 32 heads (257 and 291 in calls of their own) and 1479 for 96 (289, 844); with 200
+// empty ones in place of the tokens 593 and 1064.
 bool tc_path(int n_seqs, int64_t T, int d_k, int d_v, int dtype)
 {
     return dtype == KDA_BF16 && d_k <= 128 && d_v <= 128 && T >= (d_k <= 64 ? 128 : 32) * (int64_t)n_seqs;

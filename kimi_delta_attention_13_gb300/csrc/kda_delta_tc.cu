@@ -22,15 +22,15 @@
 // The products of one chunk: 3 x 8 for X, 6 x 4 for T R, 3 x 8 for the update, 3 x 4 for T V, 2 x 8 for S^T q, 2 x 4 for
 // the scores with U, 8 for the Gram, of [128 x 64 x 16] each at 43 cycles: some 5,000 cycles.
 //
-// Bound by that chain, and by instruction fetch: a chunk takes some 7,400 cycles alone (8 heads).  Products that a chain needs
+// Bound by that chain, and by instruction fetch: a chunk takes some 7,900 cycles alone (8 heads).  Products that a chain needs
 // (X, T R, update: 3,100) and the passes between them (R, U and S out of tensor memory, into parts and back) follow one
 // another; the rest runs beside them, in the gaps.  Left out, to time the rest: preparation 15 % less, the splits 8 %, T V,
 // Gram and S^T q 7 %, all but the bare chain 33 %.  The loops' 80 KB of code, a product being 220 bytes of it, do not stay in
 // an SM's instruction cache, and what SMs share behind it slows them down together: warps without an instruction, per one
-// issued, 0.35 with 8 SMs at work, 0.7 with 96, 3.7 with 152.  T = 8192: 8 heads of 128 x 128 0.484 ms, 96 heads 0.510 (on
-// other GPUs up to 0.56), 152 heads 0.681, 96 of 64 x 64 0.438.  The token-by-token kernel before it took 7.2 ms, the first
-// version of this one 0.86.
-// Tried: all products in loops 0.636, 0.646 and 0.659 ms for 8, 96 and 152 heads (their issue is on the chain), those beside
+// issued, 0.35 with 8 SMs at work, 0.6 with 96, 3.7 with 152.  T = 8192: 8 heads of 128 x 128 0.49-0.50 ms, 96 heads 0.56,
+// 152 heads 0.69, 96 of 64 x 64 0.48, on each of four GPUs at 2070 MHz throughout (one measured before: 0.484, 0.510, 0.681,
+// 0.438).  The token-by-token kernel before it took 7.2 ms, the first version of this one 0.86.
+// Tried (on that one): all products in loops 0.636, 0.646 and 0.659 ms for 8, 96 and 152 heads (their issue is on the chain), those beside
 // the chain in loops 0.532, 0.574, 0.689, by a warp of their own 0.503, 0.576, 0.704; waits without a first look 0.571,
 // 0.576, 0.660; before T V stood once and the joins' and R's loops were rolled 0.492, 0.528, 0.720.  Without gain: the
 // chain's loads 32 columns at a time or ahead (spills), tf32 rounding by cvt.rna (6 % slower).  T folded into k, so
