@@ -466,7 +466,7 @@ typedef enum {
  *                     s = max |x| / 127 (rounded to fp32) over its d_v values, its codes x / s rounded to
  *                     the nearest whole number (the exact quotient, ties to even).  A row with a NaN
  *                     or an infinity gets a NaN scale: it reads back as NaN throughout.  A row whose largest
- *                     is below 1e-36 has a subnormal scale, of few bits or 0: codes stop at +-127 there.
+ *                     is below 1.5e-36 has a subnormal scale, of few bits or 0: codes stop at +-127 there.
  *   dst_idx, src_idx  device int64 [n] or NULL (identity).  An index outside its slot range skips that
  *                     pair and shows as KDA_ERR_INDEX_RANGE in kda_device_status.  Two entries of dst_idx
  *                     must not be the same.
